@@ -27,7 +27,9 @@
  * Visibility: query head h uses KV head h / (Hq/Hkv) (contiguous groups).
  * Query i of s sits at position pos = kv_len(s) - q_len(s) + i; key t is
  * visible iff t < kv_len(s), and (causal == 0 or t <= pos), and
- * (window <= 0 or t > pos - window).
+ * (window <= 0 or t > pos - window). A plan may add a prefix mask
+ * (ua_plan_create_prefix), a cap on the scores and a distance bias
+ * (ua_plan_set_scores).
  *
  * fp8 e4m3 caches hold per-tensor scaled values: the key is code * k_scale,
  * the value code * v_scale ("vllm_triton_unified_attention_notes", the load
@@ -200,6 +202,33 @@ ua_status ua_plan_create_ex(ua_plan** out, const int32_t* cu_query_lens_host,
                             ua_stream_t stream);
 
 /*
+ * ua_plan_create_prefix -- a plan with a prefix mask: causal, but the first
+ * prefix_lens_host[s] keys of sequence s are visible to all of its queries
+ * (an image or instruction that attends to itself both ways). Key t is
+ * visible to the query at position pos iff t < kv_len, and (t <= pos or
+ * t < prefix_len), and (window <= 0 or t > pos - window).
+ * prefix_lens_host: [num_seqs], each >= 0; a prefix beyond kv_len reaches as
+ * far as the keys do (a prompt given in chunks), 0 is the causal mask. The
+ * plan keeps its own copy. Other arguments, work and errors as
+ * ua_plan_create_ex; UA_ERR_INVALID_ARG for a null or negative prefix too.
+ * ua_schedule_prefix -- its scheduler alone, as ua_schedule.
+ */
+ua_status ua_plan_create_prefix(ua_plan** out, const int32_t* cu_query_lens_host,
+                                const int32_t* kv_lens_host, const int32_t* prefix_lens_host,
+                                int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                int32_t head_dim, int32_t block_size, int32_t max_blocks_per_seq,
+                                int32_t kv_dtype, int32_t window, int32_t num_splits,
+                                int32_t decode_rows_max, ua_stream_t stream);
+ua_status ua_schedule_prefix(const int32_t* cu_query_lens_host, const int32_t* kv_lens_host,
+                             const int32_t* prefix_lens_host, int32_t num_seqs,
+                             int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                             int32_t block_size, int32_t max_blocks_per_seq, int32_t kv_dtype,
+                             int32_t window, int32_t num_splits, int32_t num_sms,
+                             int32_t decode_rows_max, ua_plan_info* info, ua_tile* prefill_tiles,
+                             int64_t prefill_cap, ua_tile* decode_tiles, int64_t decode_cap,
+                             ua_combine_group* groups, int64_t groups_cap);
+
+/*
  * ua_forward -- attention for the batch the plan was built for: the boxed
  * O_{t+1} = softmax(q K^T) V equation of "flashatten takeaways EP2 工程" (kv
  * cache section) over the paged cache, evaluated tile by tile as
@@ -368,6 +397,27 @@ ua_status ua_plan_set_unified_max(ua_plan* plan, int32_t enable, float phi);
  * count) instead of the scheduler's num_prefill_ctas; 0 restores it. Results
  * do not depend on it. */
 ua_status ua_plan_set_prefill_ctas(ua_plan* plan, int32_t num_ctas);
+
+/* Score shapes for later ua_forward calls on this plan. With x = scale * q.k
+ * (times k_scale for an e4m3 cache), the score of query position pos and key
+ * position t becomes
+ *   x <- softcap * tanh(x / softcap)            softcap > 0
+ *   x <- x - alibi_slopes[head] * |pos - t|     alibi_slopes given
+ * in this order, before mask and softmax. Positions are those in the cache.
+ * softcap: 0 (none), or from UA_MIN_SOFTCAP to UA_MAX_SOFTCAP (the absolute
+ *   error of a capped score is a few 2^-24 of the cap).
+ * alibi_slopes: device [num_q_heads] float (finite; on the plan's device), or
+ *   NULL (none). Not copied: the caller keeps it until the last forward that
+ *   uses it (or graph that captured one) has run.
+ * Every prefill and decode kernel applies them, together with the window, the
+ * causal or prefix mask, the unified max and fp8 products; ua_forward_oneshot,
+ * ua_forward_host and ua_forward_static_scratch, which take no plan, have
+ * plain scores. set_scores(plan, 0, NULL) restores plain scores.
+ * Returns UA_ERR_INVALID_ARG for a null plan, a softcap outside its range, or
+ * slopes that are misaligned or not device memory of the plan's device. */
+#define UA_MIN_SOFTCAP 0.0009765625f
+#define UA_MAX_SOFTCAP 4096.f
+ua_status ua_plan_set_scores(ua_plan* plan, float softcap, const float* alibi_slopes);
 
 /* fp8 tensor-core products for the prefill tiles of an fp8 (e4m3) cache:
  * the low-precision path of the "Fused Attention" notes (Q.K^T on fp8

@@ -27,6 +27,8 @@ UA_KV_FP8_E4M3 = 1
 UA_MAX_SPLITS = 128
 UA_DECODE_ROWS = 8
 UA_PREFILL_ROWS = 256
+UA_MIN_SOFTCAP = 2.0 ** -10
+UA_MAX_SOFTCAP = 4096.0
 
 # Every symbol include/ua.h declares.
 EXPORTS = (
@@ -35,6 +37,7 @@ EXPORTS = (
     "ua_gather_kv_debug", "ua_plan_set_profiling", "ua_plan_kernel_times",
     "ua_forward_static_scratch", "ua_plan_set_debug", "ua_append_kv",
     "ua_plan_set_unified_max", "ua_plan_set_prefill_ctas", "ua_plan_set_fp8_products", "ua_forward_host",
+    "ua_plan_set_scores", "ua_plan_create_prefix", "ua_schedule_prefix",
 )
 
 
@@ -87,6 +90,13 @@ _SIGS = {
                                   _F, _I32, _P]),
     "ua_forward_host": (_I32, [_P, _P, _P, _P, _P, _P, _P, _I32, _I32, _I32, _I32, _I32,
                                _I32, _I64, _I32, _F, _I32, _I32, _F, _F, _I32, _I32P, _P]),
+    "ua_plan_set_scores": (_I32, [_P, _F, _P]),
+    "ua_plan_create_prefix": (_I32, [ctypes.POINTER(_P), _I32P, _I32P, _I32P, _I32, _I32, _I32,
+                                     _I32, _I32, _I32, _I32, _I32, _I32, _I32, _P]),
+    "ua_schedule_prefix": (_I32, [_I32P, _I32P, _I32P, _I32, _I32, _I32, _I32, _I32, _I32, _I32,
+                                  _I32, _I32, _I32, _I32, ctypes.POINTER(ua_plan_info),
+                                  ctypes.POINTER(ua_tile), _I64, ctypes.POINTER(ua_tile), _I64,
+                                  ctypes.POINTER(ua_combine_group), _I64]),
     "ua_plan_get_info": (_I32, [_P, ctypes.POINTER(ua_plan_info)]),
     "ua_last_device_error": (_I32, [_P, _I32P]),
     "ua_plan_destroy": (_I32, [_P]),
@@ -130,26 +140,41 @@ def _i32_array(values):
     return (ctypes.c_int32 * max(1, len(vals)))(*vals)
 
 
+def _prefix_array(prefix_lens, num_seqs, causal):
+    """Host prefix lengths for the C ABI, which knows the prefix mask as causal."""
+    lens = list(prefix_lens)
+    if not causal:
+        raise ValueError("a prefix mask is causal: causal must be 1 with prefix_lens")
+    if len(lens) != num_seqs:
+        raise ValueError(f"prefix_lens has {len(lens)} entries for {num_seqs} sequences")
+    return _i32_array(lens)
+
+
 def ua_status_string(status: int) -> str:
     return lib().ua_status_string(int(status)).decode()
 
 
 def ua_schedule(cu_query_lens, kv_lens, num_q_heads, num_kv_heads, head_dim, block_size,
                 max_blocks_per_seq, kv_dtype=UA_KV_BF16, causal=1, window=0, num_splits=0,
-                num_sms=152, decode_rows_max=-1):
+                num_sms=152, decode_rows_max=-1, prefix_lens=None):
     """Run the CPU scheduler alone; returns (info, prefill, decode, groups) as
-    lists of dicts. Raises UAError on a rejected problem."""
+    lists of dicts. prefix_lens: a prefix mask (ua_schedule_prefix). Raises
+    UAError on a rejected problem."""
     cu, kv = _i32_array(cu_query_lens), _i32_array(kv_lens)
     n = len(list(kv_lens))
     info = ua_plan_info()
     args = (cu, kv, n, num_q_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq,
             kv_dtype, causal, window, num_splits, num_sms, decode_rows_max)
-    _check(lib().ua_schedule(*args, ctypes.byref(info), None, 0, None, 0, None, 0), "ua_schedule")
+    fn = lib().ua_schedule
+    if prefix_lens is not None:
+        args = (cu, kv, _prefix_array(prefix_lens, n, causal)) + args[2:9] + args[10:]
+        fn = lib().ua_schedule_prefix
+    _check(fn(*args, ctypes.byref(info), None, 0, None, 0, None, 0), "ua_schedule")
     pre = (ua_tile * max(1, info.num_prefill_tiles))()
     dec = (ua_tile * max(1, info.num_decode_tiles))()
     grp = (ua_combine_group * max(1, info.num_combine_groups))()
-    _check(lib().ua_schedule(*args, ctypes.byref(info), pre, info.num_prefill_tiles, dec,
-                             info.num_decode_tiles, grp, info.num_combine_groups), "ua_schedule")
+    _check(fn(*args, ctypes.byref(info), pre, info.num_prefill_tiles, dec,
+              info.num_decode_tiles, grp, info.num_combine_groups), "ua_schedule")
 
     def rows(arr, n, cls):
         return [{f: getattr(arr[i], f) for f, _ in cls._fields_} for i in range(n)]
@@ -167,11 +192,21 @@ def _stream_handle(stream) -> int:
 
 def ua_plan_create(cu_query_lens, kv_lens, num_q_heads, num_kv_heads, head_dim, block_size,
                    max_blocks_per_seq, kv_dtype=UA_KV_BF16, causal=1, window=0, num_splits=0,
-                   decode_rows_max=-1, stream=None) -> int:
-    """Create a plan from host lengths; returns the opaque plan handle."""
+                   decode_rows_max=-1, stream=None, prefix_lens=None) -> int:
+    """Create a plan from host lengths; returns the opaque plan handle.
+    prefix_lens: keys of each sequence that all its queries see (a prefix
+    mask, ua_plan_create_prefix)."""
     cu, kv = _i32_array(cu_query_lens), _i32_array(kv_lens)
     n = len(list(kv_lens))
     h = ctypes.c_void_p()
+    if prefix_lens is not None:
+        _check(lib().ua_plan_create_prefix(ctypes.byref(h), cu, kv,
+                                           _prefix_array(prefix_lens, n, causal), n, num_q_heads,
+                                           num_kv_heads, head_dim, block_size,
+                                           max_blocks_per_seq, kv_dtype, window, num_splits,
+                                           decode_rows_max, _stream_handle(stream)),
+               "ua_plan_create_prefix")
+        return h.value
     _check(lib().ua_plan_create_ex(ctypes.byref(h), cu, kv, n, num_q_heads, num_kv_heads,
                                    head_dim, block_size, max_blocks_per_seq, kv_dtype, causal,
                                    window, num_splits, decode_rows_max, _stream_handle(stream)),
@@ -291,6 +326,16 @@ def ua_plan_set_unified_max(plan: int, phi=None):
            "ua_plan_set_unified_max")
 
 
+def ua_plan_set_scores(plan: int, softcap=0.0, alibi_slopes=None):
+    """Scores capped at softcap (0: none) and lowered by alibi_slopes[head] per
+    position of distance (None: none) in later forwards on this plan. The
+    slopes (a float32 CUDA tensor) must outlive those forwards."""
+    ptr = lambda t: t if isinstance(t, int) else t.data_ptr()
+    _check(lib().ua_plan_set_scores(plan, float(softcap),
+                                    None if alibi_slopes is None else ptr(alibi_slopes)),
+           "ua_plan_set_scores")
+
+
 KERNEL_KINDS = ("prefill", "decode", "combine", "append", "stage")
 
 
@@ -323,8 +368,11 @@ def ua_forward_static_scratch(q, k_cache, v_cache, out, cu_query_lens, kv_lens, 
 class Plan:
     """RAII wrapper around a plan handle."""
 
+    _slopes = None  # the forwards read the caller's tensor: kept as long as they may
+
     def __init__(self, *args, **kwargs):
         self.handle = ua_plan_create(*args, **kwargs)
+        self.num_q_heads = int(args[2] if len(args) > 2 else kwargs["num_q_heads"])
 
     @property
     def info(self) -> ua_plan_info:
@@ -335,6 +383,16 @@ class Plan:
 
     def append_kv(self, *args, **kwargs):
         ua_append_kv(self.handle, *args, **kwargs)
+
+    def set_scores(self, softcap=0.0, alibi_slopes=None):
+        import torch
+        if alibi_slopes is not None and (
+                alibi_slopes.shape != (self.num_q_heads,) or not alibi_slopes.is_contiguous()
+                or alibi_slopes.dtype != torch.float32):
+            raise ValueError(f"alibi_slopes: a contiguous float32 tensor of {self.num_q_heads} "
+                             "slopes is needed")
+        ua_plan_set_scores(self.handle, softcap, alibi_slopes)
+        self._slopes = alibi_slopes
 
     def last_device_error(self) -> int:
         return ua_last_device_error(self.handle)

@@ -53,7 +53,7 @@ _KERNEL_SOURCES = {
     "append": ("append.cu",),
     "stage": ("stage.cu",),
 }
-_SHARED_SOURCES = ("sm100.cuh", "ua_device.cuh", "ua_kernels.h", "tma_host.cu", "planner.cpp",
+_SHARED_SOURCES = ("sm100.cuh", "score_shape.cuh", "ua_device.cuh", "ua_kernels.h", "tma_host.cu", "planner.cpp",
                    "planner.h", "ua.h")
 
 

@@ -31,6 +31,7 @@
 // leaves its normalised partial and base-2 lse in the workspace; with arrival
 // counters given, the last piece of a group to finish merges the group in the
 // same launch (otherwise the combine kernel does).
+#include "score_shape.cuh"
 #include "sm100.cuh"
 #include "ua_device.cuh"
 #include "planner.h"
@@ -207,12 +208,17 @@ struct StepMask {
   int hi_full;     // keys < hi_full are visible to every row (upper side)
   int lo_full;     // keys >= lo_full are visible to every row (lower side)
   int pos[2];      // query position of the lane's two rows
+  int last[2];     // last key the causal mask leaves them (pos, or the prefix's last key)
   int causal;
   int window;
   float phi2;      // unified max in log2 units of the scaled score; NaN: off
+  // Score shape (SHAPED instances): the cap, 0 for none, with its argument's
+  // multiplier, and the distance slopes (times log2 e) of the two rows.
+  float cap_log2, cap_arg;
+  float slope2[2];
 };
 
-template <int D, bool FP8>
+template <int D, bool FP8, bool SHAPED>
 __device__ __forceinline__ void compute_step(WarpState<D>& st, StepRegs<D, FP8>& r,
                                              const uint8_t* vp, int kv_hi,
                                              const uint32_t (&qb)[D / 16][2], const float (&cc)[2],
@@ -241,6 +247,19 @@ __device__ __forceinline__ void compute_step(WarpState<D>& st, StepRegs<D, FP8>&
   x[1] = (s[0][1] + s[1][1]) * cc[1];
   x[2] = (s[0][2] + s[1][2]) * cc[0];
   x[3] = (s[0][3] + s[1][3]) * cc[1];
+  if constexpr (SHAPED) {
+    // HBM-bound: one instance applies whatever the call asks for (uniform
+    // branches; without a bias the slopes are zero).
+    if (mk.cap_log2 > 0.f) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = cap_score(x[e] * mk.cap_arg, mk.cap_log2);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int key = base + key_of_row(g + 8 * (e >> 1));
+      x[e] = fmaf(-mk.slope2[e & 1], static_cast<float>(abs(mk.pos[e & 1] - key)), x[e]);
+    }
+  }
   // Masking (a select, so that nothing read from outside the visible set can
   // reach the result) only on steps that straddle a bound.
   if (base < mk.lo_full || base + 16 > mk.hi_full) {
@@ -249,7 +268,7 @@ __device__ __forceinline__ void compute_step(WarpState<D>& st, StepRegs<D, FP8>&
       const int key = base + key_of_row(g + 8 * (e >> 1));
       const int pos = mk.pos[e & 1];
       bool ok = key < mk.kv_hi;
-      if (mk.causal) ok = ok && key <= pos;
+      if (mk.causal) ok = ok && key <= (SHAPED ? mk.last[e & 1] : pos);
       if (mk.window > 0) ok = ok && key > pos - mk.window;
       x[e] = ok ? x[e] : -INFINITY;
     }
@@ -342,7 +361,7 @@ struct Ring {
   static_assert(kWarps * UA_DECODE_ROWS * (D + 2) * 4 <= kRing, "merge buffers alias the ring");
 };
 
-template <int D, bool FP8>
+template <int D, bool FP8, bool SHAPED>
 __global__ void __launch_bounds__(kThreads, Ring<D, FP8>::kCtasPerSm)
     decode_kernel(const __grid_constant__ CUtensorMap map_k,
                   const __grid_constant__ CUtensorMap map_v, const KernelParams p) {
@@ -464,6 +483,21 @@ __global__ void __launch_bounds__(kThreads, Ring<D, FP8>::kCtasPerSm)
     }
     mk.hi_full = p.causal ? min(kv_hi, min_pos + 1) : kv_hi;
     mk.lo_full = p.window > 0 ? max_pos - p.window + 1 : INT_MIN;
+    if constexpr (SHAPED) {
+      const int prefix = p.shape.prefix_lens ? p.shape.prefix_lens[tile.seq] : 0;
+      mk.cap_log2 = p.shape.cap_log2;
+      mk.cap_arg = p.shape.cap_arg;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int n = 2 * t + j;
+        mk.last[j] = max(mk.pos[j], prefix - 1);
+        mk.slope2[j] =
+            p.shape.slopes && n < nrows
+                ? p.shape.slopes[tile.kv_head * p.qpk + (tile.row0 + n) % p.qpk] * kLog2e
+                : 0.f;
+      }
+      if (p.causal) mk.hi_full = min(kv_hi, max(min_pos + 1, prefix));
+    }
   }
 
   WarpState<D> st_state;
@@ -528,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, Ring<D, FP8>::kCtasPerSm)
       const uint8_t* vstage = stage + 16 * RC::kRowBytes;
       read_k<D, FP8>(r, stage, step_base(done), kv_hi, g, t);
       if constexpr (!kLateV<D>) read_v<D, FP8>(r, vstage, step_base(done), kv_hi, g, t);
-      compute_step<D, FP8>(st_state, r, vstage, kv_hi, qb, cc, mk, step_base(done), g, t);
+      compute_step<D, FP8, SHAPED>(st_state, r, vstage, kv_hi, qb, cc, mk, step_base(done), g, t);
       __syncwarp();  // every lane has consumed the stage: it may be refilled
       if (issued < my_n) {
         if ((issued & 31) == 0) refill_ids(issued >> 5);
@@ -695,8 +729,8 @@ __global__ void __launch_bounds__(kThreads, Ring<D, FP8>::kCtasPerSm)
   stamp_end();
 }
 
-template <int D, bool FP8>
-cudaError_t launch_decode_d(const KernelParams& p, cudaStream_t stream, bool after_prefill) {
+template <int D, bool FP8, bool SHAPED>
+cudaError_t launch_decode_as(const KernelParams& p, cudaStream_t stream, bool after_prefill) {
   CUtensorMap mk, mv;
   const int elt = FP8 ? 1 : 2;
   using PL = PageLayout<D, FP8>;
@@ -709,10 +743,11 @@ cudaError_t launch_decode_d(const KernelParams& p, cudaStream_t stream, bool aft
                            PL::kBoxDims, 16, PL::kSwizzle);
   if (e != cudaSuccess) return e;
   static std::atomic<uint64_t> smem_set{0};
-  e = set_smem_once(decode_kernel<D, FP8>, Ring<D, FP8>::kAlloc, smem_set);
+  e = set_smem_once(decode_kernel<D, FP8, SHAPED>, Ring<D, FP8>::kAlloc, smem_set);
   if (e != cudaSuccess) return e;
   if (!after_prefill) {
-    decode_kernel<D, FP8><<<p.num_tiles, kThreads, Ring<D, FP8>::kAlloc, stream>>>(mk, mv, p);
+    decode_kernel<D, FP8, SHAPED>
+        <<<p.num_tiles, kThreads, Ring<D, FP8>::kAlloc, stream>>>(mk, mv, p);
     return cudaGetLastError();
   }
   cudaLaunchConfig_t cfg = {};
@@ -725,7 +760,13 @@ cudaError_t launch_decode_d(const KernelParams& p, cudaStream_t stream, bool aft
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_kernel<D, FP8>, mk, mv, p);
+  return cudaLaunchKernelEx(&cfg, decode_kernel<D, FP8, SHAPED>, mk, mv, p);
+}
+
+template <int D, bool FP8>
+cudaError_t launch_decode_d(const KernelParams& p, cudaStream_t stream, bool after_prefill) {
+  return shape_of(p.shape) == kShapePlain ? launch_decode_as<D, FP8, false>(p, stream, after_prefill)
+                                          : launch_decode_as<D, FP8, true>(p, stream, after_prefill);
 }
 
 }  // namespace

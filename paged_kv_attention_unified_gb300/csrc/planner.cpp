@@ -15,15 +15,17 @@ inline int64_t round_down(int64_t a, int64_t b) { return (a / b) * b; }
 
 // Key range [lo, hi) read by the packed rows [row0, row0 + nrows) of one
 // sequence. Query token i = row / qpk sits at pos = ctx + i; with a causal
-// mask it sees keys up to pos, with a window only keys above pos - window.
+// mask it sees keys up to pos and those below the sequence's prefix length,
+// with a window only keys above pos - window.
 // lo is rounded down to the 16-token step; the kernels mask what lies below
 // the true bound.
-void key_range(const Problem& p, int32_t ctx, int32_t kv_len, int32_t row0, int32_t nrows,
-               int32_t* lo, int32_t* hi) {
+void key_range(const Problem& p, int32_t seq, int32_t ctx, int32_t kv_len, int32_t row0,
+               int32_t nrows, int32_t* lo, int32_t* hi) {
   const int qpk = p.num_q_heads / p.num_kv_heads;
   const int64_t min_pos = ctx + row0 / qpk;
   const int64_t max_pos = ctx + (row0 + nrows - 1) / qpk;
-  int64_t h = p.causal ? std::min<int64_t>(kv_len, max_pos + 1) : kv_len;
+  const int64_t prefix = p.prefix_lens ? p.prefix_lens[seq] : 0;
+  int64_t h = p.causal ? std::min<int64_t>(kv_len, std::max(max_pos + 1, prefix)) : kv_len;
   int64_t l = 0;
   if (p.window > 0) l = std::max<int64_t>(0, min_pos - p.window + 1);
   l = round_down(l, kKeyStep);
@@ -97,6 +99,7 @@ ua_status validate(const Problem& p) {
   if (p.kv_dtype != UA_KV_BF16 && p.kv_dtype != UA_KV_FP8_E4M3) return UA_ERR_INVALID_ARG;
   if (p.num_splits < 0 || p.num_splits > UA_MAX_SPLITS) return UA_ERR_INVALID_ARG;
   if (p.causal != 0 && p.causal != 1) return UA_ERR_INVALID_ARG;
+  if (p.prefix_lens && p.causal == 0) return UA_ERR_INVALID_ARG;  // every key is visible already
   if (p.num_seqs > 0 && (p.cu_query_lens == nullptr || p.kv_lens == nullptr))
     return UA_ERR_INVALID_ARG;
   if (p.head_dim < 32 || p.head_dim > 256 || p.head_dim % 32 != 0) return UA_ERR_UNSUPPORTED;
@@ -108,6 +111,7 @@ ua_status validate(const Problem& p) {
     const int64_t q0 = p.cu_query_lens[s], q1 = p.cu_query_lens[s + 1];
     const int64_t ql = q1 - q0, kv = p.kv_lens[s];
     if (ql < 0 || kv < 0 || kv < ql) return UA_ERR_INVALID_ARG;
+    if (p.prefix_lens && p.prefix_lens[s] < 0) return UA_ERR_INVALID_ARG;
     if (ceil_div(kv, p.block_size) > p.max_blocks_per_seq) return UA_ERR_INVALID_ARG;
     if (ql * qpk > INT32_MAX) return UA_ERR_INVALID_ARG;
   }
@@ -167,7 +171,7 @@ ua_status build_schedule(const Problem& p, Schedule* out) {
         b.seq = q;
         b.row0 = static_cast<int32_t>(r0);
         b.nrows = static_cast<int32_t>(std::min<int64_t>(UA_DECODE_ROWS, rows - r0));
-        key_range(p, ctx, kv, b.row0, b.nrows, &b.kv_lo, &b.kv_hi);
+        key_range(p, q, ctx, kv, b.row0, b.nrows, &b.kv_lo, &b.kv_hi);
         blocks.push_back(b);
       }
       span_end.push_back(static_cast<int32_t>(blocks.size()));
@@ -180,7 +184,7 @@ ua_status build_schedule(const Problem& p, Schedule* out) {
       t.kv_head = 0;
       t.row0 = static_cast<int32_t>(r0);
       t.nrows = static_cast<int32_t>(std::min<int64_t>(UA_PREFILL_ROWS, rows - r0));
-      key_range(p, ctx, kv, t.row0, t.nrows, &t.kv_lo, &t.kv_hi);
+      key_range(p, q, ctx, kv, t.row0, t.nrows, &t.kv_lo, &t.kv_hi);
       t.kv_lo = static_cast<int32_t>(round_down(t.kv_lo, kPrefillKeyTile));
       t.slot = -1;
       t.group = -1;
@@ -479,7 +483,7 @@ ua_status build_schedule(const Problem& p, Schedule* out) {
       for (int32_t r0 = t.row0; r0 < t.row0 + t.nrows; r0 += kPrefillQueryTile) {
         int32_t lo = 0, hi = 0;
         const int32_t rows = std::min(kPrefillQueryTile, t.row0 + t.nrows - r0);
-        key_range(p, p.kv_lens[t.seq] - ql, p.kv_lens[t.seq], r0, rows, &lo, &hi);
+        key_range(p, t.seq, p.kv_lens[t.seq] - ql, p.kv_lens[t.seq], r0, rows, &lo, &hi);
         cost[i] += ceil_div(std::max<int64_t>(0, hi - t.kv_lo), kPrefillKeyTile);
       }
       total_cost += cost[i];

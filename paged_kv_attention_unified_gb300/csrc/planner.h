@@ -18,6 +18,7 @@ namespace ua {
 struct Problem {
   const int32_t* cu_query_lens = nullptr;  // host [num_seqs + 1]
   const int32_t* kv_lens = nullptr;        // host [num_seqs]
+  const int32_t* prefix_lens = nullptr;    // host [num_seqs] or null: keys below it are seen by every query
   int32_t num_seqs = 0;
   int32_t num_q_heads = 0;
   int32_t num_kv_heads = 0;

@@ -34,6 +34,7 @@
 // MMAs in flight and frees the tensor memory before the CTA exits.
 #include <cuda.h>
 
+#include "score_shape.cuh"
 #include "sm100.cuh"
 #include "ua_device.cuh"
 #include "ua_kernels.h"
@@ -134,6 +135,7 @@ struct Bars {
 // Geometry of one work tile, computed the same way by every role.
 struct Geometry {
   int q_start, ctx, nrows, kv_lo, kv_hi;
+  int prefix;                // keys below it are visible to every row (0: none)
   int rows[kTilesPerCta];    // valid rows of each query tile
   int ntiles[kTilesPerCta];  // key tiles each query tile needs
   int nmax;                  // key tiles loaded
@@ -158,6 +160,7 @@ __device__ __forceinline__ Geometry geometry_of(const PrefillParams& p, const ua
   g.nrows = min(tile.nrows, qlen * p.qpk - tile.row0);
   g.kv_hi = min(min(tile.kv_hi, kv_len), p.max_blocks_per_seq * p.block_size);
   g.kv_lo = tile.kv_lo;
+  g.prefix = p.shape.prefix_lens ? p.shape.prefix_lens[tile.seq] : 0;
   g.nmax = 0;
 #pragma unroll
   for (int t = 0; t < kTilesPerCta; ++t) {
@@ -165,7 +168,8 @@ __device__ __forceinline__ Geometry geometry_of(const PrefillParams& p, const ua
     g.ntiles[t] = 0;
     if (g.rows[t] > 0) {
       const int last = tile.row0 + t * kRows + g.rows[t] - 1;
-      const int hi = p.causal ? min(g.kv_hi, g.ctx + last / p.qpk + 1) : g.kv_hi;
+      const int hi =
+          p.causal ? min(g.kv_hi, max(g.ctx + last / p.qpk + 1, g.prefix)) : g.kv_hi;
       g.ntiles[t] = hi > g.kv_lo ? (hi - g.kv_lo + kKeys - 1) / kKeys : 0;
     }
     g.nmax = max(g.nmax, g.ntiles[t]);
@@ -499,7 +503,7 @@ __device__ __forceinline__ void mma_role(const PrefillParams& p, const uint8_t* 
 // What the softmax of one query tile needs of a work tile, as scalars (a
 // runtime index into the descriptor would put it in local memory).
 struct SoftmaxTile {
-  int kv_head, row0, q_start, ctx, kv_lo, kv_hi, nmax;
+  int kv_head, row0, q_start, ctx, kv_lo, kv_hi, prefix, nmax;
   int n_t;     // key tiles of this query tile
   int rows_t;  // valid rows of this query tile
 };
@@ -508,7 +512,7 @@ struct SoftmaxTile {
 // only touch TMEM lanes 32 * (warp % 4) .. + 31, which fixes the rows of each
 // warp. `done` is the number of key tiles this query tile has already had in
 // earlier work tiles (barrier phases), `step` the ring position of key tile 0.
-template <int D, bool F8>
+template <int D, bool F8, int SHAPE>
 __device__ __forceinline__ bool softmax_tile(const PrefillParams& p, const SoftmaxTile& g, int t,
                                              int done, int step, uint8_t* sQ, uint8_t* sV,
                                              uint32_t tmem,
@@ -528,7 +532,9 @@ __device__ __forceinline__ bool softmax_tile(const PrefillParams& p, const Softm
   const int pos = g.ctx + row / p.qpk;
   // Scores are used as x = s * c with c >= 0: a negative scale flips the sign
   // of the raw scores once, so that the row max is always a max.
-  const bool neg = p.score_scale_log2 < 0.f;
+  // Shaped scores are final base-2 values (their multiplier is 1 from there on).
+  constexpr bool kShaped = (SHAPE & (kShapeCap | kShapeBias)) != 0;
+  const bool neg = !kShaped && p.score_scale_log2 < 0.f;
   float c = neg ? -p.score_scale_log2 : p.score_scale_log2;
   if constexpr (F8) {
     // This thread's Q row to e4m3 with its own scale (inv = 448 / max |q|,
@@ -577,6 +583,10 @@ __device__ __forceinline__ bool softmax_tile(const PrefillParams& p, const Softm
     mbar_arrive(bar.q_full(t));
     c = __fdiv_rn(c, inv);
   }
+  const int last_key = SHAPE != kShapePlain ? max(pos, g.prefix - 1) : pos;  // causal bound
+  float slope2 = 0.f;
+  if constexpr ((SHAPE & kShapeBias) != 0)
+    slope2 = p.shape.slopes[g.kv_head * p.qpk + row % p.qpk] * kLog2e;
   float m = -INFINITY, l = 0.f;
   for (int j = 0; j < n_t; ++j) {
     if (!__all_sync(0xffffffffu, mbar_wait(bar.s_full(t), (done + j) & 1, abort, p.timeout_ns)))
@@ -599,9 +609,12 @@ __device__ __forceinline__ bool softmax_tile(const PrefillParams& p, const Softm
 #pragma unroll
       for (int i = 0; i < kKeys; ++i) x[i] = -x[i];
     }
+    if constexpr (kShaped)
+      shape_row<kKeys, SHAPE>(x, c, c * p.shape.cap_arg, p.shape.cap_log2, slope2, base - pos);
+    const float mult = kShaped ? 1.f : c;
     // Mask by select: keys past the range, past the row's position (causal)
     // or at or below pos - window.
-    const int hi_col = min(g.kv_hi, p.causal ? pos + 1 : g.kv_hi) - base;
+    const int hi_col = min(g.kv_hi, p.causal ? last_key + 1 : g.kv_hi) - base;
     const int lo_col = p.window > 0 ? pos - p.window + 1 - base : INT_MIN;
     if (hi_col < kKeys || lo_col > 0) {
 #pragma unroll
@@ -618,13 +631,13 @@ __device__ __forceinline__ bool softmax_tile(const PrefillParams& p, const Softm
       mxp[(i / 2) % kAcc] = fmax3(mxp[(i / 2) % kAcc], x[i], x[i + 1]);
     const float mx_raw = fmax3(fmax3(mxp[0], mxp[1], mxp[2]), fmax3(mxp[3], mxp[4], mxp[5]),
                                fmaxf(mxp[6], mxp[7]));
-    const float m_new = fmaxf(m, mx_raw * c);
+    const float m_new = fmaxf(m, mx_raw * mult);
     const bool grow = (m == -INFINITY) || (m_new > m + kRescaleThreshold);
     const float m_use = grow ? m_new : m;
     const float alpha = grow ? ((m == -INFINITY) ? 0.f : ex2(m - m_use)) : 1.f;
     const float sub = (m_use == -INFINITY) ? 0.f : m_use;
     // p = 2^(x * c - m): one paired fma per two keys, then ex2; paired sums.
-    const uint64_t c2 = f2_pack(c, c), nsub2 = f2_pack(-sub, -sub);
+    const uint64_t c2 = f2_pack(mult, mult), nsub2 = f2_pack(-sub, -sub);
     uint64_t sum2[kAcc / 2];
 #pragma unroll
     for (int a = 0; a < kAcc / 2; ++a) sum2[a] = f2_pack(0.f, 0.f);
@@ -736,7 +749,7 @@ __device__ __forceinline__ bool softmax_tile(const PrefillParams& p, const Softm
 }
 
 // Softmax warpgroup of query tile t over the CTA's work tiles.
-template <int D, bool F8>
+template <int D, bool F8, int SHAPE>
 __device__ __forceinline__ void softmax_role(const PrefillParams& p, const uint8_t* ring, int t,
                                              uint8_t* sQ, uint8_t* sV, uint32_t tmem,
                                              const Bars<D, F8>& bar,
@@ -758,11 +771,12 @@ __device__ __forceinline__ void softmax_role(const PrefillParams& p, const uint8
     st.ctx = it.g.ctx;
     st.kv_lo = it.g.kv_lo;
     st.kv_hi = it.g.kv_hi;
+    st.prefix = it.g.prefix;
     st.nmax = it.g.nmax;
     st.n_t = t ? it.g.ntiles[1] : it.g.ntiles[0];
     st.rows_t = t ? it.g.rows[1] : it.g.rows[0];
     if (st.n_t > 0) {
-      if (!softmax_tile<D, F8>(p, st, t, done, step, sQ, sV, tmem, bar, abort, warp, lane)) {
+      if (!softmax_tile<D, F8, SHAPE>(p, st, t, done, step, sQ, sV, tmem, bar, abort, warp, lane)) {
         give_up(p, abort);
         return;
       }
@@ -772,7 +786,7 @@ __device__ __forceinline__ void softmax_role(const PrefillParams& p, const uint8
   }
 }
 
-template <int D, bool F8>
+template <int D, bool F8, int SHAPE>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap map_q,
                    const __grid_constant__ CUtensorMap map_k,
@@ -847,7 +861,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-    softmax_role<D, F8>(p, ring, (warp - 4) / 4, sQ, sV, tmem, bar, abort, warp, lane);
+    softmax_role<D, F8, SHAPE>(p, ring, (warp - 4) / 4, sQ, sV, tmem, bar, abort, warp, lane);
   }
   tc_fence_before();
   __syncthreads();
@@ -858,24 +872,38 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0 && p.span_end != nullptr) atomicMax(p.span_end, globaltimer_ns());
 }
 
-template <int D, bool F8>
-cudaError_t launch_d(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
+template <int D, bool F8, int SHAPE>
+cudaError_t launch_as(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
                      const PrefillParams& p, cudaStream_t stream) {
   // The register split above assumes the launch budget; refuse to launch a
   // build whose register count differs (the increase could never be granted).
   static int checked = 0;
   if (!checked) {
     cudaFuncAttributes attr;
-    cudaError_t e = cudaFuncGetAttributes(&attr, prefill_kernel<D, F8>);
+    cudaError_t e = cudaFuncGetAttributes(&attr, prefill_kernel<D, F8, SHAPE>);
     if (e != cudaSuccess) return e;
     if (attr.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
     checked = 1;
   }
   static std::atomic<uint64_t> smem_set{0};
-  cudaError_t e = set_smem_once(prefill_kernel<D, F8>, Smem<D, F8>::kAlloc, smem_set);
+  cudaError_t e = set_smem_once(prefill_kernel<D, F8, SHAPE>, Smem<D, F8>::kAlloc, smem_set);
   if (e != cudaSuccess) return e;
-  prefill_kernel<D, F8><<<p.num_ctas, kThreads, Smem<D, F8>::kAlloc, stream>>>(mq, mk, mv, p);
+  prefill_kernel<D, F8, SHAPE>
+      <<<p.num_ctas, kThreads, Smem<D, F8>::kAlloc, stream>>>(mq, mk, mv, p);
   return cudaGetLastError();
+}
+
+template <int D, bool F8>
+cudaError_t launch_d(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
+                     const PrefillParams& p, cudaStream_t stream) {
+  constexpr int P = kShapePrefix, C = kShapeCap, B = kShapeBias;
+  switch (shape_of(p.shape)) {
+    case kShapePlain: return launch_as<D, F8, kShapePlain>(mq, mk, mv, p, stream);
+    case P: return launch_as<D, F8, P>(mq, mk, mv, p, stream);
+    case P | C: return launch_as<D, F8, P | C>(mq, mk, mv, p, stream);
+    case P | B: return launch_as<D, F8, P | B>(mq, mk, mv, p, stream);
+    default: return launch_as<D, F8, P | C | B>(mq, mk, mv, p, stream);
+  }
 }
 
 }  // namespace

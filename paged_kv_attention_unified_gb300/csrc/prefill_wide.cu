@@ -26,6 +26,7 @@
 // MMAs in flight and frees the tensor memory before the CTA exits.
 #include <cuda.h>
 
+#include "score_shape.cuh"
 #include "sm100.cuh"
 #include "ua_device.cuh"
 #include "ua_kernels.h"
@@ -102,6 +103,7 @@ struct Item {
   int q_start, ctx, kv_lo, kv_hi;
   int ntiles;                    // key tiles of 64 from kv_lo
   int end;                       // 1: no more items for this CTA
+  int prefix;                    // keys below it are visible to every row (0: none)
 };
 static_assert(sizeof(Item) <= kItemBytes, "item descriptor too large");
 
@@ -160,7 +162,9 @@ __device__ __forceinline__ void scheduler_role(const PrefillParams& p, const Bar
       it.kv_lo = tile.kv_lo;
       it.kv_hi = kv_hi;
       const int last = it.row0 + it.rows - 1;
-      const int hi = p.causal ? min(kv_hi, it.ctx + last / p.qpk + 1) : kv_hi;
+      it.prefix = p.shape.prefix_lens ? p.shape.prefix_lens[tile.seq] : 0;
+      const int hi =
+          p.causal ? min(kv_hi, max(it.ctx + last / p.qpk + 1, it.prefix)) : kv_hi;
       it.ntiles = hi > it.kv_lo ? (hi - it.kv_lo + kKeys - 1) / kKeys : 0;
       if (it.ntiles > 0) ok = publish(it);
     }
@@ -378,7 +382,7 @@ __device__ __forceinline__ void mma_role(const PrefillParams& p, const uint8_t* 
 // Warps 4-7, one thread per row r (TMEM lane r; warp w may only touch lanes
 // 32 (w % 4) .. + 31). g0: key tiles of earlier items (barrier phases and S
 // buffers).
-template <int D>
+template <int D, int SHAPE>
 __device__ __forceinline__ bool softmax_item(const PrefillParams& p, const Item& it, int g0,
                                              uint8_t* sV, uint32_t tmem, const Bars& bar,
                                              volatile int32_t* abort, int warp, int lane) {
@@ -392,8 +396,14 @@ __device__ __forceinline__ bool softmax_item(const PrefillParams& p, const Item&
   const int pos = it.ctx + row / p.qpk;
   // Scores are used as x = s * c with c >= 0: a negative scale flips the sign
   // of the raw scores once, so that the row max is always a max.
-  const bool neg = p.score_scale_log2 < 0.f;
+  // Shaped scores are final base-2 values (their multiplier is 1 from there on).
+  constexpr bool kShaped = (SHAPE & (kShapeCap | kShapeBias)) != 0;
+  const bool neg = !kShaped && p.score_scale_log2 < 0.f;
   const float c = neg ? -p.score_scale_log2 : p.score_scale_log2;
+  const int last_key = SHAPE != kShapePlain ? max(pos, it.prefix - 1) : pos;  // causal bound
+  float slope2 = 0.f;
+  if constexpr ((SHAPE & kShapeBias) != 0)
+    slope2 = p.shape.slopes[it.kv_head * p.qpk + row % p.qpk] * kLog2e;
   float m = -INFINITY, l = 0.f;
   const int n = it.ntiles;
   for (int j = 0; j < n; ++j) {
@@ -418,9 +428,12 @@ __device__ __forceinline__ bool softmax_item(const PrefillParams& p, const Item&
 #pragma unroll
       for (int i = 0; i < kKeys; ++i) x[i] = -x[i];
     }
+    if constexpr (kShaped)
+      shape_row<kKeys, SHAPE>(x, c, c * p.shape.cap_arg, p.shape.cap_log2, slope2, base - pos);
+    const float mult = kShaped ? 1.f : c;
     // Mask by select: keys past the range, past the row's position (causal)
     // or at or below pos - window.
-    const int hi_col = min(it.kv_hi, p.causal ? pos + 1 : it.kv_hi) - base;
+    const int hi_col = min(it.kv_hi, p.causal ? last_key + 1 : it.kv_hi) - base;
     const int lo_col = p.window > 0 ? pos - p.window + 1 - base : INT_MIN;
     if (hi_col < kKeys || lo_col > 0) {
 #pragma unroll
@@ -439,12 +452,12 @@ __device__ __forceinline__ bool softmax_item(const PrefillParams& p, const Item&
     // The reference max moves only when the row max grew by more than 2^8:
     // P and l use the same stale reference, so the result is exact up to
     // rounding and O is rescaled only on those steps.
-    const float m_new = fmaxf(m, mx_raw * c);
+    const float m_new = fmaxf(m, mx_raw * mult);
     const bool grow = (m == -INFINITY) || (m_new > m + kRescaleThreshold);
     const float m_use = grow ? m_new : m;
     const float alpha = grow ? ((m == -INFINITY) ? 0.f : ex2(m - m_use)) : 1.f;
     const float sub = (m_use == -INFINITY) ? 0.f : m_use;
-    const uint64_t c2 = f2_pack(c, c), nsub2 = f2_pack(-sub, -sub);
+    const uint64_t c2 = f2_pack(mult, mult), nsub2 = f2_pack(-sub, -sub);
     uint64_t sum2[kAcc / 2];
 #pragma unroll
     for (int a = 0; a < kAcc / 2; ++a) sum2[a] = f2_pack(0.f, 0.f);
@@ -535,7 +548,7 @@ __device__ __forceinline__ bool softmax_item(const PrefillParams& p, const Item&
   return true;
 }
 
-template <int D>
+template <int D, int SHAPE>
 __device__ __forceinline__ void softmax_role(const PrefillParams& p, const uint8_t* slot,
                                              uint8_t* sV, uint32_t tmem, const Bars& bar,
                                              volatile int32_t* abort, int warp, int lane) {
@@ -549,7 +562,7 @@ __device__ __forceinline__ void softmax_role(const PrefillParams& p, const uint8
     __syncwarp();
     if (lane == 0) mbar_arrive(bar.item_empty());
     if (it.end) break;
-    if (!softmax_item<D>(p, it, g0, sV, tmem, bar, abort, warp, lane)) {
+    if (!softmax_item<D, SHAPE>(p, it, g0, sV, tmem, bar, abort, warp, lane)) {
       give_up(p, abort);
       return;
     }
@@ -557,7 +570,7 @@ __device__ __forceinline__ void softmax_role(const PrefillParams& p, const uint8
   }
 }
 
-template <int D>
+template <int D, int SHAPE>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_wide_kernel(const __grid_constant__ CUtensorMap map_q,
                         const __grid_constant__ CUtensorMap map_k,
@@ -621,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 3) {
     if (lane == 0) scheduler_role(p, bar, slot, abort);
   } else {
-    softmax_role<D>(p, slot, sV, tmem, bar, abort, warp, lane);
+    softmax_role<D, SHAPE>(p, slot, sV, tmem, bar, abort, warp, lane);
   }
   tc_fence_before();
   __syncthreads();
@@ -632,8 +645,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0 && p.span_end != nullptr) atomicMax(p.span_end, globaltimer_ns());
 }
 
-template <int D>
-cudaError_t launch(const PrefillParams& p, const void* q, const void* k_cache,
+template <int D, int SHAPE>
+cudaError_t launch_as(const PrefillParams& p, const void* q, const void* k_cache,
                    const void* v_cache, int64_t total_q, int num_kv_heads, cudaStream_t stream) {
   CUtensorMap mq, mk, mv;
   {
@@ -654,10 +667,23 @@ cudaError_t launch(const PrefillParams& p, const void* q, const void* k_cache,
                            p.rows_per_box, true);
   if (e != cudaSuccess) return e;
   static std::atomic<uint64_t> smem_set{0};
-  e = set_smem_once(prefill_wide_kernel<D>, Geo<D>::kAlloc, smem_set);
+  e = set_smem_once(prefill_wide_kernel<D, SHAPE>, Geo<D>::kAlloc, smem_set);
   if (e != cudaSuccess) return e;
-  prefill_wide_kernel<D><<<p.num_ctas, kThreads, Geo<D>::kAlloc, stream>>>(mq, mk, mv, p);
+  prefill_wide_kernel<D, SHAPE><<<p.num_ctas, kThreads, Geo<D>::kAlloc, stream>>>(mq, mk, mv, p);
   return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch(const PrefillParams& p, const void* q, const void* k, const void* v,
+                   int64_t total_q, int num_kv_heads, cudaStream_t stream) {
+  constexpr int P = kShapePrefix, C = kShapeCap, B = kShapeBias;
+  switch (shape_of(p.shape)) {
+    case kShapePlain: return launch_as<D, kShapePlain>(p, q, k, v, total_q, num_kv_heads, stream);
+    case P: return launch_as<D, P>(p, q, k, v, total_q, num_kv_heads, stream);
+    case P | C: return launch_as<D, P | C>(p, q, k, v, total_q, num_kv_heads, stream);
+    case P | B: return launch_as<D, P | B>(p, q, k, v, total_q, num_kv_heads, stream);
+    default: return launch_as<D, P | C | B>(p, q, k, v, total_q, num_kv_heads, stream);
+  }
 }
 
 

@@ -43,6 +43,9 @@ struct ua_plan {
   uint64_t wait_timeout_ns = 2000000000ull;
   int32_t prefill_ctas_override = 0;  // ua_plan_set_prefill_ctas (0: the scheduler's count)
   bool fp8_products = false;          // ua_plan_set_fp8_products
+  float softcap = 0.f;                // ua_plan_set_scores
+  const float* alibi_slopes = nullptr;
+  int32_t* d_prefix = nullptr;        // ua_plan_create_prefix: device prefix lengths (in d_meta)
   // kernel timing (ua_plan_set_profiling)
   struct EventPair {
     cudaEvent_t start = nullptr, stop = nullptr;
@@ -165,10 +168,11 @@ void free_plan_memory(ua_plan* p) {
 ua::Problem make_problem(const int32_t* cu, const int32_t* kv, int32_t num_seqs, int32_t hq,
                          int32_t hkv, int32_t d, int32_t bs, int32_t max_blocks, int32_t dtype,
                          int32_t causal, int32_t window, int32_t num_splits, int32_t num_sms,
-                         int32_t decode_rows_max) {
+                         int32_t decode_rows_max, const int32_t* prefix = nullptr) {
   ua::Problem p;
   p.cu_query_lens = cu;
   p.kv_lens = kv;
+  p.prefix_lens = prefix;
   p.num_seqs = num_seqs;
   p.num_q_heads = hq;
   p.num_kv_heads = hkv;
@@ -232,6 +236,10 @@ ua::KernelParams base_params(const ua_plan* plan, const void* q, const void* k, 
   kp.timeout_ns = plan->wait_timeout_ns;
   kp.unified_max_on = plan->unified_max_on ? 1 : 0;
   kp.unified_max_log2 = plan->unified_max * ua::kLog2e;
+  kp.shape.cap_log2 = plan->softcap * ua::kLog2e;
+  kp.shape.cap_arg = plan->softcap > 0.f ? 2.f / plan->softcap : 0.f;
+  kp.shape.slopes = plan->alibi_slopes;
+  kp.shape.prefix_lens = plan->d_prefix;
   return kp;
 }
 
@@ -276,6 +284,44 @@ cudaError_t span_reset(ua_plan* p, int slots, cudaStream_t cs) {
   return e;
 }
 
+// The scheduler behind ua_schedule and ua_schedule_prefix.
+ua_status schedule(const int32_t* cu_query_lens_host, const int32_t* kv_lens_host,
+                   const int32_t* prefix_lens_host, int32_t num_seqs, int32_t num_q_heads,
+                   int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                   int32_t max_blocks_per_seq, int32_t kv_dtype, int32_t causal, int32_t window,
+                   int32_t num_splits, int32_t num_sms, int32_t decode_rows_max,
+                   ua_plan_info* info, ua_tile* prefill_tiles, int64_t prefill_cap,
+                   ua_tile* decode_tiles, int64_t decode_cap, ua_combine_group* groups,
+                   int64_t groups_cap) {
+  if (info == nullptr) return UA_ERR_INVALID_ARG;
+  const int sms = num_sms > 0 ? num_sms : 152;
+  ua::Problem pr = make_problem(cu_query_lens_host, kv_lens_host, num_seqs, num_q_heads,
+                                num_kv_heads, head_dim, block_size, max_blocks_per_seq, kv_dtype,
+                                causal, window, num_splits, sms, decode_rows_max,
+                                prefix_lens_host);
+  ua::Schedule s;
+  try {
+    ua_status st = ua::build_schedule(pr, &s);
+    if (st != UA_OK) return st;
+  } catch (const std::bad_alloc&) {
+    return UA_ERR_INVALID_ARG;
+  }
+  fill_info(s, head_dim, sms, info);
+  if (prefill_tiles) {
+    if (prefill_cap < static_cast<int64_t>(s.prefill.size())) return UA_ERR_INVALID_ARG;
+    std::memcpy(prefill_tiles, s.prefill.data(), s.prefill.size() * sizeof(ua_tile));
+  }
+  if (decode_tiles) {
+    if (decode_cap < static_cast<int64_t>(s.decode.size())) return UA_ERR_INVALID_ARG;
+    std::memcpy(decode_tiles, s.decode.data(), s.decode.size() * sizeof(ua_tile));
+  }
+  if (groups) {
+    if (groups_cap < static_cast<int64_t>(s.groups.size())) return UA_ERR_INVALID_ARG;
+    std::memcpy(groups, s.groups.data(), s.groups.size() * sizeof(ua_combine_group));
+  }
+  return UA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -300,32 +346,25 @@ ua_status ua_schedule(const int32_t* cu_query_lens_host, const int32_t* kv_lens_
                       int32_t num_sms, int32_t decode_rows_max, ua_plan_info* info,
                       ua_tile* prefill_tiles, int64_t prefill_cap, ua_tile* decode_tiles,
                       int64_t decode_cap, ua_combine_group* groups, int64_t groups_cap) {
-  if (info == nullptr) return UA_ERR_INVALID_ARG;
-  const int sms = num_sms > 0 ? num_sms : 152;
-  ua::Problem pr = make_problem(cu_query_lens_host, kv_lens_host, num_seqs, num_q_heads,
-                                num_kv_heads, head_dim, block_size, max_blocks_per_seq, kv_dtype,
-                                causal, window, num_splits, sms, decode_rows_max);
-  ua::Schedule s;
-  try {
-    ua_status st = ua::build_schedule(pr, &s);
-    if (st != UA_OK) return st;
-  } catch (const std::bad_alloc&) {
-    return UA_ERR_INVALID_ARG;
-  }
-  fill_info(s, head_dim, sms, info);
-  if (prefill_tiles) {
-    if (prefill_cap < static_cast<int64_t>(s.prefill.size())) return UA_ERR_INVALID_ARG;
-    std::memcpy(prefill_tiles, s.prefill.data(), s.prefill.size() * sizeof(ua_tile));
-  }
-  if (decode_tiles) {
-    if (decode_cap < static_cast<int64_t>(s.decode.size())) return UA_ERR_INVALID_ARG;
-    std::memcpy(decode_tiles, s.decode.data(), s.decode.size() * sizeof(ua_tile));
-  }
-  if (groups) {
-    if (groups_cap < static_cast<int64_t>(s.groups.size())) return UA_ERR_INVALID_ARG;
-    std::memcpy(groups, s.groups.data(), s.groups.size() * sizeof(ua_combine_group));
-  }
-  return UA_OK;
+  return schedule(cu_query_lens_host, kv_lens_host, nullptr, num_seqs, num_q_heads, num_kv_heads,
+                  head_dim, block_size, max_blocks_per_seq, kv_dtype, causal, window, num_splits,
+                  num_sms, decode_rows_max, info, prefill_tiles, prefill_cap, decode_tiles,
+                  decode_cap, groups, groups_cap);
+}
+
+ua_status ua_schedule_prefix(const int32_t* cu_query_lens_host, const int32_t* kv_lens_host,
+                             const int32_t* prefix_lens_host, int32_t num_seqs,
+                             int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                             int32_t block_size, int32_t max_blocks_per_seq, int32_t kv_dtype,
+                             int32_t window, int32_t num_splits, int32_t num_sms,
+                             int32_t decode_rows_max, ua_plan_info* info, ua_tile* prefill_tiles,
+                             int64_t prefill_cap, ua_tile* decode_tiles, int64_t decode_cap,
+                             ua_combine_group* groups, int64_t groups_cap) {
+  if (num_seqs > 0 && prefix_lens_host == nullptr) return UA_ERR_INVALID_ARG;
+  return schedule(cu_query_lens_host, kv_lens_host, prefix_lens_host, num_seqs, num_q_heads,
+                  num_kv_heads, head_dim, block_size, max_blocks_per_seq, kv_dtype, 1, window,
+                  num_splits, num_sms, decode_rows_max, info, prefill_tiles, prefill_cap,
+                  decode_tiles, decode_cap, groups, groups_cap);
 }
 
 }  // extern "C"
@@ -346,7 +385,7 @@ ua_status create_plan(ua_plan** out, const int32_t* cu_query_lens_host,
                       int32_t max_blocks_per_seq, int32_t kv_dtype, int32_t causal,
                       int32_t window, int32_t num_splits, int32_t decode_rows_max,
                       ua_stream_t stream, const HostRange* extra, int n_extra,
-                      void** extra_dev) {
+                      void** extra_dev, const int32_t* prefix_lens_host = nullptr) {
   if (out == nullptr) return UA_ERR_INVALID_ARG;
   *out = nullptr;
   int dev = 0, sms = 0;
@@ -358,7 +397,7 @@ ua_status create_plan(ua_plan** out, const int32_t* cu_query_lens_host,
   plan->device = dev;
   plan->prob = make_problem(cu_query_lens_host, kv_lens_host, num_seqs, num_q_heads,
                             num_kv_heads, head_dim, block_size, max_blocks_per_seq, kv_dtype,
-                            causal, window, num_splits, sms, decode_rows_max);
+                            causal, window, num_splits, sms, decode_rows_max, prefix_lens_host);
   ua_status st;
   try {
     st = ua::build_schedule(plan->prob, &plan->sched);
@@ -373,6 +412,7 @@ ua_status create_plan(ua_plan** out, const int32_t* cu_query_lens_host,
   // The plan keeps no pointer to the caller's host arrays.
   plan->prob.cu_query_lens = nullptr;
   plan->prob.kv_lens = nullptr;
+  plan->prob.prefix_lens = nullptr;
   fill_info(plan->sched, head_dim, sms, &plan->info);
 
   const ua::Schedule& s = plan->sched;
@@ -385,7 +425,9 @@ ua_status create_plan(ua_plan** out, const int32_t* cu_query_lens_host,
   const size_t n_stage = s.stage.size(), n_st = s.staged_table.size();
   const size_t off_stage = off_app + n_app * sizeof(ua_tile);
   const size_t off_st = off_stage + n_stage * sizeof(ua_tile);
-  size_t bytes_meta = off_st + n_st * sizeof(int32_t);
+  const size_t off_prefix = off_st + n_st * sizeof(int32_t);
+  const size_t n_prefix = prefix_lens_host && num_seqs > 0 ? static_cast<size_t>(num_seqs) : 0;
+  size_t bytes_meta = off_prefix + n_prefix * sizeof(int32_t);
   std::vector<size_t> off_extra(static_cast<size_t>(n_extra > 0 ? n_extra : 0));
   for (int i = 0; i < n_extra; ++i) {
     bytes_meta = (bytes_meta + 15) & ~static_cast<size_t>(15);
@@ -409,6 +451,7 @@ ua_status create_plan(ua_plan** out, const int32_t* cu_query_lens_host,
   if (n_app) std::memcpy(host + off_app, s.append.data(), n_app * sizeof(ua_tile));
   if (n_stage) std::memcpy(host + off_stage, s.stage.data(), n_stage * sizeof(ua_tile));
   if (n_st) std::memcpy(host + off_st, s.staged_table.data(), n_st * sizeof(int32_t));
+  if (n_prefix) std::memcpy(host + off_prefix, prefix_lens_host, n_prefix * sizeof(int32_t));
   for (int i = 0; i < n_extra; ++i)
     if (extra[i].bytes) std::memcpy(host + off_extra[i], extra[i].ptr, extra[i].bytes);
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
@@ -434,6 +477,7 @@ ua_status create_plan(ua_plan** out, const int32_t* cu_query_lens_host,
   plan->d_append = reinterpret_cast<ua_tile*>(base + off_app);
   plan->d_stage = reinterpret_cast<ua_tile*>(base + off_stage);
   plan->d_staged_table = reinterpret_cast<int32_t*>(base + off_st);
+  if (n_prefix) plan->d_prefix = reinterpret_cast<int32_t*>(base + off_prefix);
   for (int i = 0; i < n_extra; ++i) extra_dev[i] = base + off_extra[i];
   if (s.staged_pages > 0) {
     const size_t bytes = static_cast<size_t>(s.staged_pages) * ua::kStagePage *
@@ -669,6 +713,20 @@ ua_status ua_plan_create(ua_plan** out, const int32_t* cu_query_lens_host,
                            causal, window, num_splits, -1, stream);
 }
 
+ua_status ua_plan_create_prefix(ua_plan** out, const int32_t* cu_query_lens_host,
+                                const int32_t* kv_lens_host, const int32_t* prefix_lens_host,
+                                int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                int32_t head_dim, int32_t block_size, int32_t max_blocks_per_seq,
+                                int32_t kv_dtype, int32_t window, int32_t num_splits,
+                                int32_t decode_rows_max, ua_stream_t stream) {
+  if (out == nullptr) return UA_ERR_INVALID_ARG;
+  *out = nullptr;
+  if (num_seqs > 0 && prefix_lens_host == nullptr) return UA_ERR_INVALID_ARG;
+  return create_plan(out, cu_query_lens_host, kv_lens_host, num_seqs, num_q_heads, num_kv_heads,
+                     head_dim, block_size, max_blocks_per_seq, kv_dtype, 1, window, num_splits,
+                     decode_rows_max, stream, nullptr, 0, nullptr, prefix_lens_host);
+}
+
 ua_status ua_plan_get_info(const ua_plan* plan, ua_plan_info* info) {
   if (plan == nullptr || info == nullptr) return UA_ERR_INVALID_ARG;
   *info = plan->info;
@@ -768,6 +826,7 @@ ua_status ua_forward(const ua_plan* plan, const void* q, const void* k_cache,
     pp.window = plan->prob.window;
     pp.score_scale_log2 = kp.score_scale_log2;
     pp.out_scale = kp.v_scale;
+    pp.shape = kp.shape;
     const bool wide = ua::prefill_is_wide(plan->prob.head_dim);
     pp.rows_per_box = wide ? ua::prefill_wide_rows_per_box(pp.block_size)
                            : (pp.block_size < 128 ? pp.block_size : 128);
@@ -1113,6 +1172,26 @@ ua_status ua_plan_set_unified_max(ua_plan* plan, int32_t enable, float phi) {
   if (enable && !(std::fabs(phi) <= 1e30f)) return UA_ERR_INVALID_ARG;  // NaN, inf, huge
   plan->unified_max_on = enable != 0;
   plan->unified_max = enable ? phi : 0.f;
+  return UA_OK;
+}
+
+ua_status ua_plan_set_scores(ua_plan* plan, float softcap, const float* alibi_slopes) {
+  if (plan == nullptr) return UA_ERR_INVALID_ARG;
+  if (softcap != 0.f && !(softcap >= UA_MIN_SOFTCAP && softcap <= UA_MAX_SOFTCAP))
+    return UA_ERR_INVALID_ARG;  // NaN too
+  if (alibi_slopes != nullptr) {
+    if ((reinterpret_cast<uintptr_t>(alibi_slopes) & 3u) != 0) return UA_ERR_INVALID_ARG;
+    cudaPointerAttributes at;
+    if (cudaPointerGetAttributes(&at, alibi_slopes) != cudaSuccess) {
+      cudaGetLastError();  // not a later launch's error
+      return UA_ERR_CUDA;
+    }
+    if (at.type != cudaMemoryTypeManaged &&
+        !(at.type == cudaMemoryTypeDevice && at.device == plan->device))
+      return UA_ERR_INVALID_ARG;
+  }
+  plan->softcap = softcap;
+  plan->alibi_slopes = alibi_slopes;
   return UA_OK;
 }
 

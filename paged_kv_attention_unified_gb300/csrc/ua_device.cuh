@@ -15,6 +15,14 @@ namespace ua {
 // _attn_fwd: qk_scale = sm_scale * 1/log(2)).
 constexpr float kLog2e = 1.4426950408889634f;
 
+// Score shape of a call (score_shape.cuh); all zero: plain scores.
+struct ScoreShape {
+  float cap_log2;              // cap * log2(e); 0: no cap
+  float cap_arg;               // base-2 scaled score -> argument u of the cap: 2 log2(e) / cap_log2
+  const float* slopes;         // device [num_q_heads], or null: no distance bias
+  const int32_t* prefix_lens;  // device [num_seqs], or null: no prefix
+};
+
 struct KernelParams {
   const void* q;
   const void* k_cache;
@@ -51,6 +59,7 @@ struct KernelParams {
   // (atomicMax) on the device global timer, in ns.
   unsigned long long* span_start;
   unsigned long long* span_end;
+  ScoreShape shape;
 };
 
 struct CombineParams {

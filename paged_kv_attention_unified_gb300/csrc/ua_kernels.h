@@ -53,6 +53,7 @@ struct PrefillParams {
   // CTA's end (atomicMax) on the device global timer, in ns.
   unsigned long long* span_start;
   unsigned long long* span_end;
+  ScoreShape shape;
 };
 
 // Bit 0 of PrefillParams::debug_flags: the TMA producer skips every load, so

@@ -1,0 +1,125 @@
+"""Shaped scores without a GPU: the oracle pinned, the scheduler's key ranges
+under a prefix mask against a brute-force enumeration, and refusals."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import paged_kv_attention_unified_gb300 as ua
+import workloads as W
+from oracle import scores as S
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from paged_kv_attention_unified_gb300 import build
+    build.build()
+
+
+def _raw(case):
+    r = case.raw()
+    return (r["q"], r["k_cache"], r["v_cache"], r["cu_query_lens"], r["kv_lens"], r["block_tables"],
+            case.block_size, case.scale)
+
+
+def test_oracle_without_shape_is_the_plain_oracle():
+    for window in (0, 20):
+        case = W.random_small_case(5, head_dim=32, max_kv=120, window=window)
+        exp, _ = oracle.paged_attention(*_raw(case), causal=case.causal, window=window)
+        got, spread = S.paged_attention_shaped(*_raw(case), causal=case.causal, window=window)
+        assert np.allclose(got, exp, atol=1e-12)
+        assert np.all(spread >= np.abs(got) - 1e-12)
+
+
+def test_oracle_against_dense_torch():
+    """One dense sequence with every shape at once, by elementary torch operations."""
+    case = W.make_case("dense", [20], [50], 4, 2, 32, 16, seed=3)
+    cap, slopes, prefix, window = 3.0, [0.5, 0.25, 0.1, 0.0], 40, 33
+    got, _ = S.paged_attention_shaped(*_raw(case), window=window, softcap=cap, slopes=slopes,
+                                      prefix_lens=[prefix])
+    k, v = (c[case.block_tables[0].long()].reshape(-1, 2, 32)[:50].double()
+            for c in (case.k_cache, case.v_cache))
+    pos, t = torch.arange(30, 50)[:, None], torch.arange(50)[None, :]
+    seen = ((t <= pos) | (t < prefix)) & (t > pos - window)
+    for h in range(4):
+        x = case.q[:, h].double() @ k[:, h // 2].T * case.scale
+        x = torch.tanh(x / cap) * cap - slopes[h] * (pos - t).abs().double()
+        p = torch.softmax(x.masked_fill(~seen, -torch.inf), -1)
+        assert np.allclose(got[:, h], (p @ v[:, h // 2]).numpy(), atol=1e-12)
+
+
+def test_oracle_prefix_and_bias_by_hand():
+    assert S.visible_with_prefix(6, 2, 0, True, 0, 0).tolist() == [0, 1, 2, 3, 4]
+    assert S.visible_with_prefix(6, 6, 1, True, 0, 4).tolist() == [0, 1, 2, 3]
+    assert S.visible_with_prefix(6, 6, 5, True, 3, 4).tolist() == [3, 4, 5]
+    assert S.visible_with_prefix(6, 6, 1, True, 2, 100).tolist() == [0, 1, 2, 3, 4, 5]
+    assert np.allclose(S.shape_scores([3.0, 0.0], np.array([2, -2]), 2.0, 0.5),
+                       [2 * np.tanh(1.5) - 1.0, -1.0])
+
+
+def _ranges(cu, kv, prefix, hq, hkv, d, window, decode_rows_max=-1, bs=16):
+    info, pre, dec, grp = ua.ua_schedule(cu, kv, hq, hkv, d, bs, max(1, max(kv) // bs + 1),
+                                         window=window, decode_rows_max=decode_rows_max,
+                                         prefix_lens=prefix)
+    qpk = hq // hkv
+    covered = {}
+    for t in pre + dec:
+        for r in range(t["row0"], t["row0"] + t["nrows"]):
+            covered.setdefault((t["seq"], t["kv_head"], r), []).append((t["kv_lo"], t["kv_hi"]))
+    for s in range(len(kv)):
+        ql = cu[s + 1] - cu[s]
+        for g in range(hkv):
+            for r in range(ql * qpk):
+                pieces = sorted(covered.pop((s, g, r)))
+                for (_, a), (b, _) in zip(pieces, pieces[1:]):
+                    assert a == b
+                vis = S.visible_with_prefix(kv[s], ql, r // qpk, True, window, prefix[s])
+                assert pieces[0][0] <= vis.min() and vis.max() < pieces[-1][1] <= kv[s]
+    assert not covered
+    return info, pre, dec
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_schedule_covers_every_key_a_row_sees(seed):
+    rng = np.random.default_rng(seed)
+    n = int(rng.integers(1, 6))
+    ql = rng.integers(0, 200, n)
+    kv = ql + rng.integers(0, 400, n)
+    prefix = rng.integers(0, 500, n)
+    cu = [0] + np.cumsum(ql).tolist()
+    _ranges(cu, kv.tolist(), prefix.tolist(), 8, 2, [64, 128, 192, 96][seed % 4],
+            int(rng.choice([0, 50])), decode_rows_max=int(rng.choice([-1, 0])))
+
+
+def test_schedule_reads_no_further_than_rows_see():
+    # 300 tokens, prefix 200: tiles of 64 tokens (qpk 4) end at the prefix or at their last row
+    _, pre, _ = _ranges([0, 300], [300], [200], 4, 1, 128, 0)
+    assert sorted({(t["row0"], t["kv_hi"]) for t in pre}) == [
+        (0, 200), (256, 200), (512, 200), (768, 256), (1024, 300)]
+    # prefix 0 is the causal schedule
+    for f in ("kv_lo", "kv_hi", "row0"):
+        a = [t[f] for t in ua.ua_schedule([0, 300], [300], 4, 1, 128, 16, 20, prefix_lens=[0])[1]]
+        assert a == [t[f] for t in ua.ua_schedule([0, 300], [300], 4, 1, 128, 16, 20)[1]]
+
+
+def test_prefix_refusals():
+    with pytest.raises(ua.UAError) as e:
+        ua.ua_schedule([0, 4], [4], 4, 4, 64, 16, 1, prefix_lens=[-1])
+    assert e.value.status == ua.UA_ERR_INVALID_ARG
+    with pytest.raises(ValueError):
+        ua.ua_schedule([0, 4], [4], 4, 4, 64, 16, 1, prefix_lens=[1, 2])
+    with pytest.raises(ValueError):
+        ua.ua_schedule([0, 4], [4], 4, 4, 64, 16, 1, causal=0, prefix_lens=[1])
+    info = ua.ua_plan_info()
+    i32 = lambda *v: (ctypes.c_int32 * len(v))(*v)  # noqa: E731
+    assert ua.lib().ua_schedule_prefix(i32(0, 4), i32(4), None, 1, 4, 4, 64, 16, 1, 0, 0, 0, 0, -1,
+                                       ctypes.byref(info), None, 0, None, 0, None, 0) == ua.UA_ERR_INVALID_ARG
+    # an empty batch needs no prefix
+    assert ua.lib().ua_schedule_prefix(None, None, None, 0, 4, 4, 64, 16, 1, 0, 0, 0, 0, -1,
+                                       ctypes.byref(info), None, 0, None, 0, None, 0) == ua.UA_OK
+
+
+def test_scores_need_a_plan():
+    assert ua.lib().ua_plan_set_scores(None, 0.0, None) == ua.UA_ERR_INVALID_ARG
