@@ -350,6 +350,88 @@ ua_status ua_append_kv(const ua_plan* plan, const void* k_new, const void* v_new
                        void* v_cache, const int32_t* block_tables, int64_t num_blocks,
                        float k_scale, float v_scale, ua_stream_t stream);
 
+/*
+ * Rotary positions. A rope holds what rotates a model's heads: for each pair
+ * i < rotary_dim / 2 a frequency w_i in radians per position, and an
+ * amplitude m. The pair (a, b) of a head at position p becomes
+ *
+ *   a' = m (a cos(p w_i) - b sin(p w_i)),  b' = m (b cos(p w_i) + a sin(p w_i))
+ *
+ * where the pair is (x[i], x[i + rotary_dim / 2]) in the half layout and
+ * (x[2i], x[2i + 1]) in the interleaved one; the elements from rotary_dim on
+ * stay as they are. A rope is host memory only: it serves every device, and
+ * may be destroyed while work that used it is still queued or captured.
+ */
+typedef struct ua_rope ua_rope;
+typedef enum { UA_ROPE_HALF = 0, UA_ROPE_INTERLEAVED = 1 } ua_rope_layout;
+typedef enum {
+  UA_ROPE_PLAIN = 0,   /* w_i = base^(-2i / rotary_dim) */
+  UA_ROPE_LINEAR = 1,  /* w_i / factor */
+  UA_ROPE_NTK = 2,     /* base * factor^(rotary_dim / (rotary_dim - 2)) for base */
+  UA_ROPE_BANDS = 3,   /* pairs by their turns over the original length L, r_i = L w_i / 2 pi:
+                          w_i from `high` turns on, w_i / factor up to `low`, and between them
+                          w_i (s + (1 - s) / factor), s = (r_i - low) / (high - low) */
+  UA_ROPE_YARN = 4     /* the same blend with a ramp over the pair index, from
+                          floor(i(high)) to ceil(i(low)) with
+                          i(r) = rotary_dim ln(L / (2 pi r)) / (2 ln base), clamped to
+                          [0, rotary_dim - 1]; the amplitude is 0.1 ln(factor) + 1 */
+} ua_rope_scaling;
+
+/*
+ * ua_rope_frequencies -- the frequencies and the amplitude of a configuration,
+ * in binary64 on the host: inv_freq_host [rotary_dim / 2] and *amplitude (1
+ * but for UA_ROPE_YARN). factor >= 1 stretches contexts of
+ * original_max_position tokens (unused by UA_ROPE_PLAIN); low < high are turn
+ * counts (BANDS: usually 1 and 4; YARN: 1 and 32), used by these two only.
+ * Returns UA_ERR_INVALID_ARG for a rotary_dim that is odd or outside 2..256
+ * (NTK: below 4), a base not above 1, an unknown scaling, or factors and
+ * lengths that are not finite and in range.
+ */
+ua_status ua_rope_frequencies(int32_t rotary_dim, double base, int32_t scaling, double factor,
+                              double original_max_position, double low, double high,
+                              double* inv_freq_host, float* amplitude);
+
+/* ua_rope_create / ua_rope_destroy -- a rope from frequencies (any, with
+ * |w_i| <= 2 pi) and an amplitude (finite). rotary_dim: even, 2..256. */
+ua_status ua_rope_create(ua_rope** out, int32_t rotary_dim, int32_t layout,
+                         const double* inv_freq_host, float amplitude);
+ua_status ua_rope_destroy(ua_rope* rope);
+
+/*
+ * ua_rope_append_kv -- ua_append_kv with rotary positions: rotates the step's
+ * queries and new keys, leaves the queries in q_out (for ua_forward) and
+ * writes keys and values into the paged cache, in one launch.
+ * q, k_new, v_new: device bf16, one row per token of the plan (Hq * d, Hkv * d
+ *   and Hkv * d elements), rows q_stride, k_stride and v_stride elements apart
+ *   (multiples of 8, at least a row), e.g. inside one fused projection's
+ *   output; 16-byte aligned.
+ * q_out: device [total_q, num_q_heads, head_dim] bf16, contiguous. It may be q
+ *   itself when q's rows are contiguous (q is then rotated in place);
+ *   otherwise it must not overlap q, k_new or v_new.
+ * positions: device int32 [total_q], the rotary position of each token, or
+ *   NULL: the token's logical position in the cache, kv_len - q_len + i.
+ *   (Positions differ from it when, say, older tokens were dropped from the
+ *   cache.) They only enter the angle; any value is allowed. The angle's
+ *   error stays below 2^-22 of a turn for |position| up to 2^24.
+ * k_cache, v_cache, block_tables, num_blocks, k_scale, v_scale: as for
+ *   ua_append_kv. The rotated key is rounded once: to bf16, or as
+ *   e4m3(k' / k_scale) from the binary32 value.
+ * A token whose page id is outside [0, num_blocks) (or whose position lies
+ * past the page table) is not written to the cache and UA_ERR_BOUNDS is
+ * recorded in the plan's error word; its query is still rotated.
+ * Stream-ordered on `stream`; issue it before ua_forward on the same stream.
+ * May be captured into a graph. Returns UA_ERR_INVALID_ARG for a null plan or
+ * rope, a rotary_dim above the plan's head_dim, null or misaligned pointers,
+ * bad strides, an overlapping q_out, a bad num_blocks or scale, or a plan of
+ * another device than the current one.
+ */
+ua_status ua_rope_append_kv(const ua_plan* plan, const ua_rope* rope, const void* q,
+                            int64_t q_stride, const void* k_new, int64_t k_stride,
+                            const void* v_new, int64_t v_stride, void* q_out, void* k_cache,
+                            void* v_cache, const int32_t* block_tables, int64_t num_blocks,
+                            const int32_t* positions, float k_scale, float v_scale,
+                            ua_stream_t stream);
+
 /* Counts and sizes of a plan (host memory only). */
 ua_status ua_plan_get_info(const ua_plan* plan, ua_plan_info* info);
 

@@ -29,6 +29,13 @@ UA_DECODE_ROWS = 8
 UA_PREFILL_ROWS = 256
 UA_MIN_SOFTCAP = 2.0 ** -10
 UA_MAX_SOFTCAP = 4096.0
+UA_ROPE_HALF = 0
+UA_ROPE_INTERLEAVED = 1
+UA_ROPE_PLAIN = 0
+UA_ROPE_LINEAR = 1
+UA_ROPE_NTK = 2
+UA_ROPE_BANDS = 3
+UA_ROPE_YARN = 4
 
 # Every symbol include/ua.h declares.
 EXPORTS = (
@@ -37,6 +44,7 @@ EXPORTS = (
     "ua_gather_kv_debug", "ua_plan_set_profiling", "ua_plan_kernel_times",
     "ua_forward_static_scratch", "ua_plan_set_debug", "ua_append_kv",
     "ua_plan_set_unified_max", "ua_plan_set_prefill_ctas", "ua_plan_set_fp8_products", "ua_forward_host",
+    "ua_rope_frequencies", "ua_rope_create", "ua_rope_destroy", "ua_rope_append_kv",
     "ua_plan_set_scores", "ua_plan_create_prefix", "ua_schedule_prefix",
 )
 
@@ -71,6 +79,7 @@ _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
 _I64 = ctypes.c_int64
 _F = ctypes.c_float
+_D = ctypes.c_double
 _I32P = ctypes.POINTER(ctypes.c_int32)
 
 _SIGS = {
@@ -90,6 +99,12 @@ _SIGS = {
                                   _F, _I32, _P]),
     "ua_forward_host": (_I32, [_P, _P, _P, _P, _P, _P, _P, _I32, _I32, _I32, _I32, _I32,
                                _I32, _I64, _I32, _F, _I32, _I32, _F, _F, _I32, _I32P, _P]),
+    "ua_rope_frequencies": (_I32, [_I32, _D, _I32, _D, _D, _D, _D, ctypes.POINTER(_D),
+                                   ctypes.POINTER(_F)]),
+    "ua_rope_create": (_I32, [ctypes.POINTER(_P), _I32, _I32, ctypes.POINTER(_D), _F]),
+    "ua_rope_destroy": (_I32, [_P]),
+    "ua_rope_append_kv": (_I32, [_P, _P, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P, _I64, _P,
+                                 _F, _F, _P]),
     "ua_plan_set_scores": (_I32, [_P, _F, _P]),
     "ua_plan_create_prefix": (_I32, [ctypes.POINTER(_P), _I32P, _I32P, _I32P, _I32, _I32, _I32,
                                      _I32, _I32, _I32, _I32, _I32, _I32, _I32, _P]),
@@ -242,6 +257,70 @@ def ua_append_kv(plan, k_new, v_new, k_cache, v_cache, block_tables, num_blocks,
                               float(v_scale), _stream_handle(stream)), "ua_append_kv")
 
 
+def ua_rope_frequencies(rotary_dim, base=10000.0, scaling=UA_ROPE_PLAIN, factor=1.0,
+                        original_max_position=0.0, low=1.0, high=4.0):
+    """(frequencies in radians per position, amplitude) of a rotary configuration."""
+    w = (ctypes.c_double * max(1, int(rotary_dim) // 2))()
+    m = ctypes.c_float(0.0)
+    _check(lib().ua_rope_frequencies(int(rotary_dim), float(base), int(scaling), float(factor),
+                                     float(original_max_position), float(low), float(high), w,
+                                     ctypes.byref(m)), "ua_rope_frequencies")
+    return list(w), m.value
+
+
+def ua_rope_create(inv_freq, interleaved=False, amplitude=1.0) -> int:
+    """A rope over 2 * len(inv_freq) elements of each head; returns its handle."""
+    w = [float(x) for x in inv_freq]
+    h = ctypes.c_void_p()
+    _check(lib().ua_rope_create(ctypes.byref(h), 2 * len(w),
+                                UA_ROPE_INTERLEAVED if interleaved else UA_ROPE_HALF,
+                                (ctypes.c_double * max(1, len(w)))(*w), float(amplitude)),
+           "ua_rope_create")
+    return h.value
+
+
+def ua_rope_destroy(rope: int):
+    _check(lib().ua_rope_destroy(rope), "ua_rope_destroy")
+
+
+def _token_rows(t, name, tokens):
+    """Pointer and row stride of a bf16 [tokens, heads, head_dim] tensor whose
+    rows are contiguous (their distance is free)."""
+    import torch
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[0] != tokens or stride[2] != 1 or stride[1] != shape[2] or (
+            t.dtype != torch.bfloat16):
+        raise ValueError(f"{name}: a bf16 [tokens, heads, head_dim] tensor with contiguous rows "
+                         f"is needed, of q's {tokens} tokens ({t.dtype}, shape {tuple(shape)}, "
+                         f"strides {stride})")
+    # with one token (or none) the stride is whatever torch holds: any valid one serves
+    return t.data_ptr(), stride[0] if shape[0] > 1 else shape[1] * shape[2]
+
+
+def ua_rope_append_kv(plan, rope, q, k_new, v_new, q_out, k_cache, v_cache, block_tables,
+                      num_blocks, positions=None, k_scale=1.0, v_scale=1.0, stream=None):
+    """Rotate the step's q into q_out (q itself: in place), and its new keys
+    and values into the paged cache, on `stream`. q, k_new and v_new are
+    [tokens, heads, head_dim] CUDA tensors whose token rows may be strided."""
+    import torch
+    n = q.shape[0]
+    qp, qs = _token_rows(q, "q", n)
+    kp, ks = _token_rows(k_new, "k_new", n)
+    vp, vs = _token_rows(v_new, "v_new", n)
+    if not q_out.is_contiguous() or q_out.shape != q.shape or q_out.dtype != q.dtype:
+        raise ValueError("q_out: a contiguous tensor of q's shape and type is needed")
+    if positions is not None and (positions.shape != (n,) or not positions.is_contiguous()
+                                  or positions.dtype != torch.int32):
+        raise ValueError(f"positions: a contiguous int32 tensor of q's {n} tokens is needed")
+    ptr = lambda t: t if isinstance(t, int) else t.data_ptr()
+    _check(lib().ua_rope_append_kv(plan, rope, qp, qs, kp, ks, vp, vs, q_out.data_ptr(),
+                                   ptr(k_cache), ptr(v_cache), ptr(block_tables),
+                                   int(num_blocks),
+                                   None if positions is None else positions.data_ptr(),
+                                   float(k_scale), float(v_scale), _stream_handle(stream)),
+           "ua_rope_append_kv")
+
+
 def ua_forward_oneshot(q, k_cache, v_cache, out, cu_query_lens_host, kv_lens_host,
                        cu_query_lens, kv_lens, block_tables, num_q_heads, num_kv_heads,
                        head_dim, block_size, max_blocks_per_seq, num_blocks, kv_dtype, max_q,
@@ -365,6 +444,40 @@ def ua_forward_static_scratch(q, k_cache, v_cache, out, cu_query_lens, kv_lens, 
         "ua_forward_static_scratch")
 
 
+class Rope:
+    """RAII wrapper around a rope: rotary frequencies (radians per position,
+    one per pair), their layout and the amplitude of the rotated pairs."""
+
+    def __init__(self, inv_freq, interleaved=False, amplitude=1.0):
+        self.handle = None
+        self.handle = ua_rope_create(inv_freq, interleaved, amplitude)
+
+    @classmethod
+    def scaled(cls, rotary_dim, base=10000.0, scaling=UA_ROPE_PLAIN, factor=1.0,
+               original_max_position=0.0, low=1.0, high=4.0, interleaved=False):
+        """The rope of a configuration (ua_rope_frequencies)."""
+        w, m = ua_rope_frequencies(rotary_dim, base, scaling, factor, original_max_position,
+                                   low, high)
+        return cls(w, interleaved, m)
+
+    def close(self):
+        if self.handle:
+            ua_rope_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+
 class Plan:
     """RAII wrapper around a plan handle."""
 
@@ -383,6 +496,9 @@ class Plan:
 
     def append_kv(self, *args, **kwargs):
         ua_append_kv(self.handle, *args, **kwargs)
+
+    def rope_append_kv(self, rope, *args, **kwargs):
+        ua_rope_append_kv(self.handle, getattr(rope, "handle", rope), *args, **kwargs)
 
     def set_scores(self, softcap=0.0, alibi_slopes=None):
         import torch

@@ -51,6 +51,7 @@ _KERNEL_SOURCES = {
     "prefill": ("prefill.cu",),
     "prefill_wide": ("prefill_wide.cu",),
     "append": ("append.cu",),
+    "rope": ("rope.cu",),
     "stage": ("stage.cu",),
 }
 _SHARED_SOURCES = ("sm100.cuh", "score_shape.cuh", "ua_device.cuh", "ua_kernels.h", "tma_host.cu", "planner.cpp",

@@ -14,6 +14,12 @@
 #include "planner.h"
 #include "ua_kernels.h"
 
+struct ua_rope {
+  int32_t rotary_dim = 0;
+  int32_t layout = UA_ROPE_HALF;
+  ua::RopeTable table{};
+};
+
 struct ua_plan {
   int device = 0;
   ua::Problem prob;
@@ -917,6 +923,160 @@ ua_status ua_append_kv(const ua_plan* plan, const void* k_new, const void* v_new
   mp->last_stream = cs;
   auto* ev = timing_begin(mp, 3, cs);
   if (ua::launch_append(ap, cs) != cudaSuccess) return UA_ERR_CUDA;
+  timing_end(ev, cs);
+  return UA_OK;
+}
+
+ua_status ua_rope_frequencies(int32_t rotary_dim, double base, int32_t scaling, double factor,
+                              double original_max_position, double low, double high,
+                              double* inv_freq_host, float* amplitude) {
+  if (inv_freq_host == nullptr || amplitude == nullptr) return UA_ERR_INVALID_ARG;
+  if (rotary_dim < 2 || rotary_dim > 256 || rotary_dim % 2 != 0) return UA_ERR_INVALID_ARG;
+  if (!(base > 1.0) || !std::isfinite(base)) return UA_ERR_INVALID_ARG;
+  if (scaling < UA_ROPE_PLAIN || scaling > UA_ROPE_YARN) return UA_ERR_INVALID_ARG;
+  if (scaling != UA_ROPE_PLAIN && (!(factor >= 1.0) || !std::isfinite(factor)))
+    return UA_ERR_INVALID_ARG;
+  if (scaling == UA_ROPE_NTK && rotary_dim < 4) return UA_ERR_INVALID_ARG;
+  if (scaling == UA_ROPE_BANDS || scaling == UA_ROPE_YARN) {
+    if (!(original_max_position > 0.0) || !std::isfinite(original_max_position) || !(low > 0.0) ||
+        !(high > low) || !std::isfinite(high))
+      return UA_ERR_INVALID_ARG;
+  }
+  const int n = rotary_dim / 2;
+  const double two_pi = 6.283185307179586476925286766559;
+  double b = base;
+  if (scaling == UA_ROPE_NTK)
+    b *= std::pow(factor, static_cast<double>(rotary_dim) / (rotary_dim - 2));
+  double ramp_lo = 0.0, ramp_hi = 0.0;
+  if (scaling == UA_ROPE_YARN) {
+    // index of the pair that makes `turns` turns over the original length
+    auto at = [&](double turns) {
+      return rotary_dim * std::log(original_max_position / (turns * two_pi)) /
+             (2.0 * std::log(base));
+    };
+    ramp_lo = std::max(0.0, std::floor(at(high)));
+    ramp_hi = std::min<double>(rotary_dim - 1, std::ceil(at(low)));
+  }
+  for (int i = 0; i < n; ++i) {
+    double w = std::pow(b, -static_cast<double>(i) / n);
+    if (scaling == UA_ROPE_LINEAR) w /= factor;
+    if (scaling == UA_ROPE_BANDS) {
+      const double turns = original_max_position * w / two_pi;
+      const double keep = std::min(1.0, std::max(0.0, (turns - low) / (high - low)));
+      w *= keep + (1.0 - keep) / factor;
+    }
+    if (scaling == UA_ROPE_YARN) {
+      const double ramp =
+          std::min(1.0, std::max(0.0, (i - ramp_lo) / std::max(ramp_hi - ramp_lo, 0.001)));
+      w *= (1.0 - ramp) + ramp / factor;
+    }
+    inv_freq_host[i] = w;
+  }
+  *amplitude = scaling == UA_ROPE_YARN ? static_cast<float>(0.1 * std::log(factor) + 1.0) : 1.f;
+  return UA_OK;
+}
+
+ua_status ua_rope_create(ua_rope** out, int32_t rotary_dim, int32_t layout,
+                         const double* inv_freq_host, float amplitude) {
+  if (out == nullptr) return UA_ERR_INVALID_ARG;
+  *out = nullptr;
+  if (inv_freq_host == nullptr || rotary_dim < 2 || rotary_dim > 256 || rotary_dim % 2 != 0)
+    return UA_ERR_INVALID_ARG;
+  if (layout != UA_ROPE_HALF && layout != UA_ROPE_INTERLEAVED) return UA_ERR_INVALID_ARG;
+  if (!std::isfinite(amplitude)) return UA_ERR_INVALID_ARG;
+  // |w| <= 2 pi: at most a turn per position (the kernel's angle arithmetic
+  // removes whole turns from products of the position with these)
+  for (int32_t i = 0; i < rotary_dim / 2; ++i)
+    if (!(std::fabs(inv_freq_host[i]) <= 6.2831853071795865)) return UA_ERR_INVALID_ARG;
+  ua_rope* r = new (std::nothrow) ua_rope();
+  if (r == nullptr) return UA_ERR_INVALID_ARG;
+  r->rotary_dim = rotary_dim;
+  r->layout = layout;
+  r->table.amplitude = amplitude;
+  for (int32_t i = 0; i < rotary_dim / 2; ++i) {
+    const double turns = inv_freq_host[i] / 6.283185307179586476925286766559;
+    r->table.hi[i] = static_cast<float>(turns);
+    r->table.lo[i] = static_cast<float>(turns - static_cast<double>(r->table.hi[i]));
+  }
+  *out = r;
+  return UA_OK;
+}
+
+ua_status ua_rope_destroy(ua_rope* rope) {
+  delete rope;
+  return UA_OK;
+}
+
+ua_status ua_rope_append_kv(const ua_plan* plan, const ua_rope* rope, const void* q,
+                            int64_t q_stride, const void* k_new, int64_t k_stride,
+                            const void* v_new, int64_t v_stride, void* q_out, void* k_cache,
+                            void* v_cache, const int32_t* block_tables, int64_t num_blocks,
+                            const int32_t* positions, float k_scale, float v_scale,
+                            ua_stream_t stream) {
+  if (plan == nullptr || rope == nullptr) return UA_ERR_INVALID_ARG;
+  const ua::Problem& pr = plan->prob;
+  if (rope->rotary_dim > pr.head_dim) return UA_ERR_INVALID_ARG;
+  if (plan->sched.append.empty()) return UA_OK;
+  if (!q || !k_new || !v_new || !q_out || !k_cache || !v_cache || !block_tables)
+    return UA_ERR_INVALID_ARG;
+  for (const void* x : {q, k_new, v_new, static_cast<const void*>(q_out),
+                        static_cast<const void*>(k_cache), static_cast<const void*>(v_cache)})
+    if (!aligned16(x)) return UA_ERR_INVALID_ARG;
+  const int64_t q_row = static_cast<int64_t>(pr.num_q_heads) * pr.head_dim;
+  const int64_t kv_row = static_cast<int64_t>(pr.num_kv_heads) * pr.head_dim;
+  if (q_stride < q_row || k_stride < kv_row || v_stride < kv_row || q_stride % 8 != 0 ||
+      k_stride % 8 != 0 || v_stride % 8 != 0)
+    return UA_ERR_INVALID_ARG;
+  // q_out is q itself (contiguous rows) or apart from every input's rows.
+  const uintptr_t o0 = reinterpret_cast<uintptr_t>(q_out);
+  const uintptr_t o1 = o0 + static_cast<uintptr_t>(plan->total_q * q_row) * 2;
+  auto apart = [&](const void* x, int64_t stride, int64_t row) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(x);
+    const uintptr_t b = a + static_cast<uintptr_t>((plan->total_q - 1) * stride + row) * 2;
+    return b <= o0 || o1 <= a;
+  };
+  if (!(q == q_out && q_stride == q_row) && !apart(q, q_stride, q_row)) return UA_ERR_INVALID_ARG;
+  if (!apart(k_new, k_stride, kv_row) || !apart(v_new, v_stride, kv_row)) return UA_ERR_INVALID_ARG;
+  if (num_blocks <= 0 || num_blocks >= INT32_MAX) return UA_ERR_INVALID_ARG;
+  const bool fp8 = pr.kv_dtype == UA_KV_FP8_E4M3;
+  if (fp8 && (!std::isfinite(k_scale) || !std::isfinite(v_scale) || k_scale == 0.f ||
+              v_scale == 0.f))
+    return UA_ERR_INVALID_ARG;
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return UA_ERR_CUDA;
+  if (dev != plan->device) return UA_ERR_INVALID_ARG;
+  ua::RopeAppendParams rp;
+  std::memset(&rp, 0, sizeof(rp));
+  rp.q = q;
+  rp.k_new = k_new;
+  rp.v_new = v_new;
+  rp.q_out = q_out;
+  rp.k_cache = k_cache;
+  rp.v_cache = v_cache;
+  rp.q_stride = q_stride;
+  rp.k_stride = k_stride;
+  rp.v_stride = v_stride;
+  rp.tiles = plan->d_append;
+  rp.block_tables = block_tables;
+  rp.positions = positions;
+  rp.err = plan->d_err;
+  rp.num_blocks = num_blocks;
+  rp.num_tiles = static_cast<int32_t>(plan->sched.append.size());
+  rp.num_q_heads = pr.num_q_heads;
+  rp.num_kv_heads = pr.num_kv_heads;
+  rp.head_dim = pr.head_dim;
+  rp.max_blocks_per_seq = pr.max_blocks_per_seq;
+  rp.block_size = pr.block_size;
+  rp.rotary_dim = rope->rotary_dim;
+  rp.interleaved = rope->layout == UA_ROPE_INTERLEAVED ? 1 : 0;
+  rp.fp8 = fp8 ? 1 : 0;
+  rp.k_scale = k_scale;
+  rp.v_scale = v_scale;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  ua_plan* mp = const_cast<ua_plan*>(plan);
+  mp->last_stream = cs;
+  auto* ev = timing_begin(mp, 3, cs);
+  if (ua::launch_rope_append(rope->table, rp, cs) != cudaSuccess) return UA_ERR_CUDA;
   timing_end(ev, cs);
   return UA_OK;
 }

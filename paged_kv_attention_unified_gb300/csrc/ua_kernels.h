@@ -138,6 +138,44 @@ struct AppendParams {
 
 cudaError_t launch_append(const AppendParams& p, cudaStream_t stream);
 
+// Rotary append: the append step with q and k_new rotated to their positions.
+// Frequencies in turns per position (w / 2 pi) as the sum of two floats, by
+// value in the launch: a rope needs no device memory and serves any device.
+struct RopeTable {
+  float hi[128];
+  float lo[128];
+  float amplitude;
+};
+
+struct RopeAppendParams {
+  const void* q;                 // [total_tokens] rows of Hq * d bf16, q_stride elements apart
+  const void* k_new;             // Hkv * d bf16, k_stride apart
+  const void* v_new;             // Hkv * d bf16, v_stride apart
+  void* q_out;                   // [total_tokens][Hq][d] bf16 (may be q when that is contiguous)
+  void* k_cache;                 // [num_blocks][block_size][Hkv][d] bf16 or e4m3
+  void* v_cache;
+  int64_t q_stride, k_stride, v_stride;
+  const ua_tile* tiles;          // append tiles of the plan
+  const int32_t* block_tables;   // device [num_seqs][max_blocks_per_seq]
+  const int32_t* positions;      // device [total_tokens], or null: the slots' positions
+  int32_t* err;                  // error word (UA_ERR_BOUNDS)
+  int64_t num_blocks;
+  int32_t num_tiles;
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  int32_t head_dim;
+  int32_t max_blocks_per_seq;
+  int32_t block_size;
+  int32_t rotary_dim;            // even, 2 .. head_dim
+  int32_t interleaved;           // 1: pairs (2i, 2i + 1); 0: (i, i + rotary_dim / 2)
+  int32_t fp8;                   // 1: e4m3 cache, code = e4m3(x / scale)
+  float k_scale;
+  float v_scale;
+};
+
+cudaError_t launch_rope_append(const RopeTable& rope, const RopeAppendParams& p,
+                               cudaStream_t stream);
+
 // fp8 prefill staging: e4m3 pages of the prefill sequences -> bf16 staging
 // pages of 128 slots (exact, scale-free).
 struct StageParams {
