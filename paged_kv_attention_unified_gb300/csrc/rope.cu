@@ -17,6 +17,21 @@
 // and the position as two exact floats (p = 4096 p1 + p0); the products'
 // exact remainders (fma) are kept and whole turns removed before the parts
 // are added, which leaves an error below 2^-22 turns up to |p| = 2^24.
+//
+// HBM-bound: per token Hq d 2 B read and written, 2 Hkv d 2 B read and
+// 2 Hkv d elt written. One CTA per append tile of the plan (up to 8 new tokens
+// of one sequence): its 8 warps take one token each, or share the tile's
+// tokens when there are fewer (a decode step has one), a warp taking as many
+// whole heads at a time as its 32 lanes hold. A lane owns one unit of a head:
+// 32 bytes, two 16-byte chunks that hold whole pairs -- chunks u and
+// u + rotary_dim / 16 in the half layout, 2u and 2u + 1 otherwise -- so that a
+// rotation needs no other lane's data, in place is safe, and a lane's eight
+// (cos, sin) stay in registers over all heads of its token. They come from a
+// table in shared memory that the CTA fills once (rotary_dim / 2 sines per
+// token) while the first loads are under way.
+// When the half layout's pairs do not fall on whole chunks (rotary_dim not a
+// multiple of 16), a lane owns 16 consecutive elements and reads their
+// partners from its warp's copy of the heads in shared memory.
 #include <cstdint>
 
 #include "planner.h"
@@ -28,7 +43,9 @@ namespace ua {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
 constexpr int kMaxPairs = 128;  // rotary_dim / 2 at head_dim 256
+static_assert(kWarps == kAppendTokens, "at most one token of an append tile per warp");
 
 // (cos, sin) of 2 pi * p * (f_hi + f_lo).
 __device__ __forceinline__ float2 rotation(int32_t p, float f_hi, float f_lo) {
@@ -43,81 +60,208 @@ __device__ __forceinline__ float2 rotation(int32_t p, float f_hi, float f_lo) {
   return cs;
 }
 
-__device__ __forceinline__ float bf16_at(const void* p, int64_t i) {
-  return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p)[i]);
+// 16 bytes of a row that may be rewritten in place (no read-only path).
+__device__ __forceinline__ uint4 ld_row(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p)
+               : "memory");
+  return r;
 }
 
-// One CTA per append tile (up to 8 new tokens of one sequence).
-template <bool FP8>
+// Eight values of a chunk as binary32, and back.
+__device__ __forceinline__ void widen8(uint4 w, float (&x)[8]) {
+  x[0] = bf16_lo(w.x), x[1] = bf16_hi(w.x), x[2] = bf16_lo(w.y), x[3] = bf16_hi(w.y);
+  x[4] = bf16_lo(w.z), x[5] = bf16_hi(w.z), x[6] = bf16_lo(w.w), x[7] = bf16_hi(w.w);
+}
+__device__ __forceinline__ uint4 narrow8(const float (&x)[8]) {
+  return make_uint4(pack2<false>(x[0], x[1]), pack2<false>(x[2], x[3]), pack2<false>(x[4], x[5]),
+                    pack2<false>(x[6], x[7]));
+}
+__device__ __forceinline__ uint2 quantize8(const float (&x)[8], float scale) {
+  return make_uint2(to_e4m3x4(__fdiv_rn(x[0], scale), __fdiv_rn(x[1], scale),
+                              __fdiv_rn(x[2], scale), __fdiv_rn(x[3], scale)),
+                    to_e4m3x4(__fdiv_rn(x[4], scale), __fdiv_rn(x[5], scale),
+                              __fdiv_rn(x[6], scale), __fdiv_rn(x[7], scale)));
+}
+
+// How a lane's two chunks hold its pairs.
+enum Layout {
+  kHalf,         // a in the first chunk, b in the second (rotary_dim a multiple of 16)
+  kInterleaved,  // neighbours
+  kHalfOdd,      // 16 consecutive elements, partners through shared memory
+};
+
+// Words between the 32-byte units of a warp's copy: odd, so that lanes reading
+// the same place of their units hit different banks.
+constexpr int kUnitWords = 9;
+
+template <bool FP8, Layout LAYOUT>
 __global__ void __launch_bounds__(kThreads)
     rope_append_kernel(const __grid_constant__ RopeTable rope, const RopeAppendParams p) {
+  constexpr int kUnroll = LAYOUT == kHalfOdd ? 2 : 4;  // heads per lane with loads in flight
+  constexpr int kTurns = LAYOUT == kHalfOdd ? 16 : 8;  // (cos, sin) a lane holds
   __shared__ float2 turn[kAppendTokens][kMaxPairs];
+  __shared__ uint32_t copy[LAYOUT == kHalfOdd ? kWarps * 32 * kUnitWords : 1];
   const ua_tile tile = p.tiles[blockIdx.x];
-  const int pairs = p.rotary_dim / 2;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int d = p.head_dim, pairs = p.rotary_dim / 2;
+  const int units = d / 16;       // units of a head: 2 .. 16
+  const int at_once = 32 / units;  // heads a warp holds
+  const int slot = lane / units, u = lane - slot * units;
+  // warps per token: 8, 4, 2 or 1
+  const int log_share = tile.nrows <= 1 ? 3 : (tile.nrows <= 2 ? 2 : (tile.nrows <= 4 ? 1 : 0));
+  const int w = warp >> log_share, part = warp & ((1 << log_share) - 1);
+  const bool has_token = w < tile.nrows;
+  const int heads = p.num_q_heads + 2 * p.num_kv_heads;
+  const int64_t j = tile.row0 + (has_token ? w : 0);
+  const int pos = tile.kv_lo + (has_token ? w : 0);
+
+  const bool turns = LAYOUT == kInterleaved ? 8 * u < pairs : 16 * u < p.rotary_dim;
+  const bool apart = LAYOUT == kHalf && turns;
+  const int off0 = apart ? 8 * u : 16 * u;
+  const int off1 = apart ? 8 * u + pairs : 16 * u + 8;
+
+  const __nv_bfloat16* const q_row = static_cast<const __nv_bfloat16*>(p.q) + j * p.q_stride;
+  const __nv_bfloat16* const k_row = static_cast<const __nv_bfloat16*>(p.k_new) + j * p.k_stride;
+  const __nv_bfloat16* const v_row = static_cast<const __nv_bfloat16*>(p.v_new) + j * p.v_stride;
+  const int first_k = p.num_q_heads, first_v = p.num_q_heads + p.num_kv_heads;
+  const int stride = at_once << log_share;  // heads between a warp's steps
+
+  uint4 c0[kUnroll], c1[kUnroll];
+  auto mine = [&](int h) { return has_token && slot < at_once && h < heads; };
+  auto load = [&](int h0) {
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+      const int h = h0 + i * stride + slot;
+      if (!mine(h)) continue;
+      const bool is_v = h >= first_v;
+      const __nv_bfloat16* src = h < first_k ? q_row + h * d
+                                 : is_v      ? v_row + (h - first_v) * d
+                                             : k_row + (h - first_k) * d;
+      c0[i] = ld_row(src + (is_v ? 16 * u : off0));
+      c1[i] = ld_row(src + (is_v ? 16 * u + 8 : off1));
+    }
+  };
+  load(part * at_once);
+
+  int32_t blk = -1;
+  if (pos >= 0 && pos / p.block_size < p.max_blocks_per_seq)
+    blk = p.block_tables[static_cast<int64_t>(tile.seq) * p.max_blocks_per_seq +
+                         pos / p.block_size];
+  const bool page_ok = blk >= 0 && static_cast<int64_t>(blk) < p.num_blocks;
+  if (!page_ok && has_token && lane == 0 && part == 0) record_error(p.err, UA_ERR_BOUNDS);
+  const int64_t cache_row =
+      (static_cast<int64_t>(blk) * p.block_size + pos % p.block_size) * p.num_kv_heads;
+
   for (int x = threadIdx.x; x < tile.nrows * pairs; x += kThreads) {
-    const int w = x / pairs, i = x % pairs;
-    const int32_t pos = p.positions ? p.positions[tile.row0 + w] : tile.kv_lo + w;
-    const float2 cs = rotation(pos, rope.hi[i], rope.lo[i]);
-    turn[w][i] = make_float2(cs.x * rope.amplitude, cs.y * rope.amplitude);
+    const int t = x / pairs, i = x - t * pairs;
+    const int32_t at = p.positions ? p.positions[tile.row0 + t] : tile.kv_lo + t;
+    const float2 cs = rotation(at, rope.hi[i], rope.lo[i]);
+    turn[t][i] = make_float2(cs.x * rope.amplitude, cs.y * rope.amplitude);
   }
   __syncthreads();
-  const int d = p.head_dim;
-  const int heads = p.num_q_heads + 2 * p.num_kv_heads;
-  for (int w = 0; w < tile.nrows; ++w) {
-    const int64_t j = tile.row0 + w;
-    const int pos = tile.kv_lo + w;
-    int32_t blk = -1;
-    if (pos >= 0 && pos / p.block_size < p.max_blocks_per_seq)
-      blk = p.block_tables[static_cast<int64_t>(tile.seq) * p.max_blocks_per_seq +
-                           pos / p.block_size];
-    const bool ok = blk >= 0 && static_cast<int64_t>(blk) < p.num_blocks;
-    if (!ok && threadIdx.x == 0) record_error(p.err, UA_ERR_BOUNDS);
-    const int64_t dst_row = (static_cast<int64_t>(blk) * p.block_size + pos % p.block_size) *
-                            p.num_kv_heads;
-    // One head at a time per warp, so that in place (q_out == q) every element
-    // of a head is read before any is written.
-    for (int h = threadIdx.x / 32; h < heads; h += kThreads / 32) {
-      const bool is_q = h < p.num_q_heads, is_v = h >= p.num_q_heads + p.num_kv_heads;
-      const int hh = is_q ? h : (is_v ? h - p.num_q_heads - p.num_kv_heads : h - p.num_q_heads);
-      const void* src = is_q ? p.q : (is_v ? p.v_new : p.k_new);
-      const int64_t base =
-          j * (is_q ? p.q_stride : (is_v ? p.v_stride : p.k_stride)) + static_cast<int64_t>(hh) * d;
-      float y[8];
+  if (!has_token) return;
+  // cos and sin of this lane's pairs; kHalfOdd: of its elements, the sine with
+  // the sign its partner takes.
+  float co[kTurns], si[kTurns];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const int e = (threadIdx.x & 31) + 32 * u;
-        if (e >= d) break;
-        const float a = bf16_at(src, base + e);
-        y[u] = a;
-        if (is_v || e >= p.rotary_dim) continue;
-        const bool first = p.interleaved ? (e & 1) == 0 : e < pairs;
-        const int i = p.interleaved ? e / 2 : (first ? e : e - pairs);
-        const int other = p.interleaved ? e ^ 1 : (first ? e + pairs : e - pairs);
-        const float b = bf16_at(src, base + other);
-        const float2 cs = turn[w][i];
-        y[u] = first ? fmaf(a, cs.x, -b * cs.y) : fmaf(a, cs.x, b * cs.y);
+  for (int i = 0; i < kTurns; ++i) {
+    const int e = 16 * u + i;
+    const int pair = LAYOUT == kHalfOdd ? (e < pairs ? e : e - pairs) : 8 * u + i;
+    const float2 cs = turn[w][min(pair, pairs - 1)];
+    co[i] = cs.x;
+    si[i] = LAYOUT == kHalfOdd && e < pairs ? -cs.y : cs.y;
+  }
+  uint32_t* const heads_copy = copy + warp * 32 * kUnitWords;
+
+  for (int h0 = part * at_once; h0 < heads;) {
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+      const int h = h0 + i * stride + slot;
+      const bool is_v = h >= first_v;
+      float x0[8], x1[8];
+      widen8(c0[i], x0);
+      widen8(c1[i], x1);
+      if constexpr (LAYOUT == kHalfOdd) {
+        __syncwarp();  // the copy of the step before has been read
+        uint32_t* own = heads_copy + lane * kUnitWords;
+        own[0] = c0[i].x, own[1] = c0[i].y, own[2] = c0[i].z, own[3] = c0[i].w;
+        own[4] = c1[i].x, own[5] = c1[i].y, own[6] = c1[i].z, own[7] = c1[i].w;
+        __syncwarp();
+        if (mine(h) && !is_v && turns) {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const int e = 16 * u + k;
+            if (e >= p.rotary_dim) break;
+            const int other = e < pairs ? e + pairs : e - pairs;
+            const uint32_t word =
+                heads_copy[(slot * units + other / 16) * kUnitWords + (other % 16) / 2];
+            const float b = (other & 1) ? bf16_hi(word) : bf16_lo(word);
+            float& a = k < 8 ? x0[k % 8] : x1[k % 8];
+            a = fmaf(a, co[k], b * si[k]);
+          }
+        }
+      } else if (!is_v && turns) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          if constexpr (LAYOUT == kHalf) {
+            const float a = x0[k], b = x1[k];
+            x0[k] = fmaf(a, co[k], -b * si[k]);
+            x1[k] = fmaf(b, co[k], a * si[k]);
+          } else {
+            float& lo = k < 4 ? x0[2 * (k % 4)] : x1[2 * (k % 4)];
+            float& hi = k < 4 ? x0[2 * (k % 4) + 1] : x1[2 * (k % 4) + 1];
+            if (8 * u + k < pairs) {
+              const float a = lo, b = hi;
+              lo = fmaf(a, co[k], -b * si[k]);
+              hi = fmaf(b, co[k], a * si[k]);
+            }
+          }
+        }
       }
-      __syncwarp();
-      if (!is_q && !ok) continue;
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const int e = (threadIdx.x & 31) + 32 * u;
-        if (e >= d) break;
-        if (is_q) {
-          reinterpret_cast<__nv_bfloat16*>(
-              p.q_out)[(j * p.num_q_heads + hh) * d + e] = __float2bfloat16_rn(y[u]);
+      if (!mine(h)) continue;
+      const int o0 = is_v ? 16 * u : off0, o1 = is_v ? 16 * u + 8 : off1;
+      if (h < first_k) {
+        __nv_bfloat16* dst =
+            static_cast<__nv_bfloat16*>(p.q_out) + (j * p.num_q_heads + h) * d;
+        *reinterpret_cast<uint4*>(dst + o0) = narrow8(x0);
+        *reinterpret_cast<uint4*>(dst + o1) = narrow8(x1);
+      } else if (page_ok) {
+        const int64_t at = (cache_row + h - (is_v ? first_v : first_k)) * d;
+        void* cache = is_v ? p.v_cache : p.k_cache;
+        if constexpr (FP8) {
+          const float scale = is_v ? p.v_scale : p.k_scale;
+          uint8_t* dst = static_cast<uint8_t*>(cache) + at;
+          const uint2 lo = quantize8(x0, scale), hi = quantize8(x1, scale);
+          if (o1 == o0 + 8) {
+            *reinterpret_cast<uint4*>(dst + o0) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+          } else {
+            *reinterpret_cast<uint2*>(dst + o0) = lo;
+            *reinterpret_cast<uint2*>(dst + o1) = hi;
+          }
         } else {
-          void* cache = is_v ? p.v_cache : p.k_cache;
-          const int64_t at = (dst_row + hh) * d + e;
-          if constexpr (FP8)
-            reinterpret_cast<uint8_t*>(cache)[at] = static_cast<uint8_t>(
-                to_e4m3x4(__fdiv_rn(y[u], is_v ? p.v_scale : p.k_scale), 0.f, 0.f, 0.f) & 0xFFu);
-          else
-            reinterpret_cast<__nv_bfloat16*>(cache)[at] = __float2bfloat16_rn(y[u]);
+          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(cache) + at;
+          *reinterpret_cast<uint4*>(dst + o0) = narrow8(x0);
+          *reinterpret_cast<uint4*>(dst + o1) = narrow8(x1);
         }
       }
     }
+    h0 += kUnroll * stride;
+    if (h0 < heads) load(h0);
   }
+}
+
+template <bool FP8>
+cudaError_t launch(const RopeTable& rope, const RopeAppendParams& p, cudaStream_t stream) {
+  if (p.interleaved)
+    rope_append_kernel<FP8, kInterleaved><<<p.num_tiles, kThreads, 0, stream>>>(rope, p);
+  else if (p.rotary_dim % 16 == 0)
+    rope_append_kernel<FP8, kHalf><<<p.num_tiles, kThreads, 0, stream>>>(rope, p);
+  else
+    rope_append_kernel<FP8, kHalfOdd><<<p.num_tiles, kThreads, 0, stream>>>(rope, p);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -125,13 +269,10 @@ __global__ void __launch_bounds__(kThreads)
 cudaError_t launch_rope_append(const RopeTable& rope, const RopeAppendParams& p,
                                cudaStream_t stream) {
   if (p.num_tiles <= 0) return cudaSuccess;
-  if (p.tiles == nullptr || p.rotary_dim > 2 * kMaxPairs || p.rotary_dim > p.head_dim)
+  if (p.tiles == nullptr || p.rotary_dim > 2 * kMaxPairs || p.rotary_dim > p.head_dim ||
+      p.head_dim % 32 != 0)
     return cudaErrorInvalidValue;
-  if (p.fp8)
-    rope_append_kernel<true><<<p.num_tiles, kThreads, 0, stream>>>(rope, p);
-  else
-    rope_append_kernel<false><<<p.num_tiles, kThreads, 0, stream>>>(rope, p);
-  return cudaGetLastError();
+  return p.fp8 ? launch<true>(rope, p, stream) : launch<false>(rope, p, stream);
 }
 
 }  // namespace ua
