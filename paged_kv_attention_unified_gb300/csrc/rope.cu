@@ -19,10 +19,11 @@
 // are added, which leaves an error below 2^-22 turns up to |p| = 2^24.
 //
 // HBM-bound: per token Hq d 2 B read and written, 2 Hkv d 2 B read and
-// 2 Hkv d elt written. One CTA per append tile of the plan (up to 8 new tokens
-// of one sequence): its 8 warps take one token each, or share the tile's
-// tokens when there are fewer (a decode step has one), a warp taking as many
-// whole heads at a time as its 32 lanes hold. A lane owns one unit of a head:
+// 2 Hkv d elt written. Two CTAs of 4 warps per append tile of the plan (up to 8
+// new tokens of one sequence): the 8 warps take one token each, or share the
+// tile's tokens when there are fewer (a decode step has one), a warp taking as
+// many whole heads at a time as its 32 lanes hold, with eight such steps'
+// loads in flight. A lane owns one unit of a head:
 // 32 bytes, two 16-byte chunks that hold whole pairs -- chunks u and
 // u + rotary_dim / 16 in the half layout, 2u and 2u + 1 otherwise -- so that a
 // rotation needs no other lane's data, in place is safe, and a lane's eight
@@ -42,10 +43,11 @@ namespace ua {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
+constexpr int kParts = kAppendTokens / kWarps;  // CTAs per append tile
 constexpr int kMaxPairs = 128;  // rotary_dim / 2 at head_dim 256
-static_assert(kWarps == kAppendTokens, "at most one token of an append tile per warp");
+static_assert(kAppendTokens == 8, "a tile's eight warps share its tokens by shifts");
 
 // (cos, sin) of 2 pi * p * (f_hi + f_lo).
 __device__ __forceinline__ float2 rotation(int32_t p, float f_hi, float f_lo) {
@@ -67,6 +69,14 @@ __device__ __forceinline__ uint4 ld_row(const void* p) {
                : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
                : "l"(p)
                : "memory");
+  return r;
+}
+
+// A frequency of the launch's parameter block through a generic address. As a
+// constant-bank access the lanes' different indexes are taken one by one.
+__device__ __forceinline__ float ld_param(const float* p) {
+  float r;
+  asm volatile("ld.f32 %0, [%1];" : "=f"(r) : "l"(p));
   return r;
 }
 
@@ -100,19 +110,24 @@ constexpr int kUnitWords = 9;
 template <bool FP8, Layout LAYOUT>
 __global__ void __launch_bounds__(kThreads)
     rope_append_kernel(const __grid_constant__ RopeTable rope, const RopeAppendParams p) {
-  constexpr int kUnroll = LAYOUT == kHalfOdd ? 2 : 4;  // heads per lane with loads in flight
+  constexpr int kUnroll = LAYOUT == kHalfOdd ? 4 : 8;  // heads per lane with loads in flight
   constexpr int kTurns = LAYOUT == kHalfOdd ? 16 : 8;  // (cos, sin) a lane holds
-  __shared__ float2 turn[kAppendTokens][kMaxPairs];
+  __shared__ float2 turn[kWarps][kMaxPairs];
   __shared__ uint32_t copy[LAYOUT == kHalfOdd ? kWarps * 32 * kUnitWords : 1];
-  const ua_tile tile = p.tiles[blockIdx.x];
+  const ua_tile tile = p.tiles[blockIdx.x / kParts];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int d = p.head_dim, pairs = p.rotary_dim / 2;
   const int units = d / 16;       // units of a head: 2 .. 16
   const int at_once = 32 / units;  // heads a warp holds
   const int slot = lane / units, u = lane - slot * units;
-  // warps per token: 8, 4, 2 or 1
+  // The tile's eight warps (of kParts CTAs): 8, 4, 2 or 1 to a token. The
+  // tokens of this CTA are w0 .. w0 + tokens - 1 of the tile.
   const int log_share = tile.nrows <= 1 ? 3 : (tile.nrows <= 2 ? 2 : (tile.nrows <= 4 ? 1 : 0));
-  const int w = warp >> log_share, part = warp & ((1 << log_share) - 1);
+  const int tile_warp = blockIdx.x % kParts * kWarps + warp;
+  const int w = tile_warp >> log_share, part = tile_warp & ((1 << log_share) - 1);
+  const int w0 = (blockIdx.x % kParts * kWarps) >> log_share;
+  const int tokens = min(max(kWarps >> log_share, 1), tile.nrows - w0);
+  if (tokens <= 0) return;
   const bool has_token = w < tile.nrows;
   const int heads = p.num_q_heads + 2 * p.num_kv_heads;
   const int64_t j = tile.row0 + (has_token ? w : 0);
@@ -155,10 +170,10 @@ __global__ void __launch_bounds__(kThreads)
   const int64_t cache_row =
       (static_cast<int64_t>(blk) * p.block_size + pos % p.block_size) * p.num_kv_heads;
 
-  for (int x = threadIdx.x; x < tile.nrows * pairs; x += kThreads) {
+  for (int x = threadIdx.x; x < tokens * pairs; x += kThreads) {
     const int t = x / pairs, i = x - t * pairs;
-    const int32_t at = p.positions ? p.positions[tile.row0 + t] : tile.kv_lo + t;
-    const float2 cs = rotation(at, rope.hi[i], rope.lo[i]);
+    const int32_t at = p.positions ? p.positions[tile.row0 + w0 + t] : tile.kv_lo + w0 + t;
+    const float2 cs = rotation(at, ld_param(rope.hi + i), ld_param(rope.lo + i));
     turn[t][i] = make_float2(cs.x * rope.amplitude, cs.y * rope.amplitude);
   }
   __syncthreads();
@@ -170,7 +185,7 @@ __global__ void __launch_bounds__(kThreads)
   for (int i = 0; i < kTurns; ++i) {
     const int e = 16 * u + i;
     const int pair = LAYOUT == kHalfOdd ? (e < pairs ? e : e - pairs) : 8 * u + i;
-    const float2 cs = turn[w][min(pair, pairs - 1)];
+    const float2 cs = turn[w - w0][min(pair, pairs - 1)];
     co[i] = cs.x;
     si[i] = LAYOUT == kHalfOdd && e < pairs ? -cs.y : cs.y;
   }
@@ -185,22 +200,24 @@ __global__ void __launch_bounds__(kThreads)
       widen8(c0[i], x0);
       widen8(c1[i], x1);
       if constexpr (LAYOUT == kHalfOdd) {
-        __syncwarp();  // the copy of the step before has been read
-        uint32_t* own = heads_copy + lane * kUnitWords;
-        own[0] = c0[i].x, own[1] = c0[i].y, own[2] = c0[i].z, own[3] = c0[i].w;
-        own[4] = c1[i].x, own[5] = c1[i].y, own[6] = c1[i].z, own[7] = c1[i].w;
-        __syncwarp();
-        if (mine(h) && !is_v && turns) {
+        if (h0 + i * stride < first_v) {  // (uniform) some head of this step turns
+          __syncwarp();  // the copy of the step before has been read
+          uint32_t* own = heads_copy + lane * kUnitWords;
+          own[0] = c0[i].x, own[1] = c0[i].y, own[2] = c0[i].z, own[3] = c0[i].w;
+          own[4] = c1[i].x, own[5] = c1[i].y, own[6] = c1[i].z, own[7] = c1[i].w;
+          __syncwarp();
+          if (mine(h) && !is_v && turns) {
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const int e = 16 * u + k;
-            if (e >= p.rotary_dim) break;
-            const int other = e < pairs ? e + pairs : e - pairs;
-            const uint32_t word =
-                heads_copy[(slot * units + other / 16) * kUnitWords + (other % 16) / 2];
-            const float b = (other & 1) ? bf16_hi(word) : bf16_lo(word);
-            float& a = k < 8 ? x0[k % 8] : x1[k % 8];
-            a = fmaf(a, co[k], b * si[k]);
+            for (int k = 0; k < 16; ++k) {
+              const int e = 16 * u + k;
+              if (e >= p.rotary_dim) break;
+              const int other = e < pairs ? e + pairs : e - pairs;
+              const uint32_t word =
+                  heads_copy[(slot * units + other / 16) * kUnitWords + (other % 16) / 2];
+              const float b = (other & 1) ? bf16_hi(word) : bf16_lo(word);
+              float& a = k < 8 ? x0[k % 8] : x1[k % 8];
+              a = fmaf(a, co[k], b * si[k]);
+            }
           }
         }
       } else if (!is_v && turns) {
@@ -256,11 +273,11 @@ __global__ void __launch_bounds__(kThreads)
 template <bool FP8>
 cudaError_t launch(const RopeTable& rope, const RopeAppendParams& p, cudaStream_t stream) {
   if (p.interleaved)
-    rope_append_kernel<FP8, kInterleaved><<<p.num_tiles, kThreads, 0, stream>>>(rope, p);
+    rope_append_kernel<FP8, kInterleaved><<<p.num_tiles * kParts, kThreads, 0, stream>>>(rope, p);
   else if (p.rotary_dim % 16 == 0)
-    rope_append_kernel<FP8, kHalf><<<p.num_tiles, kThreads, 0, stream>>>(rope, p);
+    rope_append_kernel<FP8, kHalf><<<p.num_tiles * kParts, kThreads, 0, stream>>>(rope, p);
   else
-    rope_append_kernel<FP8, kHalfOdd><<<p.num_tiles, kThreads, 0, stream>>>(rope, p);
+    rope_append_kernel<FP8, kHalfOdd><<<p.num_tiles * kParts, kThreads, 0, stream>>>(rope, p);
   return cudaGetLastError();
 }
 
