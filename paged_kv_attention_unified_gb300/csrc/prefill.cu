@@ -55,6 +55,9 @@ constexpr int kThreads = 384;     // 12 warps: control warpgroup + two softmax w
 constexpr uint32_t kCtrlRegs = 56;
 constexpr uint32_t kSoftmaxRegs = 224;
 constexpr int kLaunchRegs = 168;
+// Shaped scores hold 32 columns at a time: 128 * 104 + 256 * 200 = 64512.
+constexpr uint32_t kShapedCtrlRegs = 104;
+constexpr uint32_t kShapedSoftmaxRegs = 200;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 // Work-tile descriptors the scheduler warp keeps ahead: one. A CTA claims its
@@ -530,10 +533,12 @@ __device__ __forceinline__ bool softmax_tile(const PrefillParams& p, const Softm
   const int rr = min(r, g.rows_t - 1);   // rows past the end behave like the last one
   const int row = g.row0 + t * kRows + rr;
   const int pos = g.ctx + row / p.qpk;
+  // the last key that the causal mask leaves the row
+  const int last_key = SHAPE == kShapePlain ? pos : max(pos, g.prefix - 1);
   // Scores are used as x = s * c with c >= 0: a negative scale flips the sign
   // of the raw scores once, so that the row max is always a max.
-  // Shaped scores are final base-2 values (their multiplier is 1 from there on).
-  constexpr bool kShaped = (SHAPE & (kShapeCap | kShapeBias)) != 0;
+  // (Shaped scores take c with its sign.)
+  constexpr bool kShaped = SHAPE != kShapePlain;
   const bool neg = !kShaped && p.score_scale_log2 < 0.f;
   float c = neg ? -p.score_scale_log2 : p.score_scale_log2;
   if constexpr (F8) {
@@ -583,92 +588,95 @@ __device__ __forceinline__ bool softmax_tile(const PrefillParams& p, const Softm
     mbar_arrive(bar.q_full(t));
     c = __fdiv_rn(c, inv);
   }
-  const int last_key = SHAPE != kShapePlain ? max(pos, g.prefix - 1) : pos;  // causal bound
   float slope2 = 0.f;
   if constexpr ((SHAPE & kShapeBias) != 0)
     slope2 = p.shape.slopes[g.kv_head * p.qpk + row % p.qpk] * kLog2e;
+  RowSoftmax<SHAPE, F8, kKeys> shaped(c, p.shape.cap_log2, slope2);
   float m = -INFINITY, l = 0.f;
   for (int j = 0; j < n_t; ++j) {
     if (!__all_sync(0xffffffffu, mbar_wait(bar.s_full(t), (done + j) & 1, abort, p.timeout_ns)))
       return false;
     tc_fence_after();
     const int base = g.kv_lo + j * kKeys;
-    // Raw scores; the scale is folded into one fma per pair below.
-    float x[kKeys];
-    {
-      uint32_t v[kKeys / 32][32];
-#pragma unroll
-      for (int ch = 0; ch < kKeys / 32; ++ch) tmem_ld32(s_tmem + ch * 32, v[ch]);
-      tmem_wait_ld();
-#pragma unroll
-      for (int ch = 0; ch < kKeys / 32; ++ch)
-#pragma unroll
-        for (int i = 0; i < 32; ++i) x[ch * 32 + i] = __uint_as_float(v[ch][i]);
-    }
-    if (neg) {
-#pragma unroll
-      for (int i = 0; i < kKeys; ++i) x[i] = -x[i];
-    }
-    if constexpr (kShaped)
-      shape_row<kKeys, SHAPE>(x, c, c * p.shape.cap_arg, p.shape.cap_log2, slope2, base - pos);
-    const float mult = kShaped ? 1.f : c;
-    // Mask by select: keys past the range, past the row's position (causal)
-    // or at or below pos - window.
     const int hi_col = min(g.kv_hi, p.causal ? last_key + 1 : g.kv_hi) - base;
     const int lo_col = p.window > 0 ? pos - p.window + 1 - base : INT_MIN;
-    if (hi_col < kKeys || lo_col > 0) {
-#pragma unroll
-      for (int i = 0; i < kKeys; ++i)
-        if (i >= hi_col || i < lo_col) x[i] = -INFINITY;
-    }
-    // Row max with independent 3-input partial maxima.
-    constexpr int kAcc = 8;
-    float mxp[kAcc];
-#pragma unroll
-    for (int a = 0; a < kAcc; ++a) mxp[a] = x[a];
-#pragma unroll
-    for (int i = kAcc; i < kKeys; i += 2)
-      mxp[(i / 2) % kAcc] = fmax3(mxp[(i / 2) % kAcc], x[i], x[i + 1]);
-    const float mx_raw = fmax3(fmax3(mxp[0], mxp[1], mxp[2]), fmax3(mxp[3], mxp[4], mxp[5]),
-                               fmaxf(mxp[6], mxp[7]));
-    const float m_new = fmaxf(m, mx_raw * mult);
-    const bool grow = (m == -INFINITY) || (m_new > m + kRescaleThreshold);
-    const float m_use = grow ? m_new : m;
-    const float alpha = grow ? ((m == -INFINITY) ? 0.f : ex2(m - m_use)) : 1.f;
-    const float sub = (m_use == -INFINITY) ? 0.f : m_use;
-    // p = 2^(x * c - m): one paired fma per two keys, then ex2; paired sums.
-    const uint64_t c2 = f2_pack(mult, mult), nsub2 = f2_pack(-sub, -sub);
-    uint64_t sum2[kAcc / 2];
-#pragma unroll
-    for (int a = 0; a < kAcc / 2; ++a) sum2[a] = f2_pack(0.f, 0.f);
     // P packed for the P V products: bf16 pairs, or e4m3 quadruples (F8:
     // p <= 2^8 against the lagging reference, inside e4m3's range; l sums the
     // unrounded p).
     constexpr int kPk = F8 ? kKeys / 4 : kKeys / 2;
     uint32_t pk[kPk];
-    float q0 = 0.f, q1 = 0.f;
+    float alpha = 1.f;
+    if constexpr (kShaped) {
+      alpha = shaped.tile(s_tmem, base - pos, lo_col, hi_col);
+      l = shaped.l;
+    } else {
+      // Raw scores; the scale is folded into one fma per pair below.
+      float x[kKeys];
+      {
+        uint32_t v[kKeys / 32][32];
 #pragma unroll
-    for (int i = 0; i < kKeys / 2; ++i) {
-      float e0, e1;
-      f2_unpack(f2_fma(f2_pack(x[2 * i], x[2 * i + 1]), c2, nsub2), e0, e1);
-      const float p0 = ex2(e0), p1 = ex2(e1);
-      sum2[i % (kAcc / 2)] = f2_add(sum2[i % (kAcc / 2)], f2_pack(p0, p1));
-      if constexpr (F8) {
-        if (i % 2 == 0) {
-          q0 = p0;
-          q1 = p1;
-        } else {
-          pk[i / 2] = to_e4m3x4(q0, q1, p0, p1);
-        }
-      } else {
-        pk[i] = pack2<false>(p0, p1);
+        for (int ch = 0; ch < kKeys / 32; ++ch) tmem_ld32(s_tmem + ch * 32, v[ch]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int ch = 0; ch < kKeys / 32; ++ch)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) x[ch * 32 + i] = __uint_as_float(v[ch][i]);
       }
+      if (neg) {
+#pragma unroll
+        for (int i = 0; i < kKeys; ++i) x[i] = -x[i];
+      }
+      // Mask by select: keys past the range, past the row's position (causal)
+      // or at or below pos - window.
+      if (hi_col < kKeys || lo_col > 0) {
+#pragma unroll
+        for (int i = 0; i < kKeys; ++i)
+          if (i >= hi_col || i < lo_col) x[i] = -INFINITY;
+      }
+      // Row max with independent 3-input partial maxima.
+      constexpr int kAcc = 8;
+      float mxp[kAcc];
+#pragma unroll
+      for (int a = 0; a < kAcc; ++a) mxp[a] = x[a];
+#pragma unroll
+      for (int i = kAcc; i < kKeys; i += 2)
+        mxp[(i / 2) % kAcc] = fmax3(mxp[(i / 2) % kAcc], x[i], x[i + 1]);
+      const float mx_raw = fmax3(fmax3(mxp[0], mxp[1], mxp[2]), fmax3(mxp[3], mxp[4], mxp[5]),
+                                 fmaxf(mxp[6], mxp[7]));
+      const float m_new = fmaxf(m, mx_raw * c);
+      const bool grow = (m == -INFINITY) || (m_new > m + kRescaleThreshold);
+      const float m_use = grow ? m_new : m;
+      alpha = grow ? ((m == -INFINITY) ? 0.f : ex2(m - m_use)) : 1.f;
+      const float sub = (m_use == -INFINITY) ? 0.f : m_use;
+      // p = 2^(x * c - m): one paired fma per two keys, then ex2; paired sums.
+      const uint64_t c2 = f2_pack(c, c), nsub2 = f2_pack(-sub, -sub);
+      uint64_t sum2[kAcc / 2];
+#pragma unroll
+      for (int a = 0; a < kAcc / 2; ++a) sum2[a] = f2_pack(0.f, 0.f);
+      float q0 = 0.f, q1 = 0.f;
+#pragma unroll
+      for (int i = 0; i < kKeys / 2; ++i) {
+        float e0, e1;
+        f2_unpack(f2_fma(f2_pack(x[2 * i], x[2 * i + 1]), c2, nsub2), e0, e1);
+        const float p0 = ex2(e0), p1 = ex2(e1);
+        sum2[i % (kAcc / 2)] = f2_add(sum2[i % (kAcc / 2)], f2_pack(p0, p1));
+        if constexpr (F8) {
+          if (i % 2 == 0) {
+            q0 = p0;
+            q1 = p1;
+          } else {
+            pk[i / 2] = to_e4m3x4(q0, q1, p0, p1);
+          }
+        } else {
+          pk[i] = pack2<false>(p0, p1);
+        }
+      }
+      sum2[0] = f2_add(f2_add(sum2[0], sum2[1]), f2_add(sum2[2], sum2[3]));
+      float sum_lo, sum_hi;
+      f2_unpack(sum2[0], sum_lo, sum_hi);
+      l = l * alpha + (sum_lo + sum_hi);
+      m = m_use;
     }
-    sum2[0] = f2_add(f2_add(sum2[0], sum2[1]), f2_add(sum2[2], sum2[3]));
-    float sum_lo, sum_hi;
-    f2_unpack(sum2[0], sum_lo, sum_hi);
-    l = l * alpha + (sum_lo + sum_hi);
-    m = m_use;
     // Rescale O in TMEM when some row of this warp moved its max (after the
     // exponentials: the raw scores are dead by then, which keeps the register
     // peak low).
@@ -687,14 +695,16 @@ __device__ __forceinline__ bool softmax_tile(const PrefillParams& p, const Softm
         tmem_st32(o_tmem + ch * 32, v);
       }
     }
-    // P over the first 64 (bf16) or 32 (e4m3) columns of this query tile's
-    // score columns.
+    if constexpr (!kShaped) {
+      // P over the first 64 (bf16) or 32 (e4m3) columns of this query tile's
+      // score columns.
 #pragma unroll
-    for (int ch = 0; ch < kPk / 32; ++ch) {
-      uint32_t v[32];
+      for (int ch = 0; ch < kPk / 32; ++ch) {
+        uint32_t v[32];
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = pk[ch * 32 + i];
-      tmem_st32(s_tmem + ch * 32, v);
+        for (int i = 0; i < 32; ++i) v[i] = pk[ch * 32 + i];
+        tmem_st32(s_tmem + ch * 32, v);
+      }
     }
     tmem_wait_st();
     // The last key tile may end inside a page: zero the V rows past the range
@@ -847,7 +857,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtrlRegs));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(
+        SHAPE == kShapePlain ? kCtrlRegs : kShapedCtrlRegs));
     if (warp == 0 && lane == 0) {
       producer_role<D, F8, false>(&map_q, &map_k, p, ring, sQ, sK, bar.kfull(0), bar.kempty(0), bar,
                               abort, never);
@@ -860,7 +871,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       scheduler_role<D, F8>(p, bar, ring, abort);
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(
+        SHAPE == kShapePlain ? kSoftmaxRegs : kShapedSoftmaxRegs));
     softmax_role<D, F8, SHAPE>(p, ring, (warp - 4) / 4, sQ, sV, tmem, bar, abort, warp, lane);
   }
   tc_fence_before();

@@ -394,16 +394,18 @@ __device__ __forceinline__ bool softmax_item(const PrefillParams& p, const Item&
   const int rr = min(r, it.rows - 1);   // rows past the end behave like the last one
   const int row = it.row0 + rr;
   const int pos = it.ctx + row / p.qpk;
+  // the last key that the causal mask leaves the row
+  const int last_key = SHAPE == kShapePlain ? pos : max(pos, it.prefix - 1);
   // Scores are used as x = s * c with c >= 0: a negative scale flips the sign
   // of the raw scores once, so that the row max is always a max.
-  // Shaped scores are final base-2 values (their multiplier is 1 from there on).
-  constexpr bool kShaped = (SHAPE & (kShapeCap | kShapeBias)) != 0;
+  // (Shaped scores take c with its sign.)
+  constexpr bool kShaped = SHAPE != kShapePlain;
   const bool neg = !kShaped && p.score_scale_log2 < 0.f;
   const float c = neg ? -p.score_scale_log2 : p.score_scale_log2;
-  const int last_key = SHAPE != kShapePlain ? max(pos, it.prefix - 1) : pos;  // causal bound
   float slope2 = 0.f;
   if constexpr ((SHAPE & kShapeBias) != 0)
     slope2 = p.shape.slopes[it.kv_head * p.qpk + row % p.qpk] * kLog2e;
+  RowSoftmax<SHAPE, false, kKeys> shaped(c, p.shape.cap_log2, slope2);
   float m = -INFINITY, l = 0.f;
   const int n = it.ntiles;
   for (int j = 0; j < n; ++j) {
@@ -413,68 +415,71 @@ __device__ __forceinline__ bool softmax_item(const PrefillParams& p, const Item&
       return false;
     tc_fence_after();
     const int base = it.kv_lo + j * kKeys;
-    float x[kKeys];
-    {
-      uint32_t v[kKeys / 32][32];
-#pragma unroll
-      for (int ch = 0; ch < kKeys / 32; ++ch) tmem_ld32(s_tmem + ch * 32, v[ch]);
-      tmem_wait_ld();
-#pragma unroll
-      for (int ch = 0; ch < kKeys / 32; ++ch)
-#pragma unroll
-        for (int i = 0; i < 32; ++i) x[ch * 32 + i] = __uint_as_float(v[ch][i]);
-    }
-    if (neg) {
-#pragma unroll
-      for (int i = 0; i < kKeys; ++i) x[i] = -x[i];
-    }
-    if constexpr (kShaped)
-      shape_row<kKeys, SHAPE>(x, c, c * p.shape.cap_arg, p.shape.cap_log2, slope2, base - pos);
-    const float mult = kShaped ? 1.f : c;
-    // Mask by select: keys past the range, past the row's position (causal)
-    // or at or below pos - window.
     const int hi_col = min(it.kv_hi, p.causal ? last_key + 1 : it.kv_hi) - base;
     const int lo_col = p.window > 0 ? pos - p.window + 1 - base : INT_MIN;
-    if (hi_col < kKeys || lo_col > 0) {
-#pragma unroll
-      for (int i = 0; i < kKeys; ++i)
-        if (i >= hi_col || i < lo_col) x[i] = -INFINITY;
-    }
-    constexpr int kAcc = 8;
-    float mxp[kAcc];
-#pragma unroll
-    for (int a = 0; a < kAcc; ++a) mxp[a] = x[a];
-#pragma unroll
-    for (int i = kAcc; i < kKeys; i += 2)
-      mxp[(i / 2) % kAcc] = fmax3(mxp[(i / 2) % kAcc], x[i], x[i + 1]);
-    const float mx_raw = fmax3(fmax3(mxp[0], mxp[1], mxp[2]), fmax3(mxp[3], mxp[4], mxp[5]),
-                               fmaxf(mxp[6], mxp[7]));
-    // The reference max moves only when the row max grew by more than 2^8:
-    // P and l use the same stale reference, so the result is exact up to
-    // rounding and O is rescaled only on those steps.
-    const float m_new = fmaxf(m, mx_raw * mult);
-    const bool grow = (m == -INFINITY) || (m_new > m + kRescaleThreshold);
-    const float m_use = grow ? m_new : m;
-    const float alpha = grow ? ((m == -INFINITY) ? 0.f : ex2(m - m_use)) : 1.f;
-    const float sub = (m_use == -INFINITY) ? 0.f : m_use;
-    const uint64_t c2 = f2_pack(mult, mult), nsub2 = f2_pack(-sub, -sub);
-    uint64_t sum2[kAcc / 2];
-#pragma unroll
-    for (int a = 0; a < kAcc / 2; ++a) sum2[a] = f2_pack(0.f, 0.f);
     uint32_t pk[kKeys / 2];
+    float alpha = 1.f;
+    if constexpr (kShaped) {
+      alpha = shaped.tile(s_tmem, base - pos, lo_col, hi_col);
+      l = shaped.l;
+    } else {
+      float x[kKeys];
+      {
+        uint32_t v[kKeys / 32][32];
 #pragma unroll
-    for (int i = 0; i < kKeys / 2; ++i) {
-      float e0, e1;
-      f2_unpack(f2_fma(f2_pack(x[2 * i], x[2 * i + 1]), c2, nsub2), e0, e1);
-      const float p0 = ex2(e0), p1 = ex2(e1);
-      sum2[i % (kAcc / 2)] = f2_add(sum2[i % (kAcc / 2)], f2_pack(p0, p1));
-      pk[i] = pack2<false>(p0, p1);
+        for (int ch = 0; ch < kKeys / 32; ++ch) tmem_ld32(s_tmem + ch * 32, v[ch]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int ch = 0; ch < kKeys / 32; ++ch)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) x[ch * 32 + i] = __uint_as_float(v[ch][i]);
+      }
+      if (neg) {
+#pragma unroll
+        for (int i = 0; i < kKeys; ++i) x[i] = -x[i];
+      }
+      // Mask by select: keys past the range, past the row's position (causal)
+      // or at or below pos - window.
+      if (hi_col < kKeys || lo_col > 0) {
+#pragma unroll
+        for (int i = 0; i < kKeys; ++i)
+          if (i >= hi_col || i < lo_col) x[i] = -INFINITY;
+      }
+      constexpr int kAcc = 8;
+      float mxp[kAcc];
+#pragma unroll
+      for (int a = 0; a < kAcc; ++a) mxp[a] = x[a];
+#pragma unroll
+      for (int i = kAcc; i < kKeys; i += 2)
+        mxp[(i / 2) % kAcc] = fmax3(mxp[(i / 2) % kAcc], x[i], x[i + 1]);
+      const float mx_raw = fmax3(fmax3(mxp[0], mxp[1], mxp[2]), fmax3(mxp[3], mxp[4], mxp[5]),
+                                 fmaxf(mxp[6], mxp[7]));
+      // The reference max moves only when the row max grew by more than 2^8:
+      // P and l use the same stale reference, so the result is exact up to
+      // rounding and O is rescaled only on those steps.
+      const float m_new = fmaxf(m, mx_raw * c);
+      const bool grow = (m == -INFINITY) || (m_new > m + kRescaleThreshold);
+      const float m_use = grow ? m_new : m;
+      alpha = grow ? ((m == -INFINITY) ? 0.f : ex2(m - m_use)) : 1.f;
+      const float sub = (m_use == -INFINITY) ? 0.f : m_use;
+      const uint64_t c2 = f2_pack(c, c), nsub2 = f2_pack(-sub, -sub);
+      uint64_t sum2[kAcc / 2];
+#pragma unroll
+      for (int a = 0; a < kAcc / 2; ++a) sum2[a] = f2_pack(0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < kKeys / 2; ++i) {
+        float e0, e1;
+        f2_unpack(f2_fma(f2_pack(x[2 * i], x[2 * i + 1]), c2, nsub2), e0, e1);
+        const float p0 = ex2(e0), p1 = ex2(e1);
+        sum2[i % (kAcc / 2)] = f2_add(sum2[i % (kAcc / 2)], f2_pack(p0, p1));
+        pk[i] = pack2<false>(p0, p1);
+      }
+      sum2[0] = f2_add(f2_add(sum2[0], sum2[1]), f2_add(sum2[2], sum2[3]));
+      float sum_lo, sum_hi;
+      f2_unpack(sum2[0], sum_lo, sum_hi);
+      l = l * alpha + (sum_lo + sum_hi);
+      m = m_use;
     }
-    sum2[0] = f2_add(f2_add(sum2[0], sum2[1]), f2_add(sum2[2], sum2[3]));
-    float sum_lo, sum_hi;
-    f2_unpack(sum2[0], sum_lo, sum_hi);
-    l = l * alpha + (sum_lo + sum_hi);
-    m = m_use;
     // Rescale O in TMEM when some row of this warp moved its reference (the
     // previous P V must have completed first).
     if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
@@ -492,8 +497,10 @@ __device__ __forceinline__ bool softmax_item(const PrefillParams& p, const Item&
         tmem_st32(o_tmem + ch * 32, v);
       }
     }
-    // P (bf16 pairs) over the first 32 columns of this key tile's S buffer.
-    tmem_st32(s_tmem, pk);
+    if constexpr (!kShaped) {
+      // P (bf16 pairs) over the first 32 columns of this key tile's S buffer.
+      tmem_st32(s_tmem, pk);
+    }
     tmem_wait_st();
     // The last key tile may end inside a page: zero the V rows past the range
     // (they can hold anything, and 0 * NaN would reach O).
