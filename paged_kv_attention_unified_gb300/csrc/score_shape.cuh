@@ -120,6 +120,7 @@ struct RowSoftmax {
   struct Place {
     int rel0;            // first key, relative to the row
     int lo_col, hi_col;  // visible columns
+    bool after;          // (bias) the warp has visible keys after their rows
   };
 
   __device__ __forceinline__ static void load(uint32_t taddr, float (&x)[N]) {
@@ -133,8 +134,8 @@ struct RowSoftmax {
   }
 
   // Raw scores of the columns ch .. ch + N - 1 to base-2 scores minus sub, -inf
-  // where not visible. SMALL: by the polynomial. OPEN: all of them visible and
-  // (with a bias) at or before the row, where the bias is slope * rel.
+  // where not visible. SMALL: by the polynomial. OPEN: all of them visible. The
+  // bias is slope * rel as long as visible keys lie at or before their rows.
   template <bool SMALL, bool OPEN>
   __device__ __forceinline__ void scores(float (&x)[N], int ch, const Place& at, float sub) const {
     using namespace sm100;
@@ -163,7 +164,7 @@ struct RowSoftmax {
     }
     if constexpr (kBias) {
       const float mult = kCap ? 1.f : c, base = kCap ? 0.f : -sub;
-      if constexpr (OPEN) {
+      if (OPEN || !at.after) {
         const uint64_t m2 = f2_pack(mult, mult), s2 = f2_pack(slope2, slope2);
         const uint64_t first = f2_pack(fmaf(rel, slope2, base), fmaf(rel + 1.f, slope2, base));
 #pragma unroll
@@ -179,10 +180,13 @@ struct RowSoftmax {
       }
     }
     if constexpr (!OPEN) {
+      static_assert(N == 32, "one bit per column");
       const int lo = at.lo_col - ch, hi = at.hi_col - ch;
+      uint32_t seen = hi >= N ? ~0u : (hi <= 0 ? 0u : (1u << hi) - 1u);
+      seen &= lo <= 0 ? ~0u : (lo >= N ? 0u : ~0u << lo);
 #pragma unroll
       for (int i = 0; i < N; ++i)
-        if (i >= hi || i < lo) x[i] = -INFINITY;
+        if (!(seen & (1u << i))) x[i] = -INFINITY;
     }
   }
 
@@ -258,8 +262,13 @@ struct RowSoftmax {
     uint64_t sum[4];
 #pragma unroll
     for (int a = 0; a < 4; ++a) sum[a] = f2_pack(0.f, 0.f);
-    const float alpha = KEYS == N ? whole_tile(s_tmem, rel0, lo_col, hi_col, sum)
-                                  : tile_by_columns(s_tmem, Place{rel0, max(lo_col, 0), hi_col}, sum);
+    float alpha;
+    if constexpr (KEYS == N) {
+      alpha = whole_tile(s_tmem, rel0, lo_col, hi_col, sum);
+    } else {
+      const bool after = kBias && __any_sync(0xffffffffu, rel0 + min(hi_col, KEYS) > 1);
+      alpha = tile_by_columns(s_tmem, Place{rel0, max(lo_col, 0), hi_col, after}, sum);
+    }
     sum[0] = f2_add(f2_add(sum[0], sum[1]), f2_add(sum[2], sum[3]));
     float lo, hi;
     f2_unpack(sum[0], lo, hi);
@@ -270,8 +279,8 @@ struct RowSoftmax {
  private:
   __device__ __forceinline__ float tile_by_columns(uint32_t s_tmem, const Place& at,
                                                    uint64_t (&sum)[4]) {
-    const bool open = __all_sync(0xffffffffu, at.hi_col >= KEYS && at.lo_col <= 0 &&
-                                                  (!kBias || at.rel0 + KEYS - 1 <= 0));
+    const bool open =
+        __all_sync(0xffffffffu, at.hi_col >= KEYS && at.lo_col <= 0) && !at.after;
     bool is_small = true, settled = false;  // settled: no score can move a reference
     if constexpr (kCap) {
       float amax = 0.f;
@@ -283,10 +292,13 @@ struct RowSoftmax {
       }
       is_small = __all_sync(0xffffffffu, amax <= small);
       float bound = amax * fabsf(c);  // |cap tanh(x / cap)| <= |x|
-      if constexpr (kBias)
-        bound += fmaxf(slope2 * static_cast<float>(at.rel0),
-                       slope2 * static_cast<float>(at.rel0 + KEYS - 1));
-      settled = open && __all_sync(0xffffffffu, bound <= m + kSlack);
+      if constexpr (kBias) {  // the largest bias is at one of the ends, or none at the row itself
+        const float first = fabsf(static_cast<float>(at.rel0));
+        const float last = fabsf(static_cast<float>(at.rel0 + KEYS - 1));
+        const float ends = fmaxf(-slope2 * first, -slope2 * last);
+        bound += at.rel0 <= 0 && at.rel0 + KEYS > 0 ? fmaxf(ends, 0.f) : ends;
+      }
+      settled = __all_sync(0xffffffffu, bound <= m + kSlack);
     }
     float top = -INFINITY;
     if (!settled)
