@@ -140,44 +140,41 @@ struct RowSoftmax {
   __device__ __forceinline__ void scores(float (&x)[N], int ch, const Place& at, float sub) const {
     using namespace sm100;
     const float rel = static_cast<float>(at.rel0 + ch);
-    const uint64_t nsub = f2_pack(-sub, -sub);
-    if constexpr (kCap && SMALL) {
-      const uint64_t b0 = f2_pack(a0, a0), b1 = f2_pack(a1, a1), b2 = f2_pack(a2, a2),
-                     b3 = f2_pack(a3, a3);
+    // What is added to a score: -sub, and the bias of its pair of keys.
+    const bool after = kBias && !OPEN && at.after;  // (the bias is added further down)
+    const float step = kBias && !after ? slope2 : 0.f;
+    const uint64_t step2 = f2_pack(step, step);
+    const uint64_t first = kBias ? f2_pack(fmaf(rel, step, -sub), fmaf(rel + 1.f, step, -sub))
+                                 : f2_pack(-sub, -sub);
+    auto add = [&](int i) {
+      const float f = static_cast<float>(i);
+      return kBias && i > 0 ? f2_fma(f2_pack(f, f), step2, first) : first;
+    };
+    if constexpr (kCap && !SMALL) {
+      const float u_mult = c * (2.f * kLog2e / cap_log2);
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[i] = cap_score(x[i] * u_mult, cap_log2);
+#pragma unroll
+      for (int i = 0; i < N; i += 2)
+        f2_unpack(f2_add(f2_pack(x[i], x[i + 1]), add(i)), x[i], x[i + 1]);
+    } else {
+      const uint64_t b0 = f2_pack(kCap ? a0 : c, kCap ? a0 : c), b1 = f2_pack(a1, a1),
+                     b2 = f2_pack(a2, a2), b3 = f2_pack(a3, a3);
 #pragma unroll
       for (int i = 0; i < N; i += 2) {
         const uint64_t raw = f2_pack(x[i], x[i + 1]);
-        const uint64_t sq = f2_mul(raw, raw);
-        f2_unpack(f2_fma(raw, f2_fma(f2_fma(f2_fma(b3, sq, b2), sq, b1), sq, b0), nsub), x[i],
-                  x[i + 1]);
+        uint64_t poly = b0;
+        if constexpr (kCap) {
+          const uint64_t sq = f2_mul(raw, raw);
+          poly = f2_fma(f2_fma(f2_fma(b3, sq, b2), sq, b1), sq, b0);
+        }
+        f2_unpack(f2_fma(raw, poly, add(i)), x[i], x[i + 1]);
       }
-    } else if constexpr (kCap) {
-      const float u_mult = c * (2.f * kLog2e / cap_log2), top = cap_log2 - sub;
+    }
+    if (after) {
 #pragma unroll
       for (int i = 0; i < N; ++i)
-        x[i] = fmaf(-2.f * cap_log2, rcp_approx(1.f + ex2(x[i] * u_mult)), top);
-    } else if constexpr (!kBias) {
-      const uint64_t c2 = f2_pack(c, c);
-#pragma unroll
-      for (int i = 0; i < N; i += 2)
-        f2_unpack(f2_fma(f2_pack(x[i], x[i + 1]), c2, nsub), x[i], x[i + 1]);
-    }
-    if constexpr (kBias) {
-      const float mult = kCap ? 1.f : c, base = kCap ? 0.f : -sub;
-      if (OPEN || !at.after) {
-        const uint64_t m2 = f2_pack(mult, mult), s2 = f2_pack(slope2, slope2);
-        const uint64_t first = f2_pack(fmaf(rel, slope2, base), fmaf(rel + 1.f, slope2, base));
-#pragma unroll
-        for (int i = 0; i < N; i += 2) {
-          const float step = static_cast<float>(i);
-          f2_unpack(f2_fma(f2_pack(x[i], x[i + 1]), m2, f2_fma(f2_pack(step, step), s2, first)),
-                    x[i], x[i + 1]);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-          x[i] = fmaf(x[i], mult, fmaf(-slope2, fabsf(rel + static_cast<float>(i)), base));
-      }
+        x[i] = fmaf(-slope2, fabsf(rel + static_cast<float>(i)), x[i]);
     }
     if constexpr (!OPEN) {
       static_assert(N == 32, "one bit per column");
