@@ -487,7 +487,7 @@ ua_status ua_plan_set_prefill_ctas(ua_plan* plan, int32_t num_ctas);
  *   x <- x - alibi_slopes[head] * |pos - t|     alibi_slopes given
  * in this order, before mask and softmax. Positions are those in the cache.
  * softcap: 0 (none), or from UA_MIN_SOFTCAP to UA_MAX_SOFTCAP (the absolute
- *   error of a capped score is a few 2^-24 of the cap).
+ *   error of a capped score stays below 2^-20 of the cap).
  * alibi_slopes: device [num_q_heads] float (finite; on the plan's device), or
  *   NULL (none). Not copied: the caller keeps it until the last forward that
  *   uses it (or graph that captured one) has run.

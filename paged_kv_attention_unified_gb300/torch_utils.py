@@ -10,7 +10,7 @@ from typing import Optional, Sequence
 
 import torch
 
-from . import (UA_KV_BF16, UA_KV_FP8_E4M3, Plan, ua_append_kv, ua_forward)
+from . import (UA_KV_BF16, UA_KV_FP8_E4M3, Plan, Rope, ua_append_kv, ua_forward)
 
 
 @dataclasses.dataclass
@@ -69,11 +69,11 @@ def to_device(case, device="cuda") -> DeviceBatch:
 
 
 def make_plan(b: DeviceBatch, num_splits: int = 0, decode_rows_max: int = -1,
-              stream=None) -> Plan:
+              stream=None, prefix_lens: Optional[Sequence[int]] = None) -> Plan:
     return Plan(b.cu_host, b.kv_host, b.num_q_heads, b.num_kv_heads, b.head_dim, b.block_size,
                 int(b.block_tables.shape[1]), kv_dtype=b.kv_dtype, causal=b.causal,
                 window=b.window, num_splits=num_splits, decode_rows_max=decode_rows_max,
-                stream=stream)
+                stream=stream, prefix_lens=prefix_lens)
 
 
 def forward(plan: Plan, b: DeviceBatch, out: Optional[torch.Tensor] = None,
@@ -91,6 +91,16 @@ def append_kv(plan: Plan, b: DeviceBatch, k_new: torch.Tensor, v_new: torch.Tens
     """Write new K/V rows [total_q, Hkv, d] (bf16, device) into b's caches."""
     ua_append_kv(plan.handle, k_new, v_new, b.k_cache, b.v_cache, b.block_tables, b.num_blocks,
                  b.k_scale, b.v_scale, stream)
+
+
+def rope_append_kv(plan: Plan, b: DeviceBatch, rope: Rope, q: torch.Tensor, k_new: torch.Tensor,
+                   v_new: torch.Tensor, positions: Optional[torch.Tensor] = None,
+                   stream=None) -> None:
+    """Rotate the step's queries q into b.q and its new K/V rows into b's
+    caches (all bf16, device; rows may be strided). q may be b.q itself."""
+    plan.rope_append_kv(rope, q, k_new, v_new, b.q, b.k_cache, b.v_cache, b.block_tables,
+                        b.num_blocks, positions=positions, k_scale=b.k_scale, v_scale=b.v_scale,
+                        stream=stream)
 
 
 def run(case, num_splits: int = 0, decode_rows_max: int = -1, device="cuda") -> torch.Tensor:

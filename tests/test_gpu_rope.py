@@ -300,3 +300,42 @@ def test_a_layer_step_by_step(d, dtype):
                     exp, spread = p @ v, p @ np.abs(v)
                     tol = 2.0 ** -8 * np.abs(exp) + 1.01 * (2.0 ** -8 + 2.0 ** -10) * spread + 1e-4 * fp8
                     assert np.all(np.abs(as_f64(out[i, h]) - exp) <= tol)
+
+
+def test_torch_helpers_turn_in_place_and_append():
+    s = Step([3, 1, 40], [60, 33, 40], 8, 2, 128, 16, W.FP8, seed=14)
+    q_in = s.b.q.copy_(s.q).clone()
+    with tu.make_plan(s.b, prefix_lens=[10, 0, 5]) as plan, ua.Rope(_freqs(96)) as rope:
+        tu.rope_append_kv(plan, s.b, rope, s.b.q, s.k, s.v)
+        assert plan.last_device_error() == 0
+    s.check(q_in, s.b.q, _freqs(96), False)
+
+
+@pytest.mark.parametrize("nrows", range(1, 9))
+def test_every_number_of_tokens_in_a_tile(nrows):
+    """The warps of a tile share its tokens: 1, 2, 3 .. 8 of them, and a tile more."""
+    s = Step([nrows, 8 + nrows], [nrows, 50 + nrows], 5, 1, 64, 16, seed=20 + nrows)
+    for interleaved in (False, True):
+        with tu.make_plan(s.b) as plan, ua.Rope(_freqs(64), interleaved) as rope:
+            out = s.run(plan, rope)
+            assert plan.last_device_error() == 0
+        s.check(s.q, out, _freqs(64), interleaved)
+
+
+def test_a_cache_behind_2_31_elements():
+    """Slots whose element offset passes 32 bits."""
+    hkv, d, bs, blocks = 16, 256, 256, 2100  # 2.2e9 elements a cache
+    kc, vc = (torch.zeros(blocks, bs, hkv, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    g = torch.Generator().manual_seed(15)
+    rows = torch.randn(2, 2 * hkv + 16, d, generator=g).to(torch.bfloat16).cuda()
+    q, k, v = rows[:, :16].contiguous(), rows[:, 16:16 + hkv], rows[:, 16 + hkv:]
+    table = torch.tensor([[blocks - 1]], dtype=torch.int32, device="cuda")
+    w, out = _freqs(256), torch.empty(2, 16, d, dtype=torch.bfloat16, device="cuda")
+    with ua.Plan([0, 2], [200], 16, hkv, d, bs, 1) as plan, ua.Rope(w) as rope:
+        plan.rope_append_kv(rope, q, k, v, out, kc, vc, table, blocks)
+        assert plan.last_device_error() == 0
+    exp = R.rotate(as_f64(k), [198, 199], w, False)
+    got = as_f64(kc[blocks - 1, 198:200])
+    assert np.all(np.abs(got - exp) <= 2.0 ** -8 * np.abs(exp) + 2.5e-6 * R.pair_size(as_f64(k), 256, False))
+    assert torch.equal(vc[blocks - 1, 198:200], v)
+    assert int(kc[:blocks - 1].count_nonzero()) == 0

@@ -304,3 +304,58 @@ def test_slopes_that_are_no_device_floats_are_refused():
                 plan.set_scores(0.0, slopes)
         tu.forward(plan, b)
         assert plan.last_device_error() == 0
+
+
+@pytest.mark.parametrize("d,dtype", [(64, W.BF16), (128, W.BF16), (128, W.FP8), (192, W.BF16)])
+@pytest.mark.parametrize("cap", [0.0, 15.0])
+def test_steep_negative_and_zero_slopes(d, dtype, cap):
+    """Slopes that move the reference in every key tile, that favour far keys, and none."""
+    case = W.make_case(f"steep_{d}", [150, 1, 40], [700, 900, 300], 4, 2, d, 16, kv_dtype=dtype, seed=34)
+    _check(case, cap=cap, slopes=[5.0, -0.02, 0.0, 0.3])
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_whatever_unused_slots_hold(shape, d):
+    """Slots past the last key hold infinities and the type's largest values: of no consequence,
+    neither to the result nor to which way a key tile's scores are taken."""
+    case = W.make_case(f"junk_{shape}_{d}", [90, 1, 3], [333, 45, 100], 4, 2, d, 64, seed=35)
+    case.q.abs_()
+    bs = case.block_size
+    for cache in (case.k_cache, case.v_cache):
+        for s, kv in enumerate(case.kv_lens.tolist()):
+            last = int(case.block_tables[s, (kv - 1) // bs])
+            cache[last, kv % bs:] = float("inf")
+            cache[last, kv % bs::2] = torch.finfo(torch.bfloat16).max
+    _check(case, **_shape(shape, case))
+
+
+def test_scores_on_both_sides_of_half_the_cap():
+    """Some key tiles of a prompt exceed half the cap, others do not, on either side of zero."""
+    for d in (64, 128, 256):
+        case = W.make_case(f"mix_{d}", [300], [700], 4, 2, d, 16, seed=36)
+        case.k_cache[int(case.block_tables[0, 9])] *= 8      # keys 144 .. 159
+        case.k_cache[int(case.block_tables[0, 30])] *= -20   # keys 480 .. 495
+        _check(case, cap=6.0)
+        _check(case, cap=6.0, slopes=[0.05, 0.01, 0.0, 0.2])
+
+
+def test_one_plan_changes_its_scores_between_forwards():
+    case = W.make_case("changes", [1, 130], [200, 400], 4, 2, 128, 16, seed=37)
+    b = tu.to_device(case)
+    with _plan(b) as plan:
+        for cap, slopes in ((0.0, None), (9.0, None), (0.0, _slopes(4)), (9.0, _slopes(4)), (0.0, None)):
+            plan.set_scores(cap, None if slopes is None else torch.tensor(slopes, device="cuda"))
+            exp, spread = _expected(case, cap=cap, slopes=slopes)
+            assert np.all(np.abs(as_f64(tu.forward(plan, b)) - exp) <= _bound(case, exp, spread))
+
+
+@pytest.mark.parametrize("dtype", [W.BF16, W.FP8])
+def test_a_prompt_in_chunks_sees_its_prefix_as_it_comes(dtype):
+    """The prefix reaches as far as the keys do; a chunk behind it is causal."""
+    full = W.make_case("chunks", [400], [400], 4, 2, 128, 16, kv_dtype=dtype, seed=38)
+    for begin, end in ((0, 150), (150, 151), (151, 400)):
+        case = W.make_case("chunk", [end - begin], [end], 4, 2, 128, 16, kv_dtype=dtype, seed=38,
+                           num_blocks=full.num_blocks)
+        case.q.copy_(full.q[begin:end])
+        _check(case, prefix=[220])
