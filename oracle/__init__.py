@@ -34,8 +34,12 @@ running max are part of what the method computes -- P is rounded to e4m3
 relative to the running max of its block -- so that oracle follows the
 blockwise recurrence, still in binary64.
 
-Parity pins live in tests/test_oracle_pins.py, tests/test_append_pins.py and
-tests/test_fp8_products_pins.py; every function is pinned there (none is
+Shaped scores (a tanh cap, a distance bias, a prefix mask) are in
+oracle/scores.py, rotary positions in oracle/rope.py.
+
+Parity pins live in tests/test_oracle_pins.py, tests/test_append_pins.py,
+tests/test_fp8_products_pins.py, tests/test_scores_cpu.py and
+tests/test_rope_cpu.py; every function is pinned there (none is
 "parity unpinned").
 """
 from .attention import (  # noqa: F401
