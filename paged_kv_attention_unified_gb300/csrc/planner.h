@@ -127,6 +127,12 @@ constexpr int kDefaultDecodeRowsMax = 32;
 constexpr int kPrefillKeyTile = 128;
 // Rows of one tcgen05 query tile of the prefill kernel (two per prefill tile).
 constexpr int kPrefillQueryTile = 128;
+// Head dim of the prefill kernel that takes shaped scores at head_dim d: the
+// next built one, its operands padded with zeros by the TMA copies. (Plain
+// scores run in the prefill kernels at their own head dims only.)
+constexpr int padded_head_dim(int d) {
+  return d <= 64 ? 64 : (d <= 128 ? 128 : (d <= 192 ? 192 : 256));
+}
 // Slots per page of the bf16 staging cache of fp8 prefills.
 constexpr int kStagePage = 128;
 // New tokens per append tile (one warp each in the append kernel).

@@ -737,10 +737,12 @@ __device__ __forceinline__ bool softmax_tile(const PrefillParams& p, const Softm
   const bool row_ok = r < g.rows_t;
   const int tok = g.q_start + row / p.qpk;
   const int head = g.kv_head * p.qpk + row % p.qpk;
+  const int d = kShaped ? p.head_dim : D;
   uint8_t* dst = reinterpret_cast<uint8_t*>(p.out) +
-                 (static_cast<int64_t>(tok) * p.num_q_heads + head) * D * 2;
+                 (static_cast<int64_t>(tok) * p.num_q_heads + head) * d * 2;
 #pragma unroll
   for (int ch = 0; ch < D / 32; ++ch) {
+    if (kShaped && ch * 32 >= d) break;  // columns of zeros
     uint32_t v[32];
     tmem_ld32(o_tmem + ch * 32, v);
     tmem_wait_ld();
@@ -909,7 +911,9 @@ template <int D, bool F8>
 cudaError_t launch_d(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
                      const PrefillParams& p, cudaStream_t stream) {
   constexpr int P = kShapePrefix, C = kShapeCap, B = kShapeBias;
-  switch (shape_of(p.shape)) {
+  const int shape = shape_of(p.shape);
+  if (p.head_dim > D || (shape == kShapePlain && p.head_dim != D)) return cudaErrorInvalidValue;
+  switch (shape) {
     case kShapePlain: return launch_as<D, F8, kShapePlain>(mq, mk, mv, p, stream);
     case P: return launch_as<D, F8, P>(mq, mk, mv, p, stream);
     case P | C: return launch_as<D, F8, P | C>(mq, mk, mv, p, stream);
@@ -921,7 +925,8 @@ cudaError_t launch_d(const CUtensorMap& mq, const CUtensorMap& mk, const CUtenso
 }  // namespace
 
 bool prefill_supported(int head_dim, int kv_dtype, int qpk, int block_size) {
-  if (prefill_is_wide(head_dim)) return prefill_wide_supported(kv_dtype, qpk, block_size);
+  if (head_dim == 192 || head_dim == 256)
+    return prefill_wide_supported(kv_dtype, qpk, block_size);
   return (head_dim == 64 || head_dim == 128) && kv_dtype == UA_KV_BF16 && qpk >= 1 &&
          qpk <= kRows && kRows % qpk == 0 && block_size >= 16 &&
          (kKeys % block_size == 0 || block_size % kKeys == 0);
@@ -950,8 +955,8 @@ cudaError_t launch_prefill(const PrefillParams& p, const void* q, const void* k_
     e = encode_kv_page_map(&mv, v_cache, 2, head_dim, num_kv_heads, p.block_size, p.num_blocks,
                            64, p.rows_per_box, true);
   if (e != cudaSuccess) return e;
-  return head_dim == 128 ? launch_d<128, false>(mq, mk, mv, p, stream)
-                         : launch_d<64, false>(mq, mk, mv, p, stream);
+  return head_dim > 64 ? launch_d<128, false>(mq, mk, mv, p, stream)
+                       : launch_d<64, false>(mq, mk, mv, p, stream);
 }
 
 bool prefill_fp8_products_supported(int head_dim, int qpk, int block_size) {

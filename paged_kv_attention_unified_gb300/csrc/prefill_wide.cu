@@ -534,10 +534,12 @@ __device__ __forceinline__ bool softmax_item(const PrefillParams& p, const Item&
   const bool row_ok = r < it.rows;
   const int tok = it.q_start + row / p.qpk;
   const int head = it.kv_head * p.qpk + row % p.qpk;
+  const int d = kShaped ? p.head_dim : D;
   uint8_t* dst = reinterpret_cast<uint8_t*>(p.out) +
-                 (static_cast<int64_t>(tok) * p.num_q_heads + head) * D * 2;
+                 (static_cast<int64_t>(tok) * p.num_q_heads + head) * d * 2;
 #pragma unroll 1
   for (int ch = 0; ch < D / 32; ++ch) {
+    if (kShaped && ch * 32 >= d) break;  // columns of zeros
     uint32_t v[32];
     tmem_ld32(o_tmem + ch * 32, v);
     tmem_wait_ld();
@@ -659,18 +661,18 @@ cudaError_t launch_as(const PrefillParams& p, const void* q, const void* k_cache
   {
     // Q as [total_q][Hq][D]: a box of (64 dims, qpk heads, 128/qpk tokens)
     // lands as 128 packed rows (token-major, head-minor) in one panel.
-    uint64_t dims[3] = {static_cast<uint64_t>(D), static_cast<uint64_t>(p.num_q_heads),
+    uint64_t dims[3] = {static_cast<uint64_t>(p.head_dim), static_cast<uint64_t>(p.num_q_heads),
                         static_cast<uint64_t>(total_q)};
-    uint64_t strides[2] = {static_cast<uint64_t>(D) * 2,
-                           static_cast<uint64_t>(p.num_q_heads) * D * 2};
+    uint64_t strides[2] = {static_cast<uint64_t>(p.head_dim) * 2,
+                           static_cast<uint64_t>(p.num_q_heads) * p.head_dim * 2};
     uint32_t box[3] = {64, static_cast<uint32_t>(p.qpk), static_cast<uint32_t>(kRows / p.qpk)};
     cudaError_t e = encode_tiled_map(&mq, 2, 3, q, dims, strides, box, true, 128);
     if (e != cudaSuccess) return e;
   }
-  cudaError_t e = encode_kv_page_map(&mk, k_cache, 2, D, num_kv_heads, p.block_size,
+  cudaError_t e = encode_kv_page_map(&mk, k_cache, 2, p.head_dim, num_kv_heads, p.block_size,
                                      p.num_blocks, 64, p.rows_per_box, true);
   if (e == cudaSuccess)
-    e = encode_kv_page_map(&mv, v_cache, 2, D, num_kv_heads, p.block_size, p.num_blocks, 64,
+    e = encode_kv_page_map(&mv, v_cache, 2, p.head_dim, num_kv_heads, p.block_size, p.num_blocks, 64,
                            p.rows_per_box, true);
   if (e != cudaSuccess) return e;
   static std::atomic<uint64_t> smem_set{0};
@@ -684,7 +686,9 @@ template <int D>
 cudaError_t launch(const PrefillParams& p, const void* q, const void* k, const void* v,
                    int64_t total_q, int num_kv_heads, cudaStream_t stream) {
   constexpr int P = kShapePrefix, C = kShapeCap, B = kShapeBias;
-  switch (shape_of(p.shape)) {
+  const int shape = shape_of(p.shape);
+  if (p.head_dim > D || (shape == kShapePlain && p.head_dim != D)) return cudaErrorInvalidValue;
+  switch (shape) {
     case kShapePlain: return launch_as<D, kShapePlain>(p, q, k, v, total_q, num_kv_heads, stream);
     case P: return launch_as<D, P>(p, q, k, v, total_q, num_kv_heads, stream);
     case P | C: return launch_as<D, P | C>(p, q, k, v, total_q, num_kv_heads, stream);
@@ -702,7 +706,7 @@ bool prefill_wide_supported(int kv_dtype, int qpk, int block_size) {
          block_size >= 16 && (wide::kKeys % block_size == 0 || block_size % wide::kKeys == 0);
 }
 
-bool prefill_is_wide(int head_dim) { return head_dim == 192 || head_dim == 256; }
+bool prefill_is_wide(int head_dim) { return head_dim > 128; }
 
 int prefill_wide_rows_per_box(int block_size) {
   return block_size < wide::kKeys ? block_size : wide::kKeys;
@@ -714,11 +718,8 @@ cudaError_t launch_prefill_wide(const PrefillParams& p, const void* q, const voi
   if (p.num_tiles <= 0 || p.num_ctas <= 0) return cudaSuccess;
   if (p.counters == nullptr || p.rows_per_box != prefill_wide_rows_per_box(p.block_size))
     return cudaErrorInvalidValue;
-  switch (head_dim) {
-    case 192: return wide::launch<192>(p, q, k_cache, v_cache, total_q, num_kv_heads, stream);
-    case 256: return wide::launch<256>(p, q, k_cache, v_cache, total_q, num_kv_heads, stream);
-    default: return cudaErrorInvalidValue;
-  }
+  return head_dim > 192 ? wide::launch<256>(p, q, k_cache, v_cache, total_q, num_kv_heads, stream)
+                        : wide::launch<192>(p, q, k_cache, v_cache, total_q, num_kv_heads, stream);
 }
 
 }  // namespace ua

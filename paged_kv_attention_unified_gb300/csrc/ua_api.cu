@@ -52,6 +52,10 @@ struct ua_plan {
   float softcap = 0.f;                // ua_plan_set_scores
   const float* alibi_slopes = nullptr;
   int32_t* d_prefix = nullptr;        // ua_plan_create_prefix: device prefix lengths (in d_meta)
+  // For forwards with shaped scores, where those run prompts in a prefill
+  // kernel that plain scores do not have (head dims padded to the next built
+  // one): the same batch scheduled that way. Null: this plan serves both.
+  ua_plan* shaped = nullptr;
   // kernel timing (ua_plan_set_profiling)
   struct EventPair {
     cudaEvent_t start = nullptr, stop = nullptr;
@@ -174,7 +178,8 @@ void free_plan_memory(ua_plan* p) {
 ua::Problem make_problem(const int32_t* cu, const int32_t* kv, int32_t num_seqs, int32_t hq,
                          int32_t hkv, int32_t d, int32_t bs, int32_t max_blocks, int32_t dtype,
                          int32_t causal, int32_t window, int32_t num_splits, int32_t num_sms,
-                         int32_t decode_rows_max, const int32_t* prefix = nullptr) {
+                         int32_t decode_rows_max, bool shaped = false,
+                         const int32_t* prefix = nullptr) {
   ua::Problem p;
   p.cu_query_lens = cu;
   p.kv_lens = kv;
@@ -194,7 +199,8 @@ ua::Problem make_problem(const int32_t* cu, const int32_t* kv, int32_t num_seqs,
   // An fp8 cache's prefill runs on a bf16 staging copy of 128-slot pages.
   const bool fp8 = dtype == UA_KV_FP8_E4M3;
   p.prefill_ok = hkv > 0 && hq % hkv == 0 &&
-                 ua::prefill_supported(d, fp8 ? UA_KV_BF16 : dtype, hq / hkv,
+                 ua::prefill_supported(shaped ? ua::padded_head_dim(d) : d,
+                                       fp8 ? UA_KV_BF16 : dtype, hq / hkv,
                                        fp8 ? ua::kStagePage : bs);
   p.prefill_staged = fp8 && p.prefill_ok;
   return p;
@@ -247,6 +253,12 @@ ua::KernelParams base_params(const ua_plan* plan, const void* q, const void* k, 
   kp.shape.slopes = plan->alibi_slopes;
   kp.shape.prefix_lens = plan->d_prefix;
   return kp;
+}
+
+// The plan whose lists a forward takes: the shaped one once scores are shaped.
+const ua_plan* serving(const ua_plan* plan) {
+  const bool shaped = plan->softcap > 0.f || plan->alibi_slopes != nullptr;
+  return shaped && plan->shaped != nullptr ? plan->shaped : plan;
 }
 
 // Record the start event of a timed launch (no-op unless profiling).
@@ -304,7 +316,7 @@ ua_status schedule(const int32_t* cu_query_lens_host, const int32_t* kv_lens_hos
   ua::Problem pr = make_problem(cu_query_lens_host, kv_lens_host, num_seqs, num_q_heads,
                                 num_kv_heads, head_dim, block_size, max_blocks_per_seq, kv_dtype,
                                 causal, window, num_splits, sms, decode_rows_max,
-                                prefix_lens_host);
+                                prefix_lens_host != nullptr, prefix_lens_host);
   ua::Schedule s;
   try {
     ua_status st = ua::build_schedule(pr, &s);
@@ -391,7 +403,8 @@ ua_status create_plan(ua_plan** out, const int32_t* cu_query_lens_host,
                       int32_t max_blocks_per_seq, int32_t kv_dtype, int32_t causal,
                       int32_t window, int32_t num_splits, int32_t decode_rows_max,
                       ua_stream_t stream, const HostRange* extra, int n_extra,
-                      void** extra_dev, const int32_t* prefix_lens_host = nullptr) {
+                      void** extra_dev, bool shaped = false,
+                      const int32_t* prefix_lens_host = nullptr) {
   if (out == nullptr) return UA_ERR_INVALID_ARG;
   *out = nullptr;
   int dev = 0, sms = 0;
@@ -403,7 +416,8 @@ ua_status create_plan(ua_plan** out, const int32_t* cu_query_lens_host,
   plan->device = dev;
   plan->prob = make_problem(cu_query_lens_host, kv_lens_host, num_seqs, num_q_heads,
                             num_kv_heads, head_dim, block_size, max_blocks_per_seq, kv_dtype,
-                            causal, window, num_splits, sms, decode_rows_max, prefix_lens_host);
+                            causal, window, num_splits, sms, decode_rows_max, shaped,
+                            prefix_lens_host);
   ua_status st;
   try {
     st = ua::build_schedule(plan->prob, &plan->sched);
@@ -704,9 +718,27 @@ ua_status ua_plan_create_ex(ua_plan** out, const int32_t* cu_query_lens_host,
                             int32_t max_blocks_per_seq, int32_t kv_dtype, int32_t causal,
                             int32_t window, int32_t num_splits, int32_t decode_rows_max,
                             ua_stream_t stream) {
-  return create_plan(out, cu_query_lens_host, kv_lens_host, num_seqs, num_q_heads, num_kv_heads,
-                     head_dim, block_size, max_blocks_per_seq, kv_dtype, causal, window,
-                     num_splits, decode_rows_max, stream, nullptr, 0, nullptr);
+  ua_status st = create_plan(out, cu_query_lens_host, kv_lens_host, num_seqs, num_q_heads,
+                             num_kv_heads, head_dim, block_size, max_blocks_per_seq, kv_dtype,
+                             causal, window, num_splits, decode_rows_max, stream, nullptr, 0,
+                             nullptr);
+  if (st != UA_OK || ua::padded_head_dim(head_dim) == head_dim) return st;
+  // ua_plan_set_scores may follow: the schedule of shaped scores, if it
+  // differs (a long sequence, in a problem that a prefill kernel takes).
+  const ua::Problem pr = make_problem(
+      cu_query_lens_host, kv_lens_host, num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
+      max_blocks_per_seq, kv_dtype, causal, window, num_splits, 0, decode_rows_max, true);
+  const int64_t rows_max = decode_rows_max < 0 ? ua::kDefaultDecodeRowsMax : decode_rows_max;
+  if (!pr.prefill_ok || (*out)->sched.max_q * int64_t{num_q_heads / num_kv_heads} <= rows_max)
+    return UA_OK;
+  st = create_plan(&(*out)->shaped, cu_query_lens_host, kv_lens_host, num_seqs, num_q_heads,
+                   num_kv_heads, head_dim, block_size, max_blocks_per_seq, kv_dtype, causal,
+                   window, num_splits, decode_rows_max, stream, nullptr, 0, nullptr, true);
+  if (st != UA_OK) {
+    ua_plan_destroy(*out);
+    *out = nullptr;
+  }
+  return st;
 }
 
 ua_status ua_plan_create(ua_plan** out, const int32_t* cu_query_lens_host,
@@ -730,17 +762,18 @@ ua_status ua_plan_create_prefix(ua_plan** out, const int32_t* cu_query_lens_host
   if (num_seqs > 0 && prefix_lens_host == nullptr) return UA_ERR_INVALID_ARG;
   return create_plan(out, cu_query_lens_host, kv_lens_host, num_seqs, num_q_heads, num_kv_heads,
                      head_dim, block_size, max_blocks_per_seq, kv_dtype, 1, window, num_splits,
-                     decode_rows_max, stream, nullptr, 0, nullptr, prefix_lens_host);
+                     decode_rows_max, stream, nullptr, 0, nullptr, true, prefix_lens_host);
 }
 
 ua_status ua_plan_get_info(const ua_plan* plan, ua_plan_info* info) {
   if (plan == nullptr || info == nullptr) return UA_ERR_INVALID_ARG;
-  *info = plan->info;
+  *info = serving(plan)->info;
   return UA_OK;
 }
 
 ua_status ua_plan_destroy(ua_plan* plan) {
   if (plan == nullptr) return UA_OK;
+  ua_plan_destroy(plan->shaped);
   int cur = 0;
   cudaGetDevice(&cur);
   if (cur != plan->device) cudaSetDevice(plan->device);
@@ -756,6 +789,9 @@ ua_status ua_forward(const ua_plan* plan, const void* q, const void* k_cache,
                      int32_t max_q, int32_t max_kv, float scale, float k_scale, float v_scale,
                      ua_stream_t stream) {
   if (plan == nullptr) return UA_ERR_INVALID_ARG;
+  if (serving(plan) != plan)
+    return ua_forward(plan->shaped, q, k_cache, v_cache, out, cu_query_lens, kv_lens,
+                      block_tables, num_blocks, max_q, max_kv, scale, k_scale, v_scale, stream);
   const ua::Schedule& s = plan->sched;
   const bool any = !s.prefill.empty() || !s.decode.empty();
   if (!any) return UA_OK;
@@ -827,6 +863,7 @@ ua_status ua_forward(const ua_plan* plan, const void* q, const void* k_cache,
     pp.max_blocks_per_seq = staged ? s.staged_max_blocks : plan->prob.max_blocks_per_seq;
     pp.block_size = staged ? ua::kStagePage : plan->prob.block_size;
     pp.num_q_heads = plan->prob.num_q_heads;
+    pp.head_dim = plan->prob.head_dim;
     pp.qpk = kp.qpk;
     pp.causal = plan->prob.causal;
     pp.window = plan->prob.window;
@@ -1213,6 +1250,12 @@ ua_status ua_last_device_error(ua_plan* plan, int32_t* code) {
   const int32_t zero = 0;
   if (cudaMemcpy(plan->d_err, &zero, sizeof(zero), cudaMemcpyHostToDevice) != cudaSuccess)
     return UA_ERR_CUDA;
+  if (plan->shaped != nullptr) {
+    int32_t sv = 0;
+    const ua_status st = ua_last_device_error(plan->shaped, &sv);
+    if (st != UA_OK) return st;
+    if (v == UA_OK) v = sv;
+  }
   *code = v;
   return UA_OK;
 }
@@ -1226,6 +1269,7 @@ ua_status ua_gather_kv_debug(const ua_plan* plan, const void* k_cache, const voi
   if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_out) || !aligned16(v_out) ||
       num_blocks <= 0)
     return UA_ERR_INVALID_ARG;
+  plan = serving(plan);
   const ua::Schedule& s = plan->sched;
   // Row offsets from the host ranges; the kernel clamps by the device kv_lens,
   // which the caller guarantees equal the plan's.
@@ -1263,7 +1307,7 @@ ua_status ua_plan_set_profiling(ua_plan* plan, int32_t enable) {
     if (span_reset(plan, kSpanSlots, plan->last_stream) != cudaSuccess) return UA_ERR_CUDA;
   }
   plan->profiling = enable != 0;
-  return UA_OK;
+  return plan->shaped != nullptr ? ua_plan_set_profiling(plan->shaped, enable) : UA_OK;
 }
 
 ua_status ua_plan_kernel_times(ua_plan* plan, float* ms, int64_t* launches) {
@@ -1298,6 +1342,16 @@ ua_status ua_plan_kernel_times(ua_plan* plan, float* ms, int64_t* launches) {
         cudaStreamSynchronize(plan->last_stream) != cudaSuccess)
       st = UA_ERR_CUDA;
   }
+  if (plan->shaped != nullptr) {
+    float sms[UA_KERNEL_KINDS];
+    int64_t sl[UA_KERNEL_KINDS];
+    const ua_status ss = ua_plan_kernel_times(plan->shaped, sms, sl);
+    if (ss != UA_OK) st = ss;
+    for (int k = 0; k < UA_KERNEL_KINDS; ++k) {
+      ms[k] += sms[k];
+      launches[k] += sl[k];
+    }
+  }
   return st;
 }
 
@@ -1306,13 +1360,13 @@ ua_status ua_plan_set_debug(ua_plan* plan, int32_t flags, int64_t wait_timeout_n
   plan->debug_flags = flags;
   plan->wait_timeout_ns = wait_timeout_ns > 0 ? static_cast<uint64_t>(wait_timeout_ns)
                                               : 2000000000ull;
-  return UA_OK;
+  return plan->shaped != nullptr ? ua_plan_set_debug(plan->shaped, flags, wait_timeout_ns) : UA_OK;
 }
 
 ua_status ua_plan_set_prefill_ctas(ua_plan* plan, int32_t num_ctas) {
   if (plan == nullptr || num_ctas < 0) return UA_ERR_INVALID_ARG;
   plan->prefill_ctas_override = num_ctas;
-  return UA_OK;
+  return plan->shaped != nullptr ? ua_plan_set_prefill_ctas(plan->shaped, num_ctas) : UA_OK;
 }
 
 ua_status ua_plan_set_fp8_products(ua_plan* plan, int32_t enable) {
@@ -1333,7 +1387,7 @@ ua_status ua_plan_set_unified_max(ua_plan* plan, int32_t enable, float phi) {
   if (enable && !(std::fabs(phi) <= 1e30f)) return UA_ERR_INVALID_ARG;  // NaN, inf, huge
   plan->unified_max_on = enable != 0;
   plan->unified_max = enable ? phi : 0.f;
-  return UA_OK;
+  return plan->shaped != nullptr ? ua_plan_set_unified_max(plan->shaped, enable, phi) : UA_OK;
 }
 
 ua_status ua_plan_set_scores(ua_plan* plan, float softcap, const float* alibi_slopes) {
@@ -1351,8 +1405,11 @@ ua_status ua_plan_set_scores(ua_plan* plan, float softcap, const float* alibi_sl
         !(at.type == cudaMemoryTypeDevice && at.device == plan->device))
       return UA_ERR_INVALID_ARG;
   }
-  plan->softcap = softcap;
-  plan->alibi_slopes = alibi_slopes;
+  for (ua_plan* p : {plan, plan->shaped}) {
+    if (p == nullptr) continue;
+    p->softcap = softcap;
+    p->alibi_slopes = alibi_slopes;
+  }
   return UA_OK;
 }
 

@@ -41,6 +41,7 @@ struct PrefillParams {
   int32_t max_blocks_per_seq;
   int32_t block_size;
   int32_t num_q_heads;
+  int32_t head_dim;         // the tensors' (shaped scores: at most the kernel's)
   int32_t qpk;
   int32_t causal;
   int32_t window;
@@ -61,7 +62,7 @@ struct PrefillParams {
 constexpr int32_t kDebugProducerIdle = 1;
 
 // Whether the prefill kernel can take a problem with these parameters
-// (host-only check, no CUDA call).
+// (host-only check, no CUDA call). Shaped scores: ask with padded_head_dim.
 bool prefill_supported(int head_dim, int kv_dtype, int qpk, int block_size);
 
 // Persistent prefill kernel: p.num_ctas CTAs take p.tiles in order as they
@@ -88,7 +89,7 @@ cudaError_t launch_prefill_fp8_products(const PrefillParams& p, const void* k_ca
 // launch_prefill).
 bool prefill_wide_supported(int kv_dtype, int qpk, int block_size);
 int prefill_wide_rows_per_box(int block_size);
-bool prefill_is_wide(int head_dim);
+bool prefill_is_wide(int head_dim);  // which of the two kernels takes it
 cudaError_t launch_prefill_wide(const PrefillParams& p, const void* q, const void* k_cache,
                                 const void* v_cache, int64_t total_q, int head_dim,
                                 int num_kv_heads, cudaStream_t stream);

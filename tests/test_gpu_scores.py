@@ -359,3 +359,45 @@ def test_a_prompt_in_chunks_sees_its_prefix_as_it_comes(dtype):
                            num_blocks=full.num_blocks)
         case.q.copy_(full.q[begin:end])
         _check(case, prefix=[220])
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("d,dtype,hq,hkv,bs", [
+    (32, W.BF16, 4, 2, 16), (32, W.FP8, 8, 2, 32), (96, W.BF16, 4, 1, 16), (96, W.FP8, 2, 2, 128),
+    (160, W.BF16, 4, 2, 64), (160, W.FP8, 4, 4, 16), (224, W.BF16, 2, 1, 16), (224, W.FP8, 8, 4, 32)])
+def test_prompts_at_the_other_head_dims(shape, d, dtype, hq, hkv, bs):
+    """Shaped scores have a prefill kernel at every head dim (operands padded with zeros), beside
+    decoding sequences; unused slots poisoned."""
+    case = W.make_case(f"pad_{shape}_{d}_{dtype}", [200, 1, 131, 2], [257, 300, 600, 40], hq, hkv, d, bs,
+                       kv_dtype=dtype, seed=d + 2, poison=True)
+    info = _check(case, **_shape(shape, case))
+    assert info.num_prefill_tiles > 0 and info.num_decode_tiles > 0
+
+
+def test_plans_at_the_other_head_dims_switch_with_their_scores():
+    """The lists, the settings, the errors and the timing of a plan follow its scores."""
+    case = W.make_case("switch", [150, 1], [200, 90], 4, 2, 96, 16, seed=39)
+    b = tu.to_device(case)
+    with _plan(b) as never, _plan(b) as plan:
+        want = tu.forward(never, b)
+        assert plan.info.num_prefill_tiles == 0
+        for _ in range(2):
+            plan.set_scores(12.0)
+            assert plan.info.num_prefill_tiles > 0
+            ua.ua_plan_set_prefill_ctas(plan.handle, 1)
+            plan.set_unified_max(0.0)
+            exp, spread = _expected(case, cap=12.0)
+            assert np.all(np.abs(as_f64(tu.forward(plan, b)) - exp) <= _bound(case, exp, spread))
+            plan.set_scores()
+            plan.set_unified_max(None)
+            assert plan.info.num_prefill_tiles == 0
+            assert torch.equal(tu.forward(plan, b), want)
+        plan.set_scores(12.0)
+        ua.ua_plan_set_profiling(plan.handle, True)
+        tu.forward(plan, b)
+        times = ua.ua_plan_kernel_times(plan.handle)
+        assert times["prefill"][1] == 1 and times["decode"][1] == 1
+        b.block_tables[0, 2] = b.num_blocks + 7
+        tu.forward(plan, b)
+        assert plan.last_device_error() == ua.UA_ERR_BOUNDS
+        assert plan.last_device_error() == 0

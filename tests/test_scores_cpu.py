@@ -104,6 +104,15 @@ def test_schedule_reads_no_further_than_rows_see():
         assert a == [t[f] for t in ua.ua_schedule([0, 300], [300], 4, 1, 128, 16, 20)[1]]
 
 
+@pytest.mark.parametrize("d", [32, 64, 96, 128, 160, 192, 224, 256])
+def test_prompts_with_a_prefix_have_a_prefill_kernel_at_every_head_dim(d):
+    info, pre, dec = _ranges([0, 40, 41], [90, 300], [7, 0], 4, 2, d, 0)
+    assert info.num_prefill_tiles > 0 and {t["seq"] for t in dec} == {1}
+    # but none where no kernel takes the group size, or the block size
+    assert _ranges([0, 40], [90], [7], 5, 1, d, 0)[0].num_prefill_tiles == 0
+    assert _ranges([0, 40], [90], [7], 4, 2, d, 0, bs=48)[0].num_prefill_tiles == 0
+
+
 def test_prefix_refusals():
     with pytest.raises(ua.UAError) as e:
         ua.ua_schedule([0, 4], [4], 4, 4, 64, 16, 1, prefix_lens=[-1])
