@@ -210,7 +210,7 @@ ua_status ua_plan_create_ex(ua_plan** out, const int32_t* cu_query_lens_host,
  * prefix_lens_host: [num_seqs], each >= 0; a prefix beyond kv_len reaches as
  * far as the keys do (a prompt given in chunks), 0 is the causal mask. The
  * plan keeps its own copy. Sequences that are too long for the decode kernel
- * run in a prefill kernel at every head dim. Other arguments, work and errors
+ * run in a prefill kernel at every head dim (see ua_plan_set_scores). Other arguments, work and errors
  * as ua_plan_create_ex; UA_ERR_INVALID_ARG for a null or negative prefix too.
  * ua_schedule_prefix -- its scheduler alone, as ua_schedule.
  */
@@ -493,9 +493,10 @@ ua_status ua_plan_set_prefill_ctas(ua_plan* plan, int32_t num_ctas);
  *   NULL (none). Not copied: the caller keeps it until the last forward that
  *   uses it (or graph that captured one) has run.
  * Sequences too long for the decode kernel (more than decode_rows_max packed
- * rows) run in a prefill kernel at every head dim then, whereas with plain
- * scores and no prefix only the head dims 64, 128, 192 and 256 have one
- * (ua_schedule); ua_plan_get_info tells the lists of the current setting.
+ * rows; with the built-in default, where they are work enough) run in a
+ * prefill kernel at every head dim then, whereas with plain scores and no
+ * prefix only the head dims 64, 128, 192 and 256 have one (ua_schedule);
+ * ua_plan_get_info tells the lists of the current setting.
  * Every prefill and decode kernel applies them, together with the window, the
  * causal or prefix mask, the unified max and fp8 products; ua_forward_oneshot,
  * ua_forward_host and ua_forward_static_scratch, which take no plan, have

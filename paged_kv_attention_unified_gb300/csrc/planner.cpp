@@ -121,12 +121,28 @@ ua_status validate(const Problem& p) {
   return UA_OK;
 }
 
+bool padded_prefill_pays(const Problem& p) {
+  if (p.decode_rows_max >= 0) return true;
+  const int64_t qpk = p.num_q_heads / p.num_kv_heads;
+  double tile_keys = 0.0;
+  for (int32_t q = 0; q < p.num_seqs; ++q) {
+    const int64_t ql = p.cu_query_lens[q + 1] - p.cu_query_lens[q];
+    if (ql * qpk <= kDefaultDecodeRowsMax) continue;
+    int64_t keys = p.kv_lens[q];
+    if (p.window > 0) keys = std::min<int64_t>(keys, static_cast<int64_t>(p.window) + ql);
+    tile_keys += static_cast<double>(ceil_div(ql * qpk, UA_DECODE_ROWS) * p.num_kv_heads * keys);
+  }
+  const double decode_ns = tile_keys / std::min(31.0, 1900.0 / p.head_dim);
+  return decode_ns > (p.head_dim <= 128 ? 30e3 : 55e3);
+}
+
 ua_status build_schedule(const Problem& p, Schedule* out) {
   ua_status st = validate(p);
   if (st != UA_OK) return st;
   Schedule s;
   const int qpk = p.num_q_heads / p.num_kv_heads;
-  const int64_t rows_max = !p.prefill_ok ? INT64_MAX
+  const bool prefill_ok = p.prefill_ok && (!p.prefill_padded || padded_prefill_pays(p));
+  const int64_t rows_max = !prefill_ok ? INT64_MAX
                            : (p.decode_rows_max < 0 ? kDefaultDecodeRowsMax : p.decode_rows_max);
   const int num_sms = p.num_sms > 0 ? p.num_sms : 152;
 

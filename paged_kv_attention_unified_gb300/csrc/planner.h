@@ -33,6 +33,7 @@ struct Problem {
   int32_t decode_rows_max = -1; // < 0: default
   bool prefill_ok = false;      // the prefill kernel can take this problem
   bool prefill_staged = false;  // fp8 cache: the prefill kernel reads a bf16 staging copy
+  bool prefill_padded = false;  // shaped scores at a head dim without a prefill kernel of its own
 };
 
 struct Schedule {
@@ -133,6 +134,16 @@ constexpr int kPrefillQueryTile = 128;
 constexpr int padded_head_dim(int d) {
   return d <= 64 ? 64 : (d <= 128 ? 128 : (d <= 192 ? 192 : 256));
 }
+// Whether a padded problem's long sequences go to that kernel: when the decode
+// kernel would take longer for them than the other's latency. It passes about
+// 1900 / d (at most 31) keys of an 8-row tile per ns over the whole GPU; the
+// prefill kernels need about 30 us (d <= 128) or 55 us (staging, conversions
+// and two 128-row tiles one after the other) for 1000 keys however few rows
+// there are. Measured at 1000 to 1500 keys (decode / prefill): head_dim 96, 16
+// sequences of 48 rows and 8 KV heads 75 / 43 us, 4 of 96 rows 29 / 31 us, one
+// of 800 rows and 2 KV heads 25 / 42 us; head_dim 224, 4 of 144 rows 104 / 72
+// us, one of 800 rows 46 / 80 us. (decode_rows_max >= 0 decides by itself.)
+bool padded_prefill_pays(const Problem& p);
 // Slots per page of the bf16 staging cache of fp8 prefills.
 constexpr int kStagePage = 128;
 // New tokens per append tile (one warp each in the append kernel).

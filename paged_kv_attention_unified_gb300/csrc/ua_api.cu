@@ -203,6 +203,7 @@ ua::Problem make_problem(const int32_t* cu, const int32_t* kv, int32_t num_seqs,
                                        fp8 ? UA_KV_BF16 : dtype, hq / hkv,
                                        fp8 ? ua::kStagePage : bs);
   p.prefill_staged = fp8 && p.prefill_ok;
+  p.prefill_padded = shaped && ua::padded_head_dim(d) != d;
   return p;
 }
 
@@ -729,7 +730,8 @@ ua_status ua_plan_create_ex(ua_plan** out, const int32_t* cu_query_lens_host,
       cu_query_lens_host, kv_lens_host, num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
       max_blocks_per_seq, kv_dtype, causal, window, num_splits, 0, decode_rows_max, true);
   const int64_t rows_max = decode_rows_max < 0 ? ua::kDefaultDecodeRowsMax : decode_rows_max;
-  if (!pr.prefill_ok || (*out)->sched.max_q * int64_t{num_q_heads / num_kv_heads} <= rows_max)
+  if (!pr.prefill_ok || (*out)->sched.max_q * int64_t{num_q_heads / num_kv_heads} <= rows_max ||
+      !ua::padded_prefill_pays(pr))
     return UA_OK;
   st = create_plan(&(*out)->shaped, cu_query_lens_host, kv_lens_host, num_seqs, num_q_heads,
                    num_kv_heads, head_dim, block_size, max_blocks_per_seq, kv_dtype, causal,

@@ -370,7 +370,7 @@ def test_prompts_at_the_other_head_dims(shape, d, dtype, hq, hkv, bs):
     decoding sequences; unused slots poisoned."""
     case = W.make_case(f"pad_{shape}_{d}_{dtype}", [200, 1, 131, 2], [257, 300, 600, 40], hq, hkv, d, bs,
                        kv_dtype=dtype, seed=d + 2, poison=True)
-    info = _check(case, **_shape(shape, case))
+    info = _check(case, **_shape(shape, case), decode_rows_max=32)
     assert info.num_prefill_tiles > 0 and info.num_decode_tiles > 0
 
 
@@ -378,7 +378,7 @@ def test_plans_at_the_other_head_dims_switch_with_their_scores():
     """The lists, the settings, the errors and the timing of a plan follow its scores."""
     case = W.make_case("switch", [150, 1], [200, 90], 4, 2, 96, 16, seed=39)
     b = tu.to_device(case)
-    with _plan(b) as never, _plan(b) as plan:
+    with _plan(b, decode_rows_max=32) as never, _plan(b, decode_rows_max=32) as plan:
         want = tu.forward(never, b)
         assert plan.info.num_prefill_tiles == 0
         for _ in range(2):

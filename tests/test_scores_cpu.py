@@ -106,11 +106,17 @@ def test_schedule_reads_no_further_than_rows_see():
 
 @pytest.mark.parametrize("d", [32, 64, 96, 128, 160, 192, 224, 256])
 def test_prompts_with_a_prefix_have_a_prefill_kernel_at_every_head_dim(d):
-    info, pre, dec = _ranges([0, 40, 41], [90, 300], [7, 0], 4, 2, d, 0)
+    info, pre, dec = _ranges([0, 40, 41], [90, 300], [7, 0], 4, 2, d, 0, decode_rows_max=32)
     assert info.num_prefill_tiles > 0 and {t["seq"] for t in dec} == {1}
     # but none where no kernel takes the group size, or the block size
-    assert _ranges([0, 40], [90], [7], 5, 1, d, 0)[0].num_prefill_tiles == 0
-    assert _ranges([0, 40], [90], [7], 4, 2, d, 0, bs=48)[0].num_prefill_tiles == 0
+    assert _ranges([0, 40], [90], [7], 5, 1, d, 0, decode_rows_max=32)[0].num_prefill_tiles == 0
+    assert _ranges([0, 40], [90], [7], 4, 2, d, 0, decode_rows_max=32, bs=48)[0].num_prefill_tiles == 0
+    # by default only where the decode kernel would take longer, at head dims without a kernel of their own
+    own = d in (64, 128, 192, 256)
+    few, many = ([0, 40], [90], [7]), ([0, 900, 1900], [2500, 2500], [7, 7])
+    assert (_ranges(*few, 4, 2, d, 0)[0].num_prefill_tiles > 0) == own
+    assert _ranges(*many, 8, 4, d, 0)[0].num_prefill_tiles > 0
+    assert (_ranges(*many, 8, 4, d, 3)[0].num_prefill_tiles > 0) >= own
 
 
 def test_prefix_refusals():
