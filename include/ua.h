@@ -210,8 +210,9 @@ ua_status ua_plan_create_ex(ua_plan** out, const int32_t* cu_query_lens_host,
  * prefix_lens_host: [num_seqs], each >= 0; a prefix beyond kv_len reaches as
  * far as the keys do (a prompt given in chunks), 0 is the causal mask. The
  * plan keeps its own copy. Sequences that are too long for the decode kernel
- * run in a prefill kernel at every head dim (see ua_plan_set_scores). Other arguments, work and errors
- * as ua_plan_create_ex; UA_ERR_INVALID_ARG for a null or negative prefix too.
+ * run in a prefill kernel at every head dim (see ua_plan_set_scores). Other
+ * arguments, work and errors as ua_plan_create_ex; UA_ERR_INVALID_ARG for a
+ * null or negative prefix too.
  * ua_schedule_prefix -- its scheduler alone, as ua_schedule.
  */
 ua_status ua_plan_create_prefix(ua_plan** out, const int32_t* cu_query_lens_host,

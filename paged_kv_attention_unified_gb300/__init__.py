@@ -162,7 +162,7 @@ def _prefix_array(prefix_lens, num_seqs, causal):
         raise ValueError("a prefix mask is causal: causal must be 1 with prefix_lens")
     if len(lens) != num_seqs:
         raise ValueError(f"prefix_lens has {len(lens)} entries for {num_seqs} sequences")
-    return _i32_array(lens)
+    return _i32_array(min(int(x), 2 ** 31 - 1) for x in lens)  # as good as any longer one
 
 
 def ua_status_string(status: int) -> str:
@@ -285,10 +285,12 @@ def ua_rope_destroy(rope: int):
     _check(lib().ua_rope_destroy(rope), "ua_rope_destroy")
 
 
-def _token_rows(t, name, tokens):
+def _token_rows(t, name, tokens, device):
     """Pointer and row stride of a bf16 [tokens, heads, head_dim] tensor whose
     rows are contiguous (their distance is free)."""
     import torch
+    if t.get_device() != device:
+        raise ValueError(f"{name}: on {t.device}, not on the current CUDA device")
     shape, stride = t.shape, t.stride()
     if len(shape) != 3 or shape[0] != tokens or stride[2] != 1 or stride[1] != shape[2] or (
             t.dtype != torch.bfloat16):
@@ -306,14 +308,18 @@ def ua_rope_append_kv(plan, rope, q, k_new, v_new, q_out, k_cache, v_cache, bloc
     [tokens, heads, head_dim] CUDA tensors whose token rows may be strided."""
     import torch
     n = q.shape[0]
-    qp, qs = _token_rows(q, "q", n)
-    kp, ks = _token_rows(k_new, "k_new", n)
-    vp, vs = _token_rows(v_new, "v_new", n)
-    if not q_out.is_contiguous() or q_out.shape != q.shape or q_out.dtype != q.dtype:
-        raise ValueError("q_out: a contiguous tensor of q's shape and type is needed")
+    dev = torch._C._cuda_getDevice() if q.is_cuda else 0
+    qp, qs = _token_rows(q, "q", n, dev)
+    kp, ks = _token_rows(k_new, "k_new", n, dev)
+    vp, vs = _token_rows(v_new, "v_new", n, dev)
+    if not q_out.is_contiguous() or q_out.shape != q.shape or q_out.dtype != q.dtype or (
+            q_out.get_device() != dev):
+        raise ValueError("q_out: a contiguous tensor of q's shape, type and device is needed")
     if positions is not None and (positions.shape != (n,) or not positions.is_contiguous()
-                                  or positions.dtype != torch.int32):
-        raise ValueError(f"positions: a contiguous int32 tensor of q's {n} tokens is needed")
+                                  or positions.dtype != torch.int32
+                                  or positions.get_device() != dev):
+        raise ValueError(f"positions: a contiguous int32 tensor of q's {n} tokens, on its device, "
+                         "is needed")
     ptr = lambda t: t if isinstance(t, int) else t.data_ptr()
     _check(lib().ua_rope_append_kv(plan, rope, qp, qs, kp, ks, vp, vs, q_out.data_ptr(),
                                    ptr(k_cache), ptr(v_cache), ptr(block_tables),
@@ -485,9 +491,10 @@ class Plan:
 
     _slopes = None  # the forwards read the caller's tensor: kept as long as they may
 
-    def __init__(self, *args, **kwargs):
-        self.handle = ua_plan_create(*args, **kwargs)
-        self.num_q_heads = int(args[2] if len(args) > 2 else kwargs["num_q_heads"])
+    def __init__(self, cu_query_lens, kv_lens, num_q_heads, *args, **kwargs):
+        self.handle = ua_plan_create(cu_query_lens, kv_lens, num_q_heads, *args, **kwargs)
+        self.num_q_heads = int(num_q_heads)
+        self.num_tokens = int(cu_query_lens[-1]) if len(cu_query_lens) else 0
 
     @property
     def info(self) -> ua_plan_info:
@@ -499,10 +506,15 @@ class Plan:
     def append_kv(self, *args, **kwargs):
         ua_append_kv(self.handle, *args, **kwargs)
 
-    def rope_append_kv(self, rope, *args, **kwargs):
-        ua_rope_append_kv(self.handle, getattr(rope, "handle", rope), *args, **kwargs)
+    def rope_append_kv(self, rope, q, *args, **kwargs):
+        if q.shape[0] < self.num_tokens:
+            raise ValueError(f"q: {q.shape[0]} tokens, the plan has {self.num_tokens}")
+        ua_rope_append_kv(self.handle, getattr(rope, "handle", rope), q, *args, **kwargs)
 
     def set_scores(self, softcap=0.0, alibi_slopes=None):
+        """ua_plan_set_scores; the plan holds the tensor until the next call (a
+        graph that captured a forward, or one on a stream of its own, needs it
+        for as long as it runs)."""
         import torch
         if alibi_slopes is not None and (
                 alibi_slopes.shape != (self.num_q_heads,) or not alibi_slopes.is_contiguous()

@@ -888,7 +888,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int D, bool F8, int SHAPE>
 cudaError_t launch_as(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
-                     const PrefillParams& p, cudaStream_t stream) {
+                      const PrefillParams& p, cudaStream_t stream) {
   // The register split above assumes the launch budget; refuse to launch a
   // build whose register count differs (the increase could never be granted).
   static int checked = 0;

@@ -339,3 +339,43 @@ def test_a_cache_behind_2_31_elements():
     assert np.all(np.abs(got - exp) <= 2.0 ** -8 * np.abs(exp) + 2.5e-6 * R.pair_size(as_f64(k), 256, False))
     assert torch.equal(vc[blocks - 1, 198:200], v)
     assert int(kc[:blocks - 1].count_nonzero()) == 0
+
+
+def test_tensors_of_another_device_or_of_fewer_tokens_are_refused():
+    s = Step([4], [20], 4, 2, 64, 16, seed=12)
+    b, out = s.b, torch.empty(4, 4, 64, dtype=torch.bfloat16, device="cuda")
+    args = dict(q=s.q, k_new=s.k, v_new=s.v, q_out=out, k_cache=b.k_cache, v_cache=b.v_cache,
+                block_tables=b.block_tables, num_blocks=b.num_blocks,
+                positions=torch.zeros(4, dtype=torch.int32, device="cuda"))
+    with tu.make_plan(b) as plan, ua.Rope(_freqs(64)) as rope:
+        for name in ("q", "k_new", "v_new", "q_out", "positions"):
+            with pytest.raises(ValueError):
+                plan.rope_append_kv(rope, **{**args, name: args[name].cpu()})
+        short = {k: args[k][:3] for k in ("q", "k_new", "v_new", "q_out", "positions")}
+        with pytest.raises(ValueError):
+            plan.rope_append_kv(rope, **{**args, **short})
+        for got, old in zip(s.caches(), s.before):
+            assert np.array_equal(got, old, equal_nan=True)
+        plan.rope_append_kv(rope, **args)  # and as they were, they are taken
+        assert plan.last_device_error() == 0
+
+
+def test_a_plan_and_an_append_before_torch_has_touched_the_gpu():
+    """The stream is found without torch's CUDA state being set up by anyone."""
+    import subprocess
+    import sys
+    code = """
+import paged_kv_attention_unified_gb300 as ua
+plan = ua.Plan([0, 2], [200], 4, 2, 64, 256, 1)
+import torch
+q = torch.randn(2, 4, 64, dtype=torch.bfloat16, device="cuda")
+kv = torch.randn(2, 2, 64, dtype=torch.bfloat16, device="cuda")
+cache = torch.zeros(2, 1, 256, 2, 64, dtype=torch.bfloat16, device="cuda")
+out = torch.empty_like(q)
+table = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+plan.rope_append_kv(ua.Rope([1.0]), q, kv, kv, out, cache[0], cache[1], table, 1)
+assert torch.equal(cache[1, 0, 198:200], kv) and plan.last_device_error() == 0
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
+                       cwd=__import__("os").path.dirname(__import__("os").path.dirname(__file__)))
+    assert r.returncode == 0, r.stderr

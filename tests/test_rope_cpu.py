@@ -106,6 +106,14 @@ def test_append_without_plan_or_rope_is_refused():
                                           1.0, 1.0, None) == ua.UA_ERR_INVALID_ARG
 
 
+def test_host_tensors_are_refused():
+    import torch
+    q, kv = torch.zeros(2, 4, 64, dtype=torch.bfloat16), torch.zeros(2, 2, 64, dtype=torch.bfloat16)
+    cache, table = torch.zeros(1, 16, 2, 64, dtype=torch.bfloat16), torch.zeros(1, 1, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        ua.ua_rope_append_kv(None, None, q, kv, kv, torch.empty_like(q), cache, cache, table, 1)
+
+
 def _kernel_angle(p, w):
     """The rotation kernel's angle arithmetic in binary32 (fma as binary64
     products of binary32 values, exact there), in turns."""

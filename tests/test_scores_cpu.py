@@ -138,3 +138,9 @@ def test_prefix_refusals():
 
 def test_scores_need_a_plan():
     assert ua.lib().ua_plan_set_scores(None, 0.0, None) == ua.UA_ERR_INVALID_ARG
+
+
+def test_a_prefix_of_any_length_reaches_the_last_key():
+    args = ([0, 40], [90], 4, 2, 64, 16, 6)
+    for far in (90, 2 ** 31 - 1, 2 ** 31 + 5, 2 ** 40):
+        assert ua.ua_schedule(*args, prefix_lens=[far])[1:] == ua.ua_schedule(*args, prefix_lens=[90])[1:]
