@@ -10,8 +10,8 @@
 // Conversion chain: e4m3x2 -> f16x2 (hardware, exact) -> f32 -> bf16x2
 // (exact: no rounding happens for such values). NaN codes stay NaN.
 //
-// One CTA per staging page (the plan's stage tiles): 8 warps, one key row
-// (all KV heads, contiguous in both caches) per warp at a time, 16-byte loads
+// One or eight CTAs per staging page (the plan's stage tiles): 8 warps, one key
+// row (all KV heads, contiguous in both caches) per warp at a time, 16-byte loads
 // (four in flight per lane and cache) before the stores; source pages
 // through the block table; rows past the sequence's length are not written
 // (the prefill kernel masks those keys and zeroes those value rows).
@@ -53,12 +53,14 @@ __device__ __forceinline__ void widen16(uint4 c, uint4& lo, uint4& hi) {
 
 constexpr int kUnroll = 4;  // 16-byte loads per lane in flight per cache
 
-__global__ void __launch_bounds__(kStageWarps * 32) stage_kernel(const StageParams p) {
+__global__ void __launch_bounds__(kStageWarps * 32) stage_kernel(const StageParams p, int parts) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const ua_tile tile = p.tiles[blockIdx.x];
+  const ua_tile tile = p.tiles[blockIdx.x / parts];
+  const int first = tile.kv_lo + blockIdx.x % parts * (kStagePage / parts);
+  const int last = min(tile.kv_hi, first + kStagePage / parts);
   const int chunks = p.row_elems / 16;  // 16 codes per load
   const int32_t* table = p.block_tables + static_cast<int64_t>(tile.seq) * p.max_blocks_per_seq;
-  for (int t = tile.kv_lo + w; t < tile.kv_hi; t += kStageWarps) {
+  for (int t = first + w; t < last; t += kStageWarps) {
     if (t / p.block_size >= p.max_blocks_per_seq) break;
     const int32_t blk = table[t / p.block_size];
     if (blk < 0 || static_cast<int64_t>(blk) >= p.num_blocks) {
@@ -99,10 +101,18 @@ __global__ void __launch_bounds__(kStageWarps * 32) stage_kernel(const StagePara
 
 }  // namespace
 
-cudaError_t launch_stage(const StageParams& p, cudaStream_t stream) {
+cudaError_t launch_stage(const StageParams& p, int sms, cudaStream_t stream) {
   if (p.num_tiles <= 0) return cudaSuccess;
   if (p.row_elems % 16 != 0 || p.tiles == nullptr) return cudaErrorInvalidValue;
-  stage_kernel<<<p.num_tiles, kStageWarps * 32, 0, stream>>>(p);
+  static_assert(kStagePage % (8 * kStageWarps) == 0, "whole rounds of rows per part");
+  // A warp's 16 rows of a page are a chain of table lookups, loads and stores;
+  // eight CTAs to a page leave it two. Measured with one / eight CTAs: 81 pages
+  // of 8 heads of 128 27.3 / 17.9 us, 8 pages 20.6 / 8.0, 649 pages 132.9 /
+  // 90.2; 384 pages of 32 heads 273 / 238. Only rows of several load rounds
+  // with no more pages than SMs stay with one: 128 pages of 32 heads 75.1 / 85.9.
+  const bool wide_rows = p.row_elems / 16 > 32 * kUnroll;
+  const int parts = wide_rows && p.num_tiles <= sms ? 1 : 8;
+  stage_kernel<<<p.num_tiles * parts, kStageWarps * 32, 0, stream>>>(p, parts);
   return cudaGetLastError();
 }
 

@@ -840,7 +840,7 @@ ua_status ua_forward(const ua_plan* plan, const void* q, const void* k_cache,
       sp.row_elems = plan->prob.num_kv_heads * plan->prob.head_dim;
       sp.err = plan->d_err;
       auto* sev = timing_begin(mp, 4, cs);
-      if (ua::launch_stage(sp, cs) != cudaSuccess) return UA_ERR_CUDA;
+      if (ua::launch_stage(sp, plan->info.num_sms, cs) != cudaSuccess) return UA_ERR_CUDA;
       timing_end(sev, cs);
       pk = plan->d_staged_k;
       pv = plan->d_staged_v;

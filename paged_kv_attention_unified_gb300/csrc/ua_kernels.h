@@ -184,7 +184,7 @@ struct StageParams {
   const void* v_src;
   void* k_dst;                   // bf16 staging [pages][128][Hkv][d]
   void* v_dst;
-  const ua_tile* tiles;          // stage tiles of the plan (one CTA each)
+  const ua_tile* tiles;          // stage tiles of the plan
   int32_t num_tiles;
   const int32_t* block_tables;   // device [num_seqs][max_blocks_per_seq]
   int32_t max_blocks_per_seq;
@@ -194,7 +194,7 @@ struct StageParams {
   int32_t* err;                  // error word (UA_ERR_BOUNDS)
 };
 
-cudaError_t launch_stage(const StageParams& p, cudaStream_t stream);
+cudaError_t launch_stage(const StageParams& p, int sms, cudaStream_t stream);
 
 // Test aid: copy the raw K/V rows each tile reads into dense buffers.
 cudaError_t launch_gather_debug(const KernelParams& p, const int64_t* row_offsets, int head_dim,
