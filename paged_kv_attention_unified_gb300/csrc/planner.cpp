@@ -136,6 +136,15 @@ bool padded_prefill_pays(const Problem& p) {
   return decode_ns > (p.head_dim <= 128 ? 30e3 : 55e3);
 }
 
+// Bytes of K and V that the prefill kernel finds in the cache (16-bit; an
+// e4m3 cache's staging copy).
+int64_t prefill_kv_bytes(const Problem& p) {
+  int64_t keys = 0;
+  for (int32_t q = 0; q < p.num_seqs; ++q)
+    if (p.cu_query_lens[q + 1] > p.cu_query_lens[q]) keys += p.kv_lens[q];
+  return keys * p.num_kv_heads * p.head_dim * 4;
+}
+
 ua_status build_schedule(const Problem& p, Schedule* out) {
   ua_status st = validate(p);
   if (st != UA_OK) return st;
@@ -487,8 +496,9 @@ ua_status build_schedule(const Problem& p, Schedule* out) {
 
   // 4. The persistent prefill CTAs take tiles in list order as they free up.
   // The bulk keeps the order above; the shortest tiles, up to
-  // kPrefillTailShare of the work, move to the end, longest first, so that no
-  // CTA starts a long tile while the others run dry.
+  // kPrefillTailShare of the work (all of them: kPrefillLongKeys), move to the
+  // end, longest first, so that no CTA starts a long tile while the others run
+  // dry.
   if (!s.prefill.empty()) {
     const size_t n = s.prefill.size();
     std::vector<int64_t> cost(n, 0);
@@ -504,6 +514,11 @@ ua_status build_schedule(const Problem& p, Schedule* out) {
       }
       total_cost += cost[i];
     }
+    int32_t longest = 0;
+    for (const ua_tile& t : s.prefill) longest = std::max(longest, t.kv_hi - t.kv_lo);
+    const bool by_length = s.decode.empty() && (longest < kPrefillLongKeys ||
+                                                prefill_kv_bytes(p) <= kPrefillResidentBytes);
+    const double tail_share = by_length ? 1.0 : kPrefillTailShare;
     std::vector<SortKey> keys(n);
     for (size_t i = 0; i < n; ++i) keys[i] = {cost[i], 0, 0, static_cast<int32_t>(i)};
     const std::vector<int32_t> by_cost = order_by(keys);
@@ -511,7 +526,7 @@ ua_status build_schedule(const Problem& p, Schedule* out) {
     int64_t tail_cost = 0;
     for (size_t k = 0; k < n; ++k) {
       const size_t i = static_cast<size_t>(by_cost[k]);
-      if (static_cast<double>(tail_cost + cost[i]) > kPrefillTailShare * total_cost) break;
+      if (static_cast<double>(tail_cost + cost[i]) > tail_share * total_cost) break;
       tail_cost += cost[i];
       in_tail[i] = 1;
     }
