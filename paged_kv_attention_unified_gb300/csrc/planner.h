@@ -154,10 +154,10 @@ constexpr double kPrefillTailShare = 1.0 / 16.0;
 // Batches of prompts alone run their tiles longest first throughout when no
 // tile reads kPrefillLongKeys keys, or all K and V stay in L2 whatever the
 // order. Measured, grouped by head / longest first (head_dim 128, 32 heads, 8
-// of them KV): one prompt of 4096 tokens 158 / 131 us, two 274 / 248, 64 of
-// 1000 (262 MB of K and V) 757 / 701, 24 of 2048 (201 MB) 852 / 820; 8 of 4096
-// (134 MB) 950 / 944; but two of 12000 (98 MB) 1815 / 1830 and one of 30000
-// (122 MB) 5431 / 5515; one of 16384 (67 MB) 1664 / 1656.
+// of them KV): one prompt of 4096 tokens 158 / 130 us, two 274 / 247, 64 of
+// 1000 (262 MB of K and V) 757 / 702, 24 of 2048 (201 MB) 852 / 823, four of
+// 4096 (67 MB) 496 / 479; but 16 of 4096 (268 MB) 1915 / 1976, three of 8192
+// (100 MB) 1325 / 1341, one of 30000 (122 MB) 5542 / 5577.
 constexpr int32_t kPrefillLongKeys = 4096;
 constexpr int64_t kPrefillResidentBytes = 70000000;
 
