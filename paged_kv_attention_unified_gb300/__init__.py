@@ -285,20 +285,19 @@ def ua_rope_destroy(rope: int):
     _check(lib().ua_rope_destroy(rope), "ua_rope_destroy")
 
 
-def _token_rows(t, name, tokens, device):
+def _token_rows(t, name, tokens, device, bf16):
     """Pointer and row stride of a bf16 [tokens, heads, head_dim] tensor whose
     rows are contiguous (their distance is free)."""
-    import torch
+    shape, stride = t.shape, t.stride()
     if t.get_device() != device:
         raise ValueError(f"{name}: on {t.device}, not on the current CUDA device")
-    shape, stride = t.shape, t.stride()
     if len(shape) != 3 or shape[0] != tokens or stride[2] != 1 or stride[1] != shape[2] or (
-            t.dtype != torch.bfloat16):
+            t.dtype != bf16):
         raise ValueError(f"{name}: a bf16 [tokens, heads, head_dim] tensor with contiguous rows "
                          f"is needed, of q's {tokens} tokens ({t.dtype}, shape {tuple(shape)}, "
                          f"strides {stride})")
     # with one token (or none) the stride is whatever torch holds: any valid one serves
-    return t.data_ptr(), stride[0] if shape[0] > 1 else shape[1] * shape[2]
+    return t.data_ptr(), stride[0] if tokens > 1 else shape[1] * shape[2]
 
 
 def ua_rope_append_kv(plan, rope, q, k_new, v_new, q_out, k_cache, v_cache, block_tables,
@@ -307,26 +306,29 @@ def ua_rope_append_kv(plan, rope, q, k_new, v_new, q_out, k_cache, v_cache, bloc
     and values into the paged cache, on `stream`. q, k_new and v_new are
     [tokens, heads, head_dim] CUDA tensors whose token rows may be strided."""
     import torch
-    n = q.shape[0]
+    bf16, shape = torch.bfloat16, q.shape
+    n = shape[0]
     dev = torch._C._cuda_getDevice() if q.is_cuda else 0
-    qp, qs = _token_rows(q, "q", n, dev)
-    kp, ks = _token_rows(k_new, "k_new", n, dev)
-    vp, vs = _token_rows(v_new, "v_new", n, dev)
-    if not q_out.is_contiguous() or q_out.shape != q.shape or q_out.dtype != q.dtype or (
-            q_out.get_device() != dev):
+    qp, qs = _token_rows(q, "q", n, dev, bf16)
+    kp, ks = _token_rows(k_new, "k_new", n, dev, bf16)
+    vp, vs = _token_rows(v_new, "v_new", n, dev, bf16)
+    if q_out.shape != shape or q_out.dtype != bf16 or q_out.get_device() != dev or (
+            not q_out.is_contiguous()):
         raise ValueError("q_out: a contiguous tensor of q's shape, type and device is needed")
-    if positions is not None and (positions.shape != (n,) or not positions.is_contiguous()
-                                  or positions.dtype != torch.int32
-                                  or positions.get_device() != dev):
-        raise ValueError(f"positions: a contiguous int32 tensor of q's {n} tokens, on its device, "
-                         "is needed")
-    ptr = lambda t: t if isinstance(t, int) else t.data_ptr()
-    _check(lib().ua_rope_append_kv(plan, rope, qp, qs, kp, ks, vp, vs, q_out.data_ptr(),
-                                   ptr(k_cache), ptr(v_cache), ptr(block_tables),
-                                   int(num_blocks),
-                                   None if positions is None else positions.data_ptr(),
-                                   float(k_scale), float(v_scale), _stream_handle(stream)),
-           "ua_rope_append_kv")
+    pp = None
+    if positions is not None:
+        if positions.shape != (n,) or not positions.is_contiguous() or (
+                positions.dtype != torch.int32 or positions.get_device() != dev):
+            raise ValueError(f"positions: a contiguous int32 tensor of q's {n} tokens, on its "
+                             "device, is needed")
+        pp = positions.data_ptr()
+    _check(lib().ua_rope_append_kv(
+        plan, rope, qp, qs, kp, ks, vp, vs, q_out.data_ptr(),
+        k_cache if isinstance(k_cache, int) else k_cache.data_ptr(),
+        v_cache if isinstance(v_cache, int) else v_cache.data_ptr(),
+        block_tables if isinstance(block_tables, int) else block_tables.data_ptr(),
+        int(num_blocks), pp, float(k_scale), float(v_scale), _stream_handle(stream)),
+        "ua_rope_append_kv")
 
 
 def ua_forward_oneshot(q, k_cache, v_cache, out, cu_query_lens_host, kv_lens_host,
@@ -506,10 +508,13 @@ class Plan:
     def append_kv(self, *args, **kwargs):
         ua_append_kv(self.handle, *args, **kwargs)
 
-    def rope_append_kv(self, rope, q, *args, **kwargs):
-        if q.shape[0] < self.num_tokens:
-            raise ValueError(f"q: {q.shape[0]} tokens, the plan has {self.num_tokens}")
-        ua_rope_append_kv(self.handle, getattr(rope, "handle", rope), q, *args, **kwargs)
+    def rope_append_kv(self, rope, q, k_new, v_new, q_out, k_cache, v_cache, block_tables,
+                       num_blocks, positions=None, k_scale=1.0, v_scale=1.0, stream=None):
+        if len(q) < self.num_tokens:
+            raise ValueError(f"q: {len(q)} tokens, the plan has {self.num_tokens}")
+        ua_rope_append_kv(self.handle, rope.handle if isinstance(rope, Rope) else rope, q, k_new,
+                          v_new, q_out, k_cache, v_cache, block_tables, num_blocks, positions,
+                          k_scale, v_scale, stream)
 
     def set_scores(self, softcap=0.0, alibi_slopes=None):
         """ua_plan_set_scores; the plan holds the tensor until the next call (a
