@@ -118,7 +118,7 @@ typedef struct {
 
 #define UA_MAX_SPLITS 128
 #define UA_DECODE_ROWS 8     /* rows of one decode tile */
-#define UA_PREFILL_ROWS 256  /* rows of one prefill tile: two tcgen05 M=128 query tiles */
+#define UA_PREFILL_ROWS 256  /* most rows of a prefill tile: two tcgen05 M=128 query tiles */
 
 typedef struct {
   int64_t num_prefill_tiles;

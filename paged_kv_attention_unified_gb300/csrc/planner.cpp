@@ -164,6 +164,7 @@ ua_status build_schedule(const Problem& p, Schedule* out) {
   };
   std::vector<DecodeBlock> blocks;
   std::vector<int32_t> span_end;  // per decode sequence: end of its blocks
+  int64_t prefill_rows = UA_PREFILL_ROWS;  // (kPrefillQueryTile)
   {
     int64_t n_blk = 0, n_pre = 0, n_app = 0, n_dseq = 0;
     for (int32_t q = 0; q < p.num_seqs; ++q) {
@@ -176,6 +177,10 @@ ua_status build_schedule(const Problem& p, Schedule* out) {
         n_pre += ceil_div(rows, UA_PREFILL_ROWS) * p.num_kv_heads;
       }
       n_app += ceil_div(ql, kAppendTokens);
+    }
+    if (p.head_dim > 128 || (n_blk == 0 && 2 * n_pre <= num_sms)) {
+      prefill_rows = kPrefillQueryTile;
+      n_pre *= 2;
     }
     blocks.reserve(static_cast<size_t>(n_blk));
     span_end.reserve(static_cast<size_t>(n_dseq));
@@ -203,12 +208,12 @@ ua_status build_schedule(const Problem& p, Schedule* out) {
       continue;
     }
     const size_t first = s.prefill.size();
-    for (int64_t r0 = 0; r0 < rows; r0 += UA_PREFILL_ROWS) {
+    for (int64_t r0 = 0; r0 < rows; r0 += prefill_rows) {
       ua_tile t;
       t.seq = q;
       t.kv_head = 0;
       t.row0 = static_cast<int32_t>(r0);
-      t.nrows = static_cast<int32_t>(std::min<int64_t>(UA_PREFILL_ROWS, rows - r0));
+      t.nrows = static_cast<int32_t>(std::min(prefill_rows, rows - r0));
       key_range(p, q, ctx, kv, t.row0, t.nrows, &t.kv_lo, &t.kv_hi);
       t.kv_lo = static_cast<int32_t>(round_down(t.kv_lo, kPrefillKeyTile));
       t.slot = -1;

@@ -126,7 +126,13 @@ constexpr int kMinSplitTokens = 256;
 constexpr int kDefaultDecodeRowsMax = 32;
 // Key tile of the prefill kernel: its key ranges start on multiples of this.
 constexpr int kPrefillKeyTile = 128;
-// Rows of one tcgen05 query tile of the prefill kernel (two per prefill tile).
+// Rows of one tcgen05 query tile of the prefill kernels. A prefill tile has two
+// up to head_dim 128, where the kernel runs them against one another (32 heads,
+// 8 of them KV, head_dim 128: 800 tokens after 1000 38 us, in tiles of one 51),
+// but for prompts alone that leave half of the SMs without one (512 tokens
+// after 2000: 48 / 41 us). The wide kernel takes query tiles one at a time, so
+// its tiles have one (head_dim 256, two / one: the same 98 / 54 us, 1600 tokens
+// 85 / 66 us, four prompts of 4096 tokens and 32 KV heads 1101 / 1055 us).
 constexpr int kPrefillQueryTile = 128;
 // Head dim of the prefill kernel that takes shaped scores at head_dim d: the
 // next built one, its operands padded with zeros by the TMA copies. (Plain

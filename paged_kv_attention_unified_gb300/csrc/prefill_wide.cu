@@ -8,8 +8,8 @@
 // forward of the "Fused Attention" notes) -- laid out for a wide head D, whose
 // O alone takes D of the 512 TMEM columns and whose Q tile takes D/4 KB of
 // shared memory:
-//   - one query tile of 128 rows per item (the scheduler cuts each 256-row
-//     work tile of the plan into its two query tiles);
+//   - one query tile of 128 rows per item (the plan's work tiles hold one at
+//     these head dims);
 //   - key tiles of 64 keys; S is double-buffered in TMEM (columns 0 and 64),
 //     so the MMA for key tile j+1 runs while the softmax works on tile j,
 //     and O sits in columns 256 .. 256 + D - 1;
@@ -26,6 +26,7 @@
 // MMAs in flight and frees the tensor memory before the CTA exits.
 #include <cuda.h>
 
+#include "planner.h"
 #include "score_shape.cuh"
 #include "sm100.cuh"
 #include "ua_device.cuh"
@@ -38,9 +39,9 @@ using namespace sm100;
 
 namespace wide {
 
-constexpr int kRows = 128;      // query rows per item (TMEM lanes, MMA M)
+constexpr int kRows = kPrefillQueryTile;  // query rows per item (TMEM lanes, MMA M)
+static_assert(kRows == 128);
 constexpr int kKeys = 64;       // keys per key tile (MMA N of S, K of P V)
-constexpr int kPlanRows = 256;  // rows of one work tile of the plan (two items)
 constexpr int kThreads = 256;   // 8 warps
 constexpr int KS = 3;           // K ring stages
 constexpr int VS = 2;           // V ring stages
@@ -122,10 +123,9 @@ __device__ __forceinline__ bool take_item(const PrefillParams& p, const Bars& ba
 }
 
 // ------------------------------------------------------------------ scheduler
-// One thread of warp 3: claims the next work tile of the plan (256 rows) from
-// the shared queue, cuts it into its two 128-row query tiles and publishes
-// them one at a time (each once every role has taken the previous one). Per
-// query tile the key range ends at the last visible key of its last row.
+// One thread of warp 3: claims the next work tile of the plan (one query tile)
+// from the shared queue and publishes it once every role has taken the
+// previous one. The key range ends at the last visible key of its last row.
 __device__ __forceinline__ void scheduler_role(const PrefillParams& p, const Bars& bar,
                                                uint8_t* slot, volatile int32_t* abort) {
   int k = 0;
@@ -149,25 +149,23 @@ __device__ __forceinline__ void scheduler_role(const PrefillParams& p, const Bar
     const int q_start = p.cu_query_lens[tile.seq];
     const int qlen = p.cu_query_lens[tile.seq + 1] - q_start;
     const int kv_len = p.kv_lens[tile.seq];
-    const int nrows = min(tile.nrows, qlen * p.qpk - tile.row0);
+    const int nrows = min(min(tile.nrows, kRows), qlen * p.qpk - tile.row0);
     const int kv_hi = min(min(tile.kv_hi, kv_len), p.max_blocks_per_seq * p.block_size);
-    for (int t = 0; ok && t * kRows < min(nrows, kPlanRows); ++t) {
-      Item it = {};
-      it.seq = tile.seq;
-      it.kv_head = tile.kv_head;
-      it.row0 = tile.row0 + t * kRows;
-      it.rows = min(kRows, nrows - t * kRows);
-      it.q_start = q_start;
-      it.ctx = kv_len - qlen;
-      it.kv_lo = tile.kv_lo;
-      it.kv_hi = kv_hi;
-      const int last = it.row0 + it.rows - 1;
-      it.prefix = p.shape.prefix_lens ? p.shape.prefix_lens[tile.seq] : 0;
-      const int hi =
-          p.causal ? min(kv_hi, max(it.ctx + last / p.qpk + 1, it.prefix)) : kv_hi;
-      it.ntiles = hi > it.kv_lo ? (hi - it.kv_lo + kKeys - 1) / kKeys : 0;
-      if (it.ntiles > 0) ok = publish(it);
-    }
+    if (nrows <= 0) continue;
+    Item it = {};
+    it.seq = tile.seq;
+    it.kv_head = tile.kv_head;
+    it.row0 = tile.row0;
+    it.rows = nrows;
+    it.q_start = q_start;
+    it.ctx = kv_len - qlen;
+    it.kv_lo = tile.kv_lo;
+    it.kv_hi = kv_hi;
+    const int last = it.row0 + it.rows - 1;
+    it.prefix = p.shape.prefix_lens ? p.shape.prefix_lens[tile.seq] : 0;
+    const int hi = p.causal ? min(kv_hi, max(it.ctx + last / p.qpk + 1, it.prefix)) : kv_hi;
+    it.ntiles = hi > it.kv_lo ? (hi - it.kv_lo + kKeys - 1) / kKeys : 0;
+    if (it.ntiles > 0) ok = publish(it);
   }
   if (!ok) give_up(p, abort);
   __threadfence();

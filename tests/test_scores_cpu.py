@@ -94,10 +94,12 @@ def test_schedule_covers_every_key_a_row_sees(seed):
 
 
 def test_schedule_reads_no_further_than_rows_see():
-    # 300 tokens, prefix 200: tiles of 64 tokens (qpk 4) end at the prefix or at their last row
+    # 300 tokens, prefix 200: tiles of whole tokens (qpk 4) end at the prefix or at their last row
     _, pre, _ = _ranges([0, 300], [300], [200], 4, 1, 128, 0)
-    assert sorted({(t["row0"], t["kv_hi"]) for t in pre}) == [
-        (0, 200), (256, 200), (512, 200), (768, 256), (1024, 300)]
+    assert sorted(r for t in pre for r in range(t["row0"], t["row0"] + t["nrows"])) == list(range(1200))
+    for t in pre:
+        assert (t["kv_lo"], t["kv_hi"]) == (0, max(200, (t["row0"] + t["nrows"] - 1) // 4 + 1))
+    assert {t["kv_hi"] for t in pre} > {200, 300}
     # prefix 0 is the causal schedule
     for f in ("kv_lo", "kv_hi", "row0"):
         a = [t[f] for t in ua.ua_schedule([0, 300], [300], 4, 1, 128, 16, 20, prefix_lens=[0])[1]]
@@ -144,3 +146,16 @@ def test_a_prefix_of_any_length_reaches_the_last_key():
     args = ([0, 40], [90], 4, 2, 64, 16, 6)
     for far in (90, 2 ** 31 - 1, 2 ** 31 + 5, 2 ** 40):
         assert ua.ua_schedule(*args, prefix_lens=[far])[1:] == ua.ua_schedule(*args, prefix_lens=[90])[1:]
+
+
+@pytest.mark.parametrize("d", [64, 128, 160, 192, 256])
+def test_prefill_tiles_have_one_query_tile_where_that_fills_more_sms(d):
+    """One query tile (128 rows) at the wide head dims, and for prompts alone
+    that leave half of the SMs without a tile of two; two otherwise."""
+    def rows(cu, kv):
+        bounds = [cu, kv, 32, 8, d, 16, 700]
+        pre = ua.ua_schedule(*bounds, prefix_lens=[0] * len(kv))[1]
+        return max(t["nrows"] for t in pre)
+    assert rows([0, 576], [576]) == 128                     # 9 tiles of 256 rows a head, 72 in all
+    assert rows([0, 600], [600]) == (128 if d > 128 else 256)   # 80 of 152
+    assert rows([0, 576, 577], [576, 10000]) == (128 if d > 128 else 256)  # a decode step beside it
