@@ -132,8 +132,7 @@ bool padded_prefill_pays(const Problem& p) {
     if (p.window > 0) keys = std::min<int64_t>(keys, static_cast<int64_t>(p.window) + ql);
     tile_keys += static_cast<double>(ceil_div(ql * qpk, UA_DECODE_ROWS) * p.num_kv_heads * keys);
   }
-  const double decode_ns = tile_keys / std::min(31.0, 1900.0 / p.head_dim);
-  return decode_ns > (p.head_dim <= 128 ? 30e3 : 55e3);
+  return tile_keys / std::min(31.0, 1900.0 / p.head_dim) > 22e3;
 }
 
 // Bytes of K and V that the prefill kernel finds in the cache (16-bit; an

@@ -140,15 +140,15 @@ constexpr int kPrefillQueryTile = 128;
 constexpr int padded_head_dim(int d) {
   return d <= 64 ? 64 : (d <= 128 ? 128 : (d <= 192 ? 192 : 256));
 }
-// Whether a padded problem's long sequences go to that kernel: when the decode
-// kernel would take longer for them than the other's latency. It passes about
-// 1900 / d (at most 31) keys of an 8-row tile per ns over the whole GPU; the
-// prefill kernels need about 30 us (d <= 128) or 55 us (staging, conversions
-// and two 128-row tiles one after the other) for 1000 keys however few rows
-// there are. Measured at 1000 to 1500 keys (decode / prefill): head_dim 96, 16
-// sequences of 48 rows and 8 KV heads 75 / 43 us, 4 of 96 rows 29 / 31 us, one
-// of 800 rows and 2 KV heads 25 / 42 us; head_dim 224, 4 of 144 rows 104 / 72
-// us, one of 800 rows 46 / 80 us. (decode_rows_max >= 0 decides by itself.)
+// Whether a padded problem's long sequences go to that kernel: not while the
+// decode kernel, which passes about 1900 / d (at most 31) keys of an 8-row tile
+// per ns over the whole GPU, needs no more than 22 us for them (and some 10 us
+// to start); a prefill kernel takes 30 to 40 us for 1000 keys however few rows
+// there are. Measured at 1000 to 1500 keys (decode / prefill): head_dim 96, 4
+// sequences of 96 rows and 8 KV heads (20 us by that rate) 29 / 31 us, of 144
+// rows (30) 42 / 34, one of 800 rows and 2 KV heads (12) 25 / 37; head_dim 160,
+// the same 46 / 35, 58 / 38 and 31 / 40 us; head_dim 224, 4 of 48 rows (23) 44
+// / 38, one of 400 rows (13) 29 / 44. (decode_rows_max >= 0 decides by itself.)
 bool padded_prefill_pays(const Problem& p);
 // Slots per page of the bf16 staging cache of fp8 prefills.
 constexpr int kStagePage = 128;

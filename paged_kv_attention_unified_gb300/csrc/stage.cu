@@ -10,7 +10,7 @@
 // Conversion chain: e4m3x2 -> f16x2 (hardware, exact) -> f32 -> bf16x2
 // (exact: no rounding happens for such values). NaN codes stay NaN.
 //
-// One or eight CTAs per staging page (the plan's stage tiles): 8 warps, one key
+// One to sixteen CTAs per staging page (the plan's stage tiles): 8 warps, one key
 // row (all KV heads, contiguous in both caches) per warp at a time, 16-byte loads
 // (four in flight per lane and cache) before the stores; source pages
 // through the block table; rows past the sequence's length are not written
@@ -104,14 +104,17 @@ __global__ void __launch_bounds__(kStageWarps * 32) stage_kernel(const StagePara
 cudaError_t launch_stage(const StageParams& p, int sms, cudaStream_t stream) {
   if (p.num_tiles <= 0) return cudaSuccess;
   if (p.row_elems % 16 != 0 || p.tiles == nullptr) return cudaErrorInvalidValue;
-  static_assert(kStagePage % (8 * kStageWarps) == 0, "whole rounds of rows per part");
+  static_assert(kStagePage == 16 * kStageWarps, "a row per warp with sixteen CTAs to a page");
   // A warp's 16 rows of a page are a chain of table lookups, loads and stores;
-  // eight CTAs to a page leave it two. Measured with one / eight CTAs: 81 pages
-  // of 8 heads of 128 27.3 / 17.9 us, 8 pages 20.6 / 8.0, 649 pages 132.9 /
-  // 90.2; 384 pages of 32 heads 273 / 238. Only rows of several load rounds
-  // with no more pages than SMs stay with one: 128 pages of 32 heads 75.1 / 85.9.
+  // eight CTAs to a page leave it two, sixteen one. Measured with one / eight /
+  // sixteen: 8 heads of 128, 8 pages 20.6 / 8.0 / 6.8 us, 81 pages 27.3 / 17.9 /
+  // 17.8, 649 pages 132.9 / 90.2 / 96.0; 32 heads, 16 pages 71 / 17 / 16, 64
+  // pages 66 / 49 / 46, 192 pages 157 / 124 / 119. Only with wide rows (several
+  // load rounds each) and pages for most of the SMs is one CTA to a page the
+  // faster: 128 pages of 32 heads 75 / 86 / 83, of 24 heads 61 / 65 / 64.
   const bool wide_rows = p.row_elems / 16 > 32 * kUnroll;
-  const int parts = wide_rows && p.num_tiles <= sms ? 1 : 8;
+  const bool fills = 3 * p.num_tiles > 2 * sms && p.num_tiles <= sms;
+  const int parts = !wide_rows ? 8 : (fills ? 1 : 16);
   stage_kernel<<<p.num_tiles * parts, kStageWarps * 32, 0, stream>>>(p, parts);
   return cudaGetLastError();
 }
