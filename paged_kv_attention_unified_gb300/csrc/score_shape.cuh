@@ -86,14 +86,14 @@ __device__ __forceinline__ float row_max(const float (&x)[N]) {
 // softmax warps run out of the instruction cache. Capped dense causal prefill,
 // 4 x 4096 tokens, 32 heads of 128: unrolled with ex2 and reciprocal 881 us,
 // unrolled with the polynomial 728 us, in loops over 16, 32 and 64 columns 671,
-// 643 and 723 us; 597 us with the maximum left out where no score can move the
+// 643 and 723 us; 600 us with the maximum left out where no score can move the
 // reference and masks taken as bits. Without a cap: 505 us, the plain kernel;
 // with a distance bias 566 us (691 when every rise towards the row moved the
 // reference), with both 779 us.
 // KEYS 64 (the wide kernel, one query tile at a time, its products issued at
-// N = 64): unrolled, held in registers (head_dim 256 on the same batch 1211
-// us, in loops 1397 us, with a row shared by two threads 1300 us; uncapped
-// 1110 us).
+// N = 64): unrolled, held in registers (head_dim 256 on the same batch 1206
+// us; when it was 1211, in loops 1397 us and with a row shared by two threads
+// 1300 us; uncapped 1067 us).
 template <int SHAPE, bool F8, int KEYS>
 struct RowSoftmax {
   static constexpr bool kCap = (SHAPE & kShapeCap) != 0, kBias = (SHAPE & kShapeBias) != 0;

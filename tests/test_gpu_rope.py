@@ -379,3 +379,21 @@ assert torch.equal(cache[1, 0, 198:200], kv) and plan.last_device_error() == 0
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
                        cwd=__import__("os").path.dirname(__import__("os").path.dirname(__file__)))
     assert r.returncode == 0, r.stderr
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("rot,d", [(2, 32), (36, 64), (90, 96), (64, 96), (102, 224)])
+def test_infinities_stay_in_their_pair_and_zeros_keep_their_sign(rot, d, interleaved):
+    s = Step([3, 9], [3, 40], 6, 2, d, 16, seed=13)
+    q = s.q.clone()
+    q[:, :, rot:] = torch.tensor([-0.0, 0.0, 1.5, -float("inf")], device="cuda").repeat(d)[:d - rot].bfloat16()
+    pair = min(3, rot // 2 - 1)
+    a, b = (2 * pair, 2 * pair + 1) if interleaved else (pair, pair + rot // 2)
+    q[::2, :, b] = float("inf")
+    s.q = q
+    with tu.make_plan(s.b) as plan, ua.Rope(_freqs(rot), interleaved) as rope:
+        out = s.run(plan, rope)
+    assert torch.equal(out[:, :, rot:].contiguous().view(torch.int16), q[:, :, rot:].contiguous().view(torch.int16))
+    rest = [e for e in range(rot) if e not in (a, b)]
+    assert torch.isfinite(out[:, :, rest].float()).all()
+    assert not torch.isfinite(out[::2, :, [a, b]].float()).all(-1).any()
