@@ -401,3 +401,50 @@ def test_plans_at_the_other_head_dims_switch_with_their_scores():
         tu.forward(plan, b)
         assert plan.last_device_error() == ua.UA_ERR_BOUNDS
         assert plan.last_device_error() == 0
+
+
+@pytest.mark.parametrize("hkv,d,ql,kv", [
+    (20, 128, [70, 40], [300, 90]),      # rows of several load rounds, few pages: sixteen blocks each
+    (40, 64, [60] * 20, [700] * 20),     # the same, 120 pages: one block each
+    (1, 64, [300, 50], [301, 1000])])    # rows of four lanes
+def test_staging_of_e4m3_pages(hkv, d, ql, kv):
+    """Prompts over an e4m3 cache at every way of sharing a staging page between blocks; pages and
+    sequences end inside them, unused slots are poisoned."""
+    case = W.make_case(f"stage_{hkv}_{d}", ql, kv, hkv, hkv, d, 32, kv_dtype=W.FP8, seed=40, poison=True)
+    info = _check(case, cap=20.0, decode_rows_max=0)
+    assert info.num_prefill_tiles > 0
+    b = tu.to_device(case)
+    b.block_tables[0, 1] = -3
+    with _plan(b, cap=20.0, decode_rows_max=0) as plan:
+        tu.forward(plan, b)
+        assert plan.last_device_error() == ua.UA_ERR_BOUNDS
+
+
+@pytest.mark.parametrize("d,dtype", [(96, W.BF16), (160, W.FP8)])
+def test_captured_shaped_and_plain_forwards_of_one_plan(d, dtype):
+    """Graphs of a plan's plain and shaped forwards, replayed in turn: each keeps the scores, lists
+    and workspace it was captured with."""
+    case = W.make_case(f"cap_{d}", [150, 1, 33], [200, 900, 64], 4, 2, d, 16, kv_dtype=dtype, seed=41)
+    b = tu.to_device(case)
+    slopes = torch.tensor(_slopes(4), device="cuda")
+    with _plan(b, decode_rows_max=32) as plan:
+        graphs, outs = [], []
+        for cap, sl in ((0.0, None), (9.0, None), (9.0, slopes)):
+            plan.set_scores(cap, sl)
+            out = torch.empty_like(b.q)
+            tu.forward(plan, b, out)
+            torch.cuda.synchronize()
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                tu.forward(plan, b, out, stream=torch.cuda.current_stream())
+            graphs.append(g)
+            outs.append(out)
+        plan.set_scores()
+        for i in (2, 0, 1, 2, 1, 0):
+            outs[i].fill_(float("nan"))
+            graphs[i].replay()
+        torch.cuda.synchronize()
+        assert plan.last_device_error() == 0
+    for out, (cap, sl) in zip(outs, ((0.0, None), (9.0, None), (9.0, _slopes(4)))):
+        exp, spread = _expected(case, cap=cap, slopes=sl)
+        assert np.all(np.abs(as_f64(out) - exp) <= _bound(case, exp, spread))
