@@ -416,8 +416,9 @@ ua_status ua_rope_destroy(ua_rope* rope);
  *   cache.) They only enter the angle; any value is allowed. The angle's
  *   error stays below 2^-22 of a turn for |position| up to 2^24.
  * k_cache, v_cache, block_tables, num_blocks, k_scale, v_scale: as for
- *   ua_append_kv. The rotated key is rounded once: to bf16, or as
- *   e4m3(k' / k_scale) from the binary32 value.
+ *   ua_append_kv, but the scales of an e4m3 cache are normal numbers. The
+ *   rotated key is rounded once: to bf16, or as e4m3(k' / k_scale) from the
+ *   binary32 value (the quotient within 2^-20 more than half an ulp).
  * A token whose page id is outside [0, num_blocks) (or whose position lies
  * past the page table) is not written to the cache and UA_ERR_BOUNDS is
  * recorded in the plan's error word; its query is still rotated.

@@ -8,8 +8,8 @@
 // for i < rotary_dim / 2, where the pair is (x[i], x[i + rotary_dim / 2])
 // (half layout) or (x[2i], x[2i + 1]) (interleaved); elements from rotary_dim
 // on pass unchanged. Rotation in binary32, one rounding at the end: bf16 for
-// q and a bf16 cache, e4m3(x / scale) with the quotient in binary32 for an
-// e4m3 cache.
+// q and a bf16 cache, e4m3(x / scale) from a binary32 quotient for an e4m3
+// cache.
 //
 // Angles. p w_i grows to many turns (131072 radians for the first pair of a
 // long context), where a binary32 product has lost the angle's fraction. The
@@ -41,6 +41,7 @@
 // division of the index per element; with 2, 4, 6 and 8 heads in flight
 // instead of 3 151, 147, 140 and 138 us, but chunks of 3850 tokens and 32
 // heads 14.1, 16.8, 17.4 and 16.5 instead of 14.1).
+#include <cmath>
 #include <cstdint>
 
 #include "planner.h"
@@ -97,11 +98,29 @@ __device__ __forceinline__ uint4 narrow8(const float (&x)[8]) {
   return make_uint4(pack2<false>(x[0], x[1]), pack2<false>(x[2], x[3]), pack2<false>(x[4], x[5]),
                     pack2<false>(x[6], x[7]));
 }
-__device__ __forceinline__ uint2 quantize8(const float (&x)[8], float scale) {
-  return make_uint2(to_e4m3x4(__fdiv_rn(x[0], scale), __fdiv_rn(x[1], scale),
-                              __fdiv_rn(x[2], scale), __fdiv_rn(x[3], scale)),
-                    to_e4m3x4(__fdiv_rn(x[4], scale), __fdiv_rn(x[5], scale),
-                              __fdiv_rn(x[6], scale), __fdiv_rn(x[7], scale)));
+// An e4m3 cache's scale = mant / shift, |mant| in [1, 2), shift a power of two.
+struct RopeScale {
+  float shift, mant, inv;  // inv = 1 / mant
+};
+
+// x / scale for rounding to e4m3: the product with the rounded reciprocal, off
+// by two ulp at most, corrected by its remainder (as in P. Markstein, "Computation of elementary functions on the
+// IBM RISC System/6000 processor", 1990), which leaves half an ulp of binary32
+// and 2^-20 ulp more. Clamped at 1024, beyond which e4m3 saturates, so that the
+// remainder of an overflow stays a number; a zero keeps its sign. A true
+// division per element took prompts of 4 x 4096 tokens with an e4m3 cache 183
+// us, this 138 us.
+__device__ __forceinline__ float quotient(float x, const RopeScale& s) {
+  const float y = x * s.shift;
+  const float q0 = y * s.inv;
+  const float q = fminf(fmaxf(q0, -1024.f), 1024.f);
+  return copysignf(fmaf(fmaf(-q, s.mant, y), s.inv, q), q0);
+}
+__device__ __forceinline__ uint2 quantize8(const float (&x)[8], const RopeScale& s) {
+  float q[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) q[i] = quotient(x[i], s);
+  return make_uint2(to_e4m3x4(q[0], q[1], q[2], q[3]), to_e4m3x4(q[4], q[5], q[6], q[7]));
 }
 
 // How a lane's two chunks hold its pairs.
@@ -117,7 +136,8 @@ constexpr int kUnitWords = 9;
 
 template <bool FP8, Layout LAYOUT>
 __global__ void __launch_bounds__(kThreads)
-    rope_append_kernel(const __grid_constant__ RopeTable rope, const RopeAppendParams p) {
+    rope_append_kernel(const __grid_constant__ RopeTable rope, const RopeAppendParams p,
+                       const RopeScale k_scale, const RopeScale v_scale) {
   constexpr int kUnroll = LAYOUT == kHalfOdd ? 3 : 8;  // heads per lane with loads in flight
   constexpr int kTurns = LAYOUT == kHalfOdd ? 16 : 8;  // (cos, sin) a lane holds
   __shared__ float2 turn[kWarps][kMaxPairs];
@@ -275,7 +295,7 @@ __global__ void __launch_bounds__(kThreads)
         const int64_t at = (cache_row + h - (is_v ? first_v : first_k)) * d;
         void* cache = is_v ? p.v_cache : p.k_cache;
         if constexpr (FP8) {
-          const float scale = is_v ? p.v_scale : p.k_scale;
+          const RopeScale scale = is_v ? v_scale : k_scale;
           uint8_t* dst = static_cast<uint8_t*>(cache) + at;
           const uint2 lo = quantize8(x0, scale), hi = quantize8(x1, scale);
           if (o1 == o0 + 8) {
@@ -296,14 +316,22 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
+RopeScale split_scale(float scale) {
+  int e = 0;
+  const float mant = 2.f * std::frexp(scale, &e);
+  return {std::ldexp(1.f, 1 - e), mant, 1.f / mant};
+}
+
 template <bool FP8>
 cudaError_t launch(const RopeTable& rope, const RopeAppendParams& p, cudaStream_t stream) {
+  const RopeScale ks = split_scale(p.k_scale), vs = split_scale(p.v_scale);
+  const int grid = p.num_tiles * kParts;
   if (p.interleaved)
-    rope_append_kernel<FP8, kInterleaved><<<p.num_tiles * kParts, kThreads, 0, stream>>>(rope, p);
+    rope_append_kernel<FP8, kInterleaved><<<grid, kThreads, 0, stream>>>(rope, p, ks, vs);
   else if (p.rotary_dim % 16 == 0)
-    rope_append_kernel<FP8, kHalf><<<p.num_tiles * kParts, kThreads, 0, stream>>>(rope, p);
+    rope_append_kernel<FP8, kHalf><<<grid, kThreads, 0, stream>>>(rope, p, ks, vs);
   else
-    rope_append_kernel<FP8, kHalfOdd><<<p.num_tiles * kParts, kThreads, 0, stream>>>(rope, p);
+    rope_append_kernel<FP8, kHalfOdd><<<grid, kThreads, 0, stream>>>(rope, p, ks, vs);
   return cudaGetLastError();
 }
 

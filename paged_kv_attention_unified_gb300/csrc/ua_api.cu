@@ -1079,9 +1079,7 @@ ua_status ua_rope_append_kv(const ua_plan* plan, const ua_rope* rope, const void
   if (!apart(k_new, k_stride, kv_row) || !apart(v_new, v_stride, kv_row)) return UA_ERR_INVALID_ARG;
   if (num_blocks <= 0 || num_blocks >= INT32_MAX) return UA_ERR_INVALID_ARG;
   const bool fp8 = pr.kv_dtype == UA_KV_FP8_E4M3;
-  if (fp8 && (!std::isfinite(k_scale) || !std::isfinite(v_scale) || k_scale == 0.f ||
-              v_scale == 0.f))
-    return UA_ERR_INVALID_ARG;
+  if (fp8 && (!std::isnormal(k_scale) || !std::isnormal(v_scale))) return UA_ERR_INVALID_ARG;
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess) return UA_ERR_CUDA;
   if (dev != plan->device) return UA_ERR_INVALID_ARG;

@@ -397,3 +397,39 @@ def test_infinities_stay_in_their_pair_and_zeros_keep_their_sign(rot, d, interle
     rest = [e for e in range(rot) if e not in (a, b)]
     assert torch.isfinite(out[:, :, rest].float()).all()
     assert not torch.isfinite(out[::2, :, [a, b]].float()).all(-1).any()
+
+
+@pytest.mark.parametrize("k_scale,v_scale", [
+    (1.0, 0.015), (0.0071, 3.3), (448.0, -0.37), (2.0 ** -126, 2.0 ** 127), (1.9999999, 2.0 ** -20),
+    (3e38, 1.2e-38), (1.0000001, 7e-5)])
+def test_e4m3_codes_of_every_bf16_value_are_those_of_the_plain_append(k_scale, v_scale):
+    """Values that pass unrotated: every bf16 number, infinities and NaN too."""
+    n = 512
+    values = torch.arange(-2 ** 15, 2 ** 15, dtype=torch.int32).to(torch.int16).view(torch.bfloat16).cuda()
+    rows = values.view(n, 2, 64)
+    keys = torch.zeros(n, 2, 64, dtype=torch.bfloat16, device="cuda")
+    keys[:, :, 2:] = rows[:, :, 2:]                        # the first two elements turn
+    q = torch.zeros(n, 2, 64, dtype=torch.bfloat16, device="cuda")
+    table = torch.arange(4, dtype=torch.int32, device="cuda").view(1, 4)
+    caches = torch.zeros(4, 4, 128, 2, 64, dtype=torch.uint8, device="cuda")
+    with ua.Plan([0, n], [n], 2, 2, 64, 128, 4, kv_dtype=ua.UA_KV_FP8_E4M3) as plan, \
+            ua.Rope([0.5], interleaved=True) as rope:
+        plan.rope_append_kv(rope, q, keys, rows, torch.empty_like(q), caches[0], caches[1], table, 4,
+                            k_scale=k_scale, v_scale=v_scale)
+        plan.append_kv(keys, rows, caches[2], caches[3], table, 4, k_scale, v_scale)
+        assert plan.last_device_error() == 0
+    assert torch.equal(caches[1], caches[3])
+    assert torch.equal(caches[0][..., 2:], caches[2][..., 2:])
+    assert not (caches[0][..., :2] & 127).any()  # a turned zero is a zero of either sign
+
+
+@pytest.mark.parametrize("scale", [0.0, float("inf"), float("nan"), 1e-39])
+def test_scales_that_are_not_normal_numbers_are_refused(scale):
+    s = Step([4], [20], 4, 2, 64, 16, W.FP8, seed=14)
+    for name in ("k_scale", "v_scale"):
+        s.b.k_scale, s.b.v_scale = 1.0, 1.0
+        setattr(s.b, name, scale)
+        with tu.make_plan(s.b) as plan, ua.Rope(_freqs(64)) as rope:
+            with pytest.raises(ua.UAError) as e:
+                s.run(plan, rope)
+            assert e.value.status == ua.UA_ERR_INVALID_ARG
