@@ -45,6 +45,7 @@
 #include <cstdint>
 
 #include "planner.h"
+#include "sm100.cuh"
 #include "ua_device.cuh"
 #include "ua_kernels.h"
 
@@ -103,23 +104,29 @@ struct RopeScale {
   float shift, mant, inv;  // inv = 1 / mant
 };
 
-// x / scale for rounding to e4m3: the product with the rounded reciprocal, off
+// x / scale of two values for rounding to e4m3: the product with the rounded reciprocal, off
 // by two ulp at most, corrected by its remainder (as in P. Markstein, "Computation of elementary functions on the
 // IBM RISC System/6000 processor", 1990), which leaves half an ulp of binary32
 // and 2^-20 ulp more. Clamped at 1024, beyond which e4m3 saturates, so that the
 // remainder of an overflow stays a number; a zero keeps its sign. A true
 // division per element took prompts of 4 x 4096 tokens with an e4m3 cache 183
-// us, this 138 us.
-__device__ __forceinline__ float quotient(float x, const RopeScale& s) {
-  const float y = x * s.shift;
-  const float q0 = y * s.inv;
-  const float q = fminf(fmaxf(q0, -1024.f), 1024.f);
-  return copysignf(fmaf(fmaf(-q, s.mant, y), s.inv, q), q0);
+// us, this 129 us (138 without the paired arithmetic).
+__device__ __forceinline__ void quotients(float x0, float x1, const RopeScale& s, float& q0,
+                                          float& q1) {
+  using namespace sm100;
+  const uint64_t inv = f2_pack(s.inv, s.inv);
+  const uint64_t y = f2_mul(f2_pack(x0, x1), f2_pack(s.shift, s.shift));
+  float a0, a1;
+  f2_unpack(f2_mul(y, inv), a0, a1);
+  const uint64_t q = f2_pack(fminf(fmaxf(a0, -1024.f), 1024.f), fminf(fmaxf(a1, -1024.f), 1024.f));
+  f2_unpack(f2_fma(f2_fma(q, f2_pack(-s.mant, -s.mant), y), inv, q), q0, q1);
+  q0 = copysignf(q0, a0);
+  q1 = copysignf(q1, a1);
 }
 __device__ __forceinline__ uint2 quantize8(const float (&x)[8], const RopeScale& s) {
   float q[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) q[i] = quotient(x[i], s);
+  for (int i = 0; i < 8; i += 2) quotients(x[i], x[i + 1], s, q[i], q[i + 1]);
   return make_uint2(to_e4m3x4(q[0], q[1], q[2], q[3]), to_e4m3x4(q[4], q[5], q[6], q[7]));
 }
 
