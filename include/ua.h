@@ -438,6 +438,11 @@ ua_status ua_rope_append_kv(const ua_plan* plan, const ua_rope* rope, const void
 /* Counts and sizes of a plan (host memory only). */
 ua_status ua_plan_get_info(const ua_plan* plan, ua_plan_info* info);
 
+/* The batch a plan was made for (host memory only): its query tokens, heads
+ * and head_dim, which the tensors of its calls have to have. */
+ua_status ua_plan_get_batch(const ua_plan* plan, int64_t* total_q, int32_t* num_q_heads,
+                            int32_t* num_kv_heads, int32_t* head_dim);
+
 /* Kernel timing for measurement tools. While enabled, ua_forward and
  * ua_append_kv record a CUDA event pair on their stream around each kernel
  * launch (a few microseconds per launch). The exception is a batch with both

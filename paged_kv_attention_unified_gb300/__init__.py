@@ -45,7 +45,7 @@ EXPORTS = (
     "ua_forward_static_scratch", "ua_plan_set_debug", "ua_append_kv",
     "ua_plan_set_unified_max", "ua_plan_set_prefill_ctas", "ua_plan_set_fp8_products", "ua_forward_host",
     "ua_rope_frequencies", "ua_rope_create", "ua_rope_destroy", "ua_rope_append_kv",
-    "ua_plan_set_scores", "ua_plan_create_prefix", "ua_schedule_prefix",
+    "ua_plan_set_scores", "ua_plan_create_prefix", "ua_schedule_prefix", "ua_plan_get_batch",
 )
 
 
@@ -113,6 +113,7 @@ _SIGS = {
                                   ctypes.POINTER(ua_tile), _I64, ctypes.POINTER(ua_tile), _I64,
                                   ctypes.POINTER(ua_combine_group), _I64]),
     "ua_plan_get_info": (_I32, [_P, ctypes.POINTER(ua_plan_info)]),
+    "ua_plan_get_batch": (_I32, [_P, ctypes.POINTER(_I64), _I32P, _I32P, _I32P]),
     "ua_last_device_error": (_I32, [_P, _I32P]),
     "ua_plan_destroy": (_I32, [_P]),
     "ua_gather_kv_debug": (_I32, [_P, _P, _P, _P, _P, _I64, _P, _P, _I64, _P]),
@@ -304,7 +305,15 @@ def ua_rope_append_kv(plan, rope, q, k_new, v_new, q_out, k_cache, v_cache, bloc
                       num_blocks, positions=None, k_scale=1.0, v_scale=1.0, stream=None):
     """Rotate the step's q into q_out (q itself: in place), and its new keys
     and values into the paged cache, on `stream`. q, k_new and v_new are
-    [tokens, heads, head_dim] CUDA tensors whose token rows may be strided."""
+    [tokens, heads, head_dim] CUDA tensors of the plan's heads and at least its
+    tokens, whose token rows may be strided."""
+    _rope_append(plan, None, rope, q, k_new, v_new, q_out, k_cache, v_cache, block_tables,
+                 num_blocks, positions, k_scale, v_scale, stream)
+
+
+def _rope_append(plan, batch, rope, q, k_new, v_new, q_out, k_cache, v_cache, block_tables,
+                 num_blocks, positions, k_scale, v_scale, stream):
+    """batch: the plan's (tokens, query heads, KV heads, head_dim), None to ask it."""
     import torch
     bf16, shape = torch.bfloat16, q.shape
     n = shape[0]
@@ -322,6 +331,13 @@ def ua_rope_append_kv(plan, rope, q, k_new, v_new, q_out, k_cache, v_cache, bloc
             raise ValueError(f"positions: a contiguous int32 tensor of q's {n} tokens, on its "
                              "device, is needed")
         pp = positions.data_ptr()
+    # The row distances do not show the library how many heads there are: rows
+    # inside a fused projection are as wide as any plan's.
+    tokens, hq, hkv, d = ua_plan_get_batch(plan) if batch is None else batch
+    if n < tokens or shape != (n, hq, d) or k_new.shape != (n, hkv, d) or v_new.shape != (n, hkv, d):
+        raise UAError(UA_ERR_INVALID_ARG, f"ua_rope_append_kv: q {tuple(shape)}, k_new "
+                      f"{tuple(k_new.shape)}, v_new {tuple(v_new.shape)} on a plan of {tokens} "
+                      f"tokens, {hq} query heads, {hkv} KV heads and head_dim {d}")
     _check(lib().ua_rope_append_kv(
         plan, rope, qp, qs, kp, ks, vp, vs, q_out.data_ptr(),
         k_cache if isinstance(k_cache, int) else k_cache.data_ptr(),
@@ -366,6 +382,14 @@ def ua_forward_host(q_host, out_host, cu_query_lens_host, kv_lens_host, block_ta
         k_scale, v_scale, num_splits, ctypes.byref(err), _stream_handle(stream)),
         "ua_forward_host")
     return err.value
+
+
+def ua_plan_get_batch(plan: int):
+    """(query tokens, query heads, KV heads, head_dim) of a plan."""
+    n, hq, hkv, d = (ctypes.c_int64(), ctypes.c_int32(), ctypes.c_int32(), ctypes.c_int32())
+    _check(lib().ua_plan_get_batch(plan, ctypes.byref(n), ctypes.byref(hq), ctypes.byref(hkv),
+                                   ctypes.byref(d)), "ua_plan_get_batch")
+    return n.value, hq.value, hkv.value, d.value
 
 
 def ua_last_device_error(plan: int) -> int:
@@ -493,9 +517,12 @@ class Plan:
 
     _slopes = None  # the forwards read the caller's tensor: kept as long as they may
 
-    def __init__(self, cu_query_lens, kv_lens, num_q_heads, *args, **kwargs):
-        self.handle = ua_plan_create(cu_query_lens, kv_lens, num_q_heads, *args, **kwargs)
+    def __init__(self, cu_query_lens, kv_lens, num_q_heads, num_kv_heads, head_dim, *args, **kwargs):
+        self.handle = ua_plan_create(cu_query_lens, kv_lens, num_q_heads, num_kv_heads, head_dim,
+                                     *args, **kwargs)
         self.num_q_heads = int(num_q_heads)
+        self.num_kv_heads = int(num_kv_heads)
+        self.head_dim = int(head_dim)
         self.num_tokens = int(cu_query_lens[-1]) if len(cu_query_lens) else 0
 
     @property
@@ -512,9 +539,9 @@ class Plan:
                        num_blocks, positions=None, k_scale=1.0, v_scale=1.0, stream=None):
         if len(q) < self.num_tokens:
             raise ValueError(f"q: {len(q)} tokens, the plan has {self.num_tokens}")
-        ua_rope_append_kv(self.handle, rope.handle if isinstance(rope, Rope) else rope, q, k_new,
-                          v_new, q_out, k_cache, v_cache, block_tables, num_blocks, positions,
-                          k_scale, v_scale, stream)
+        _rope_append(self.handle, (self.num_tokens, self.num_q_heads, self.num_kv_heads, self.head_dim),
+                     rope.handle if isinstance(rope, Rope) else rope, q, k_new, v_new, q_out, k_cache,
+                     v_cache, block_tables, num_blocks, positions, k_scale, v_scale, stream)
 
     def set_scores(self, softcap=0.0, alibi_slopes=None):
         """ua_plan_set_scores; the plan holds the tensor until the next call (a

@@ -773,6 +773,16 @@ ua_status ua_plan_get_info(const ua_plan* plan, ua_plan_info* info) {
   return UA_OK;
 }
 
+ua_status ua_plan_get_batch(const ua_plan* plan, int64_t* total_q, int32_t* num_q_heads,
+                            int32_t* num_kv_heads, int32_t* head_dim) {
+  if (!plan || !total_q || !num_q_heads || !num_kv_heads || !head_dim) return UA_ERR_INVALID_ARG;
+  *total_q = plan->total_q;
+  *num_q_heads = plan->prob.num_q_heads;
+  *num_kv_heads = plan->prob.num_kv_heads;
+  *head_dim = plan->prob.head_dim;
+  return UA_OK;
+}
+
 ua_status ua_plan_destroy(ua_plan* plan) {
   if (plan == nullptr) return UA_OK;
   ua_plan_destroy(plan->shaped);
