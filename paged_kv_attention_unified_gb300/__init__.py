@@ -292,8 +292,8 @@ def _token_rows(t, name, tokens, device, bf16):
     shape, stride = t.shape, t.stride()
     if t.get_device() != device:
         raise ValueError(f"{name}: on {t.device}, not on the current CUDA device")
-    if len(shape) != 3 or shape[0] != tokens or stride[2] != 1 or stride[1] != shape[2] or (
-            t.dtype != bf16):
+    if len(shape) != 3 or shape[0] != tokens or stride[2] != 1 or t.dtype != bf16 or (
+            stride[1] != shape[2] and shape[1] != 1):  # (one head's distance says nothing)
         raise ValueError(f"{name}: a bf16 [tokens, heads, head_dim] tensor with contiguous rows "
                          f"is needed, of q's {tokens} tokens ({t.dtype}, shape {tuple(shape)}, "
                          f"strides {stride})")

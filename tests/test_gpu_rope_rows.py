@@ -66,3 +66,15 @@ def test_views_of_other_heads_are_refused(through):
         at = lambda c: torch.cat([c[2, 15:], c[0, :4]])  # noqa: E731  positions 15 .. 19
         assert torch.equal(at(s.cache[1]), v)
         assert s.plan.last_device_error() == 0
+
+
+def test_one_key_head_from_a_transpose():
+    with Append(hkv=1) as s:
+        q = s.rows()[0].contiguous()
+        k, v = (torch.randn(1, T, D, device="cuda").to(torch.bfloat16).transpose(0, 1) for _ in range(2))
+        want = torch.empty(T, HQ, D, dtype=torch.bfloat16, device="cuda")
+        s.call(q, k.clone(memory_format=torch.contiguous_format).view(T, 1, D), v.reshape(T, 1, D), want)
+        cache = s.cache.clone()
+        s.cache.zero_()
+        assert torch.equal(s.call(q, k, v, torch.empty_like(want)), want)
+        assert torch.equal(s.cache, cache)

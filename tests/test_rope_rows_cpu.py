@@ -113,3 +113,17 @@ def test_a_null_plan_has_no_batch():
     n, a, b, d = ctypes.c_int64(), ctypes.c_int32(), ctypes.c_int32(), ctypes.c_int32()
     refs = [ctypes.byref(x) for x in (n, a, b, d)]
     assert ua.lib().ua_plan_get_batch(None, *refs) == ua.UA_ERR_INVALID_ARG
+
+
+def test_one_head_may_have_any_distance():
+    """[tokens, 1, d] as a transpose of [1, tokens, d]: contiguous rows, whatever the stride of the
+    axis of one head says."""
+    bf16 = torch.bfloat16
+    x = torch.zeros(1, T, D, dtype=bf16).transpose(0, 1)
+    assert x.is_contiguous() and x.stride(1) != D
+    for rows in (x, torch.zeros(1, T, 2 * D, dtype=bf16).transpose(0, 1)[..., :D]):
+        assert ua._token_rows(rows, "k_new", T, -1, bf16) == (rows.data_ptr(), rows.stride(0))
+    with pytest.raises(ValueError):
+        ua._token_rows(torch.zeros(T, D, 2, dtype=bf16).transpose(1, 2)[:, :1], "k_new", T, -1, bf16)
+    with pytest.raises(ValueError):
+        ua._token_rows(torch.zeros(T, 2, 2 * D, dtype=bf16)[..., :D], "k_new", T, -1, bf16)
