@@ -503,13 +503,19 @@ ua_status ua_plan_set_prefill_ctas(ua_plan* plan, int32_t num_ctas);
  * rows; with the built-in default, where they are work enough) run in a
  * prefill kernel at every head dim then, whereas with plain scores and no
  * prefix only the head dims 64, 128, 192 and 256 have one (ua_schedule);
- * ua_plan_get_info tells the lists of the current setting.
+ * ua_plan_get_info tells the lists of the current setting. The first call that
+ * shapes the scores of such a batch schedules it a second time, with lists, a
+ * split workspace and (e4m3 cache) a staging copy of its own; a plan that stays
+ * plain, or only appends, has none of them. May be called while a stream is
+ * being captured; nothing of it is captured.
  * Every prefill and decode kernel applies them, together with the window, the
  * causal or prefix mask, the unified max and fp8 products; ua_forward_oneshot,
  * ua_forward_host and ua_forward_static_scratch, which take no plan, have
  * plain scores. set_scores(plan, 0, NULL) restores plain scores.
  * Returns UA_ERR_INVALID_ARG for a null plan, a softcap outside its range, or
- * slopes that are misaligned or not device memory of the plan's device. */
+ * slopes that are misaligned or not device memory of the plan's device;
+ * UA_ERR_CUDA where memory for the second schedule is wanting. After an error
+ * the plan is as it was. */
 #define UA_MIN_SOFTCAP 0.0009765625f
 #define UA_MAX_SOFTCAP 4096.f
 ua_status ua_plan_set_scores(ua_plan* plan, float softcap, const float* alibi_slopes);

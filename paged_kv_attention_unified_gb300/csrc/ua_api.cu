@@ -54,8 +54,11 @@ struct ua_plan {
   int32_t* d_prefix = nullptr;        // ua_plan_create_prefix: device prefix lengths (in d_meta)
   // For forwards with shaped scores, where those run prompts in a prefill
   // kernel that plain scores do not have (head dims padded to the next built
-  // one): the same batch scheduled that way. Null: this plan serves both.
+  // one): the same batch scheduled that way, made by the first
+  // ua_plan_set_scores that shapes them. Null: this plan serves both.
   ua_plan* shaped = nullptr;
+  std::vector<int32_t> lens;          // what that takes: host cu_query_lens, then kv_lens
+  cudaEvent_t uploaded = nullptr;     // (of a shaped one) its lists are there; null once seen
   // kernel timing (ua_plan_set_profiling)
   struct EventPair {
     cudaEvent_t start = nullptr, stop = nullptr;
@@ -107,7 +110,9 @@ cudaMemPool_t plan_pool(int device) {
 cudaError_t plan_alloc(void** ptr, size_t bytes, int device, cudaStream_t stream) {
   cudaMemPool_t pool = plan_pool(device);
   if (pool == nullptr) return cudaErrorMemoryAllocation;
-  return cudaMallocFromPoolAsync(ptr, bytes, pool, stream);
+  const cudaError_t e = cudaMallocFromPoolAsync(ptr, bytes, pool, stream);
+  if (e != cudaSuccess) cudaGetLastError();  // not a later launch's error
+  return e;
 }
 
 // Pinned host blocks for the plan's tile-list upload. A copy from pageable
@@ -137,7 +142,10 @@ bool pinned_take(size_t bytes, PinnedBlock* out) {
   }
   PinnedBlock b;
   b.bytes = bytes < (64u << 10) ? (64u << 10) : bytes;
-  if (cudaMallocHost(&b.ptr, b.bytes) != cudaSuccess) return false;
+  if (cudaMallocHost(&b.ptr, b.bytes) != cudaSuccess) {
+    cudaGetLastError();  // not a later launch's error
+    return false;
+  }
   if (cudaEventCreateWithFlags(&b.done, cudaEventDisableTiming) != cudaSuccess) {
     cudaFreeHost(b.ptr);
     return false;
@@ -163,6 +171,8 @@ void free_plan_memory(ua_plan* p) {
     }
   p->ev_pending.clear();
   p->ev_free.clear();
+  if (p->uploaded) cudaEventDestroy(p->uploaded);
+  p->uploaded = nullptr;
   // stream-ordered: the memory returns to the pool once the plan's last
   // stream has finished with it
   if (p->d_span) cudaFreeAsync(p->d_span, p->last_stream);
@@ -709,6 +719,90 @@ ua_status forward_host_chunked(const void* q_host, void* out_host,
   return st;
 }
 
+// Calls that a stream capture elsewhere would forbid (allocations, events), for
+// work that is not part of the captured one.
+struct OutsideCapture {
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  OutsideCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
+  ~OutsideCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
+};
+
+// The stream of the shaped plans' uploads: the caller's may be capturing, and
+// the forwards to come may be on another one.
+cudaError_t upload_stream(int dev, cudaStream_t* out) {
+  static std::mutex mu;
+  static cudaStream_t streams[kMaxDevices] = {};
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lock(mu);
+  if (streams[dev] == nullptr) {
+    const cudaError_t e = cudaStreamCreateWithFlags(&streams[dev], cudaStreamNonBlocking);
+    if (e != cudaSuccess) {
+      streams[dev] = nullptr;
+      return e;
+    }
+  }
+  *out = streams[dev];
+  return cudaSuccess;
+}
+
+// plan->shaped from plan->lens (current device: the plan's). Leaves the plan
+// as it was on failure.
+ua_status make_shaped(ua_plan* plan) {
+  const ua::Problem& pr = plan->prob;
+  const int32_t* cu = plan->lens.data();
+  const int32_t* kv = cu + pr.num_seqs + 1;
+  const ua::Problem padded = make_problem(
+      cu, kv, pr.num_seqs, pr.num_q_heads, pr.num_kv_heads, pr.head_dim, pr.block_size,
+      pr.max_blocks_per_seq, pr.kv_dtype, pr.causal, pr.window, pr.num_splits, pr.num_sms,
+      pr.decode_rows_max, true);
+  if (padded.prefill_ok && ua::padded_prefill_pays(padded)) {
+    const OutsideCapture outside;
+    cudaStream_t cs = nullptr;
+    if (upload_stream(plan->device, &cs) != cudaSuccess) return UA_ERR_CUDA;
+    ua_plan* twin = nullptr;
+    ua_status st = create_plan(&twin, cu, kv, pr.num_seqs, pr.num_q_heads, pr.num_kv_heads,
+                               pr.head_dim, pr.block_size, pr.max_blocks_per_seq, pr.kv_dtype,
+                               pr.causal, pr.window, pr.num_splits, pr.decode_rows_max,
+                               reinterpret_cast<ua_stream_t>(cs), nullptr, 0, nullptr, true);
+    if (st != UA_OK) return st;
+    twin->debug_flags = plan->debug_flags;
+    twin->wait_timeout_ns = plan->wait_timeout_ns;
+    twin->prefill_ctas_override = plan->prefill_ctas_override;
+    twin->unified_max_on = plan->unified_max_on;
+    twin->unified_max = plan->unified_max;
+    if (plan->profiling) st = ua_plan_set_profiling(twin, 1);
+    if (st == UA_OK) st = from_cuda(cudaEventCreateWithFlags(&twin->uploaded, cudaEventDisableTiming));
+    if (st == UA_OK) st = from_cuda(cudaEventRecord(twin->uploaded, cs));
+    if (st != UA_OK) {
+      ua_plan_destroy(twin);
+      return st;
+    }
+    plan->shaped = twin;
+  }
+  plan->lens = std::vector<int32_t>();
+  return UA_OK;
+}
+
+// Work on `cs` after the upload of a shaped plan's lists.
+ua_status after_upload(const ua_plan* plan, cudaStream_t cs) {
+  if (plan->uploaded == nullptr) return UA_OK;
+  const OutsideCapture outside;
+  cudaError_t e = cudaEventQuery(plan->uploaded);
+  if (e == cudaErrorNotReady) {
+    cudaGetLastError();  // not a later launch's error
+    // A capture cannot wait for what is outside it: the host does.
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(cs, &capture) == cudaSuccess && capture == cudaStreamCaptureStatusNone)
+      return from_cuda(cudaStreamWaitEvent(cs, plan->uploaded, 0));
+    cudaGetLastError();
+    e = cudaEventSynchronize(plan->uploaded);
+  }
+  if (e != cudaSuccess) return UA_ERR_CUDA;
+  cudaEventDestroy(plan->uploaded);
+  const_cast<ua_plan*>(plan)->uploaded = nullptr;
+  return UA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -724,23 +818,21 @@ ua_status ua_plan_create_ex(ua_plan** out, const int32_t* cu_query_lens_host,
                              causal, window, num_splits, decode_rows_max, stream, nullptr, 0,
                              nullptr);
   if (st != UA_OK || ua::padded_head_dim(head_dim) == head_dim) return st;
-  // ua_plan_set_scores may follow: the schedule of shaped scores, if it
-  // differs (a long sequence, in a problem that a prefill kernel takes).
-  const ua::Problem pr = make_problem(
-      cu_query_lens_host, kv_lens_host, num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
-      max_blocks_per_seq, kv_dtype, causal, window, num_splits, 0, decode_rows_max, true);
+  // ua_plan_set_scores may follow, and shaped scores have a schedule of their
+  // own where a sequence is long and a prefill kernel takes the problem.
   const int64_t rows_max = decode_rows_max < 0 ? ua::kDefaultDecodeRowsMax : decode_rows_max;
-  if (!pr.prefill_ok || (*out)->sched.max_q * int64_t{num_q_heads / num_kv_heads} <= rows_max ||
-      !ua::padded_prefill_pays(pr))
-    return UA_OK;
-  st = create_plan(&(*out)->shaped, cu_query_lens_host, kv_lens_host, num_seqs, num_q_heads,
-                   num_kv_heads, head_dim, block_size, max_blocks_per_seq, kv_dtype, causal,
-                   window, num_splits, decode_rows_max, stream, nullptr, 0, nullptr, true);
-  if (st != UA_OK) {
+  if ((*out)->sched.max_q * int64_t{num_q_heads / num_kv_heads} <= rows_max) return UA_OK;
+  try {
+    std::vector<int32_t>& lens = (*out)->lens;
+    lens.reserve(2 * static_cast<size_t>(num_seqs) + 1);
+    lens.assign(cu_query_lens_host, cu_query_lens_host + num_seqs + 1);
+    lens.insert(lens.end(), kv_lens_host, kv_lens_host + num_seqs);
+  } catch (const std::bad_alloc&) {
     ua_plan_destroy(*out);
     *out = nullptr;
+    return UA_ERR_INVALID_ARG;
   }
-  return st;
+  return UA_OK;
 }
 
 ua_status ua_plan_create(ua_plan** out, const int32_t* cu_query_lens_host,
@@ -821,6 +913,8 @@ ua_status ua_forward(const ua_plan* plan, const void* q, const void* k_cache,
   if (num_blocks >= INT32_MAX) return UA_ERR_INVALID_ARG;  // TMA block coordinates are int32
 
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  const ua_status uploaded = after_upload(plan, cs);
+  if (uploaded != UA_OK) return uploaded;
   ua_plan* mp = const_cast<ua_plan*>(plan);
   mp->last_stream = cs;
   ua::KernelParams kp = base_params(plan, q, k_cache, v_cache, out, cu_query_lens, kv_lens,
@@ -1289,6 +1383,8 @@ ua_status ua_gather_kv_debug(const ua_plan* plan, const void* k_cache, const voi
   if (offs.back() > rows_cap) return UA_ERR_INVALID_ARG;
   if (s.decode.empty()) return UA_OK;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  const ua_status uploaded = after_upload(plan, cs);
+  if (uploaded != UA_OK) return uploaded;
   int64_t* d_offs = nullptr;
   if (cudaMalloc(&d_offs, offs.size() * sizeof(int64_t)) != cudaSuccess) return UA_ERR_CUDA;
   ua_status st = from_cuda(cudaMemcpyAsync(d_offs, offs.data(), offs.size() * sizeof(int64_t),
@@ -1414,6 +1510,14 @@ ua_status ua_plan_set_scores(ua_plan* plan, float softcap, const float* alibi_sl
     if (at.type != cudaMemoryTypeManaged &&
         !(at.type == cudaMemoryTypeDevice && at.device == plan->device))
       return UA_ERR_INVALID_ARG;
+  }
+  if (!plan->lens.empty() && (softcap > 0.f || alibi_slopes != nullptr)) {
+    int cur = 0;
+    if (cudaGetDevice(&cur) != cudaSuccess) return UA_ERR_CUDA;
+    if (cur != plan->device && cudaSetDevice(plan->device) != cudaSuccess) return UA_ERR_CUDA;
+    const ua_status st = make_shaped(plan);
+    if (cur != plan->device) cudaSetDevice(cur);
+    if (st != UA_OK) return st;
   }
   for (ua_plan* p : {plan, plan->shaped}) {
     if (p == nullptr) continue;
