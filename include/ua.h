@@ -496,8 +496,11 @@ ua_status ua_plan_set_prefill_ctas(ua_plan* plan, int32_t num_ctas);
  * in this order, before mask and softmax. Positions are those in the cache.
  * softcap: 0 (none), or from UA_MIN_SOFTCAP to UA_MAX_SOFTCAP (the absolute
  *   error of a capped score stays below 2^-20 of the cap).
- * alibi_slopes: device [num_q_heads] float (finite; on the plan's device), or
- *   NULL (none). Not copied: the caller keeps it until the last forward that
+ * alibi_slopes: device [num_q_heads] float (finite, of either sign; on the
+ *   plan's device), or NULL (none). A slope is held to 2^27 / max(1024, distance
+ *   to the row's farthest visible key) in units of log2, beyond which binary32
+ *   has no range for the scores (131072 keys: 710 a position, in units of the
+ *   argument of exp). Not copied: the caller keeps it until the last forward that
  *   uses it (or graph that captured one) has run.
  * Sequences too long for the decode kernel (more than decode_rows_max packed
  * rows; with the built-in default, where they are work enough) run in a

@@ -213,9 +213,9 @@ struct StepMask {
   int window;
   float phi2;      // unified max in log2 units of the scaled score; NaN: off
   // Score shape (SHAPED instances): the cap, 0 for none, with its argument's
-  // multiplier, and the distance slopes (times log2 e) of the two rows.
+  // multiplier, and the distance biases of the two rows.
   float cap_log2, cap_arg;
-  float slope2[2];
+  RowBias bias[2];
 };
 
 template <int D, bool FP8, bool SHAPED>
@@ -257,7 +257,8 @@ __device__ __forceinline__ void compute_step(WarpState<D>& st, StepRegs<D, FP8>&
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int key = base + key_of_row(g + 8 * (e >> 1));
-      x[e] = fmaf(-mk.slope2[e & 1], static_cast<float>(abs(mk.pos[e & 1] - key)), x[e]);
+      const RowBias& b = mk.bias[e & 1];
+      x[e] = fmaf(-b.slope2, static_cast<float>(abs(mk.pos[e & 1] - key) - b.shift), x[e]);
     }
   }
   // Masking (a select, so that nothing read from outside the visible set can
@@ -491,10 +492,12 @@ __global__ void __launch_bounds__(kThreads, Ring<D, FP8>::kCtasPerSm)
       for (int j = 0; j < 2; ++j) {
         const int n = 2 * t + j;
         mk.last[j] = max(mk.pos[j], prefix - 1);
-        mk.slope2[j] =
-            p.shape.slopes && n < nrows
-                ? p.shape.slopes[tile.kv_head * p.qpk + (tile.row0 + n) % p.qpk] * kLog2e
-                : 0.f;
+        // (of the whole row: the same in every split piece)
+        if (p.shape.slopes && n < nrows)
+          mk.bias[j] = row_bias(
+              p.shape.slopes[tile.kv_head * p.qpk + (tile.row0 + n) % p.qpk],
+              p.window > 0 ? min(mk.pos[j], p.window - 1) : mk.pos[j],
+              (p.causal ? min(kv_len - 1, mk.last[j]) : kv_len - 1) - mk.pos[j]);
       }
       if (p.causal) mk.hi_full = min(kv_hi, max(min_pos + 1, prefix));
     }

@@ -588,10 +588,12 @@ __device__ __forceinline__ bool softmax_tile(const PrefillParams& p, const Softm
     mbar_arrive(bar.q_full(t));
     c = __fdiv_rn(c, inv);
   }
-  float slope2 = 0.f;
+  RowBias bias;
   if constexpr ((SHAPE & kShapeBias) != 0)
-    slope2 = p.shape.slopes[g.kv_head * p.qpk + row % p.qpk] * kLog2e;
-  RowSoftmax<SHAPE, F8, kKeys> shaped(c, p.shape.cap_log2, slope2);
+    bias = row_bias(p.shape.slopes[g.kv_head * p.qpk + row % p.qpk],
+                    p.window > 0 ? min(pos, p.window - 1) : pos,
+                    (p.causal ? min(g.kv_hi - 1, last_key) : g.kv_hi - 1) - pos);
+  RowSoftmax<SHAPE, F8, kKeys> shaped(c, p.shape.cap_log2, bias);
   float m = -INFINITY, l = 0.f;
   for (int j = 0; j < n_t; ++j) {
     if (!__all_sync(0xffffffffu, mbar_wait(bar.s_full(t), (done + j) & 1, abort, p.timeout_ns)))

@@ -400,10 +400,12 @@ __device__ __forceinline__ bool softmax_item(const PrefillParams& p, const Item&
   constexpr bool kShaped = SHAPE != kShapePlain;
   const bool neg = !kShaped && p.score_scale_log2 < 0.f;
   const float c = neg ? -p.score_scale_log2 : p.score_scale_log2;
-  float slope2 = 0.f;
+  RowBias bias;
   if constexpr ((SHAPE & kShapeBias) != 0)
-    slope2 = p.shape.slopes[it.kv_head * p.qpk + row % p.qpk] * kLog2e;
-  RowSoftmax<SHAPE, false, kKeys> shaped(c, p.shape.cap_log2, slope2);
+    bias = row_bias(p.shape.slopes[it.kv_head * p.qpk + row % p.qpk],
+                    p.window > 0 ? min(pos, p.window - 1) : pos,
+                    (p.causal ? min(it.kv_hi - 1, last_key) : it.kv_hi - 1) - pos);
+  RowSoftmax<SHAPE, false, kKeys> shaped(c, p.shape.cap_log2, bias);
   float m = -INFINITY, l = 0.f;
   const int n = it.ntiles;
   for (int j = 0; j < n; ++j) {

@@ -59,6 +59,29 @@ __device__ __forceinline__ float cap_score(float u, float cap_log2) {
   return fmaf(-2.f * cap_log2, rcp_approx(1.f + ex2(u)), cap_log2);
 }
 
+// The distance bias of one row in base 2, -slope2 * (|pos - t| - shift), with
+// softmax's freedom to move a row's scores by a constant: negative slopes
+// favour the far keys, so that the farthest visible one gets no bias there (as
+// the row's own key does under a positive slope) and the scores that count keep
+// their precision however long the context. Slopes are held to 2^27 over the
+// row's reach (131072 keys: 1024 a key, which leaves the neighbour of a favoured
+// key 2^-1024): unfavoured scores then stay within 2^27 and their rounding,
+// some 2^4, within binary32's range of 2^x between the maximum and the
+// exponentials of a key tile.
+struct RowBias {
+  float slope2 = 0.f;
+  int shift = 0;
+};
+// before, after: distances from the row to the first and the last key it sees.
+__device__ __forceinline__ RowBias row_bias(float slope, int before, int after) {
+  const int reach = max(before, after);
+  const float most = 134217728.f / static_cast<float>(max(reach, 1024));
+  RowBias b;
+  b.slope2 = fminf(fmaxf(slope * kLog2e, -most), most);
+  b.shift = b.slope2 < 0.f ? reach : 0;
+  return b;
+}
+
 // Row maximum (of the magnitudes: ABS) with independent 3-input partial
 // maxima; NaN is passed over (it reaches the output by itself).
 template <bool ABS, int N>
@@ -102,11 +125,11 @@ struct RowSoftmax {
   float c, cap_log2;     // raw score -> base 2; the cap in base 2
   float a0, a1, a2, a3;  // base-2 capped score = raw (a0 + a1 raw^2 + a2 raw^4 + a3 raw^6) ...
   float small;           // ... for |raw| up to this
-  float slope2;          // slope * log2 e
+  RowBias bias;
   float m = -INFINITY, l = 0.f;  // reference (a lagging running maximum) and sum
 
-  __device__ __forceinline__ RowSoftmax(float c_, float cap_log2_, float slope2_)
-      : c(c_), cap_log2(cap_log2_), slope2(slope2_) {
+  __device__ __forceinline__ RowSoftmax(float c_, float cap_log2_, const RowBias& bias_)
+      : c(c_), cap_log2(cap_log2_), bias(bias_) {
     if constexpr (kCap) {
       const float k = c / cap_log2, k2 = k * k;  // raw score -> argument of tanh
       a0 = c * 0.99999946f;
@@ -137,11 +160,13 @@ struct RowSoftmax {
 
   // Raw scores of the columns ch .. ch + N - 1 to base-2 scores minus sub, -inf
   // where not visible. SMALL: by the polynomial. OPEN: all of them visible. The
-  // bias is slope * rel as long as visible keys lie at or before their rows.
+  // bias is slope * (rel + shift) as long as visible keys lie at or before their
+  // rows.
   template <bool SMALL, bool OPEN>
   __device__ __forceinline__ void scores(float (&x)[N], int ch, const Place& at, float sub) const {
     using namespace sm100;
-    const float rel = static_cast<float>(at.rel0 + ch);
+    const float slope2 = bias.slope2;
+    const float rel = static_cast<float>(at.rel0 + ch + (kBias ? bias.shift : 0));
     // What is added to a score: -sub, and the bias of its pair of keys.
     const bool after = kBias && !OPEN && at.after;  // (the bias is added further down)
     const float step = kBias && !after ? slope2 : 0.f;
@@ -174,9 +199,10 @@ struct RowSoftmax {
       }
     }
     if (after) {
+      const float key = static_cast<float>(at.rel0 + ch), shift = static_cast<float>(bias.shift);
 #pragma unroll
       for (int i = 0; i < N; ++i)
-        x[i] = fmaf(-slope2, fabsf(rel + static_cast<float>(i)), x[i]);
+        x[i] = fmaf(-slope2, fabsf(key + static_cast<float>(i)) - shift, x[i]);
     }
     if constexpr (!OPEN) {
       static_assert(N == 32, "one bit per column");
@@ -224,7 +250,7 @@ struct RowSoftmax {
     const float m_old = m, m_new = fmaxf(m, top);
     float lead = 0.f;
     if constexpr (kBias && !F8)
-      lead = fminf(fmaxf(-slope2 * static_cast<float>(rel0 + KEYS - 1), 0.f), 48.f);
+      lead = fminf(fmaxf(-bias.slope2 * static_cast<float>(rel0 + KEYS - 1), 0.f), 48.f);
     if (m_new > -INFINITY && (m == -INFINITY || m_new > m + kSlack)) m = m_new + lead;
     return m == m_old ? 1.f : (m_old == -INFINITY ? 0.f : ex2(m_old - m));
   }
@@ -291,10 +317,10 @@ struct RowSoftmax {
       }
       is_small = __all_sync(0xffffffffu, amax <= small);
       float bound = amax * fabsf(c);  // |cap tanh(x / cap)| <= |x|
-      if constexpr (kBias) {  // the largest bias is at one of the ends, or none at the row itself
-        const float first = fabsf(static_cast<float>(at.rel0));
-        const float last = fabsf(static_cast<float>(at.rel0 + KEYS - 1));
-        const float ends = fmaxf(-slope2 * first, -slope2 * last);
+      if constexpr (kBias) {  // the largest bias is at one of the ends, or at most 0 at the row itself
+        const float first = static_cast<float>(abs(at.rel0) - bias.shift);
+        const float last = static_cast<float>(abs(at.rel0 + KEYS - 1) - bias.shift);
+        const float ends = fmaxf(-bias.slope2 * first, -bias.slope2 * last);
         bound += at.rel0 <= 0 && at.rel0 + KEYS > 0 ? fmaxf(ends, 0.f) : ends;
       }
       settled = __all_sync(0xffffffffu, bound <= m + kSlack);
@@ -340,9 +366,11 @@ struct RowSoftmax {
     }
     if constexpr (kBias) {
       const float mult = kCap ? 1.f : c, rel = static_cast<float>(rel0);
+      // (the rounding of the constant moves every score of the row alike)
+      const float slope2 = bias.slope2, own = slope2 * static_cast<float>(bias.shift);
 #pragma unroll
       for (int i = 0; i < N; ++i)
-        x[i] = fmaf(x[i], mult, -slope2 * fabsf(rel + static_cast<float>(i)));
+        x[i] = fmaf(x[i], mult, fmaf(-slope2, fabsf(rel + static_cast<float>(i)), own));
     }
     // a prefix alone leaves the scores raw until the exponents
     const bool raw = !kCap && !kBias, flip = raw && c < 0.f;
