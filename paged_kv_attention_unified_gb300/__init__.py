@@ -287,8 +287,8 @@ def ua_rope_destroy(rope: int):
 
 
 def _token_rows(t, name, tokens, device, bf16):
-    """Pointer and row stride of a bf16 [tokens, heads, head_dim] tensor whose
-    rows are contiguous (their distance is free)."""
+    """Pointer, row stride, heads and head_dim of a bf16 [tokens, heads, head_dim]
+    tensor whose rows are contiguous (their distance is free)."""
     shape, stride = t.shape, t.stride()
     if t.get_device() != device:
         raise ValueError(f"{name}: on {t.device}, not on the current CUDA device")
@@ -298,7 +298,8 @@ def _token_rows(t, name, tokens, device, bf16):
                          f"is needed, of q's {tokens} tokens ({t.dtype}, shape {tuple(shape)}, "
                          f"strides {stride})")
     # with one token (or none) the stride is whatever torch holds: any valid one serves
-    return t.data_ptr(), stride[0] if tokens > 1 else shape[1] * shape[2]
+    heads, d = shape[1], shape[2]
+    return t.data_ptr(), stride[0] if tokens > 1 else heads * d, heads, d
 
 
 def ua_rope_append_kv(plan, rope, q, k_new, v_new, q_out, k_cache, v_cache, block_tables,
@@ -318,9 +319,9 @@ def _rope_append(plan, batch, rope, q, k_new, v_new, q_out, k_cache, v_cache, bl
     bf16, shape = torch.bfloat16, q.shape
     n = shape[0]
     dev = torch._C._cuda_getDevice() if q.is_cuda else 0
-    qp, qs = _token_rows(q, "q", n, dev, bf16)
-    kp, ks = _token_rows(k_new, "k_new", n, dev, bf16)
-    vp, vs = _token_rows(v_new, "v_new", n, dev, bf16)
+    qp, qs, qh, qd = _token_rows(q, "q", n, dev, bf16)
+    kp, ks, kh, kd = _token_rows(k_new, "k_new", n, dev, bf16)
+    vp, vs, vh, vd = _token_rows(v_new, "v_new", n, dev, bf16)
     if q_out.shape != shape or q_out.dtype != bf16 or q_out.get_device() != dev or (
             not q_out.is_contiguous()):
         raise ValueError("q_out: a contiguous tensor of q's shape, type and device is needed")
@@ -334,7 +335,7 @@ def _rope_append(plan, batch, rope, q, k_new, v_new, q_out, k_cache, v_cache, bl
     # The row distances do not show the library how many heads there are: rows
     # inside a fused projection are as wide as any plan's.
     tokens, hq, hkv, d = ua_plan_get_batch(plan) if batch is None else batch
-    if n < tokens or shape != (n, hq, d) or k_new.shape != (n, hkv, d) or v_new.shape != (n, hkv, d):
+    if n < tokens or not (qh == hq and kh == vh == hkv and qd == kd == vd == d):
         raise UAError(UA_ERR_INVALID_ARG, f"ua_rope_append_kv: q {tuple(shape)}, k_new "
                       f"{tuple(k_new.shape)}, v_new {tuple(v_new.shape)} on a plan of {tokens} "
                       f"tokens, {hq} query heads, {hkv} KV heads and head_dim {d}")

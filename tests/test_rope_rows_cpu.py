@@ -122,7 +122,7 @@ def test_one_head_may_have_any_distance():
     x = torch.zeros(1, T, D, dtype=bf16).transpose(0, 1)
     assert x.is_contiguous() and x.stride(1) != D
     for rows in (x, torch.zeros(1, T, 2 * D, dtype=bf16).transpose(0, 1)[..., :D]):
-        assert ua._token_rows(rows, "k_new", T, -1, bf16) == (rows.data_ptr(), rows.stride(0))
+        assert ua._token_rows(rows, "k_new", T, -1, bf16)[:2] == (rows.data_ptr(), rows.stride(0))
     with pytest.raises(ValueError):
         ua._token_rows(torch.zeros(T, D, 2, dtype=bf16).transpose(1, 2)[:, :1], "k_new", T, -1, bf16)
     with pytest.raises(ValueError):
