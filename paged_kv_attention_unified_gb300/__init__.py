@@ -517,6 +517,7 @@ class Plan:
     """RAII wrapper around a plan handle."""
 
     _slopes = None  # the forwards read the caller's tensor: kept as long as they may
+    _slopes_streams = ()  # streams whose forwards the tensor's memory waits for
 
     def __init__(self, cu_query_lens, kv_lens, num_q_heads, num_kv_heads, head_dim, *args, **kwargs):
         self.handle = ua_plan_create(cu_query_lens, kv_lens, num_q_heads, num_kv_heads, head_dim,
@@ -530,8 +531,18 @@ class Plan:
     def info(self) -> ua_plan_info:
         return ua_plan_get_info(self.handle)
 
-    def forward(self, *args, **kwargs):
-        ua_forward(self.handle, *args, **kwargs)
+    def forward(self, q, k_cache, v_cache, out, cu_query_lens, kv_lens, block_tables, num_blocks,
+                max_q, max_kv, scale, k_scale=1.0, v_scale=1.0, stream=None):
+        handle = _stream_handle(stream)
+        ua_forward(self.handle, q, k_cache, v_cache, out, cu_query_lens, kv_lens, block_tables,
+                   num_blocks, max_q, max_kv, scale, k_scale, v_scale, handle)
+        if self._slopes is not None and handle not in self._slopes_streams:
+            import torch
+            if stream is None:
+                stream = torch.cuda.current_stream(self._slopes.device)
+            if isinstance(stream, torch.cuda.Stream):  # (a handle says nothing of its stream's life)
+                self._slopes.record_stream(stream)
+                self._slopes_streams += (handle,)
 
     def append_kv(self, *args, **kwargs):
         ua_append_kv(self.handle, *args, **kwargs)
@@ -545,9 +556,11 @@ class Plan:
                      v_cache, block_tables, num_blocks, positions, k_scale, v_scale, stream)
 
     def set_scores(self, softcap=0.0, alibi_slopes=None):
-        """ua_plan_set_scores; the plan holds the tensor until the next call (a
-        graph that captured a forward, or one on a stream of its own, needs it
-        for as long as it runs)."""
+        """ua_plan_set_scores; the plan holds the tensor until the next call, and
+        its memory is not given out again before the plan's forwards have run
+        on whatever torch streams (the caller keeps it for one on a raw stream
+        handle until that has run, and for a graph that captured one until the
+        last replay has)."""
         import torch
         if alibi_slopes is not None and (
                 alibi_slopes.shape != (self.num_q_heads,) or not alibi_slopes.is_contiguous()
@@ -555,7 +568,7 @@ class Plan:
             raise ValueError(f"alibi_slopes: a contiguous float32 tensor of {self.num_q_heads} "
                              "slopes is needed")
         ua_plan_set_scores(self.handle, softcap, alibi_slopes)
-        self._slopes = alibi_slopes
+        self._slopes, self._slopes_streams = alibi_slopes, ()
 
     def last_device_error(self) -> int:
         return ua_last_device_error(self.handle)

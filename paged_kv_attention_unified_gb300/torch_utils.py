@@ -10,7 +10,7 @@ from typing import Optional, Sequence
 
 import torch
 
-from . import (UA_KV_BF16, UA_KV_FP8_E4M3, Plan, Rope, ua_append_kv, ua_forward)
+from . import (UA_KV_BF16, UA_KV_FP8_E4M3, Plan, Rope, ua_append_kv)
 
 
 @dataclasses.dataclass
@@ -80,9 +80,8 @@ def forward(plan: Plan, b: DeviceBatch, out: Optional[torch.Tensor] = None,
             stream=None) -> torch.Tensor:
     if out is None:
         out = b.new_out()
-    ua_forward(plan.handle, b.q, b.k_cache, b.v_cache, out, b.cu_query_lens, b.kv_lens,
-               b.block_tables, b.num_blocks, b.max_q, b.max_kv, b.scale, b.k_scale, b.v_scale,
-               stream=stream)
+    plan.forward(b.q, b.k_cache, b.v_cache, out, b.cu_query_lens, b.kv_lens, b.block_tables,
+                 b.num_blocks, b.max_q, b.max_kv, b.scale, b.k_scale, b.v_scale, stream=stream)
     return out
 
 

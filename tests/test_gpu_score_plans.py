@@ -147,3 +147,65 @@ def test_a_plan_is_destroyed_right_after_its_scores_are_shaped():
         plan.set_scores(9.0)
         plan.close()
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("through", ["plan", "current", "helper", "closed"])
+def test_slopes_given_back_while_a_forward_on_another_stream_reads_them(through):
+    """The plan gives the slopes' memory back when its scores change (or it ends); a forward that is
+    still to run on another stream has them all the same."""
+    case = W.make_case("held", [1, 120], [300, 200], 4, 2, 128, 16, seed=6)
+    b = tu.to_device(case)
+    values, side = [0.5, 0.25, 0.1, 0.0], torch.cuda.Stream()
+    out = b.new_out()
+    torch.cuda.synchronize()
+    with tu.make_plan(b) as plan:
+        slopes = torch.tensor(values, device="cuda")
+        at = slopes.data_ptr()
+        plan.set_scores(0.0, slopes)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(50_000_000)
+        if through == "helper":
+            tu.forward(plan, b, out, stream=side)
+        else:
+            with torch.cuda.stream(side if through == "current" else None):
+                plan.forward(b.q, b.k_cache, b.v_cache, out, b.cu_query_lens, b.kv_lens, b.block_tables,
+                             b.num_blocks, b.max_q, b.max_kv, b.scale,
+                             stream=None if through == "current" else side)
+        del slopes
+        if through == "closed":
+            plan.close()
+            del plan
+        else:
+            plan.set_scores()
+        others = [torch.full((4,), 100.0, device="cuda") for _ in range(50)]
+        torch.cuda.synchronize()
+    assert _within(out, case, slopes=values)
+    assert at and len(others) == 50
+
+
+def test_biased_forwards_on_every_kind_of_stream():
+    """None, the default stream, torch streams and raw handles, once and again, and captured."""
+    case = W.make_case("kinds", [1, 120], [300, 200], 4, 2, 128, 16, seed=7)
+    b = tu.to_device(case)
+    values, side = [0.5, 0.25, 0.1, 0.0], torch.cuda.Stream()
+    with tu.make_plan(b) as plan:
+        plan.set_scores(0.0, torch.tensor(values, device="cuda"))
+        torch.cuda.synchronize()
+        for stream in (None, torch.cuda.default_stream(), side, side.cuda_stream, 0,
+                       type("Handle", (), {"cuda_stream": side.cuda_stream})(), torch.cuda.ExternalStream(side.cuda_stream)) * 2:
+            out = b.new_out()
+            torch.cuda.synchronize()
+            tu.forward(plan, b, out, stream=stream)
+            torch.cuda.synchronize()
+            assert _within(out, case, slopes=values)
+        slopes = torch.tensor(values, device="cuda")
+        plan.set_scores(0.0, slopes)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            tu.forward(plan, b, out)
+        plan.set_scores()
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert _within(out, case, slopes=values)
