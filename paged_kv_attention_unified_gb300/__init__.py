@@ -163,7 +163,8 @@ def _prefix_array(prefix_lens, num_seqs, causal):
         raise ValueError("a prefix mask is causal: causal must be 1 with prefix_lens")
     if len(lens) != num_seqs:
         raise ValueError(f"prefix_lens has {len(lens)} entries for {num_seqs} sequences")
-    return _i32_array(min(int(x), 2 ** 31 - 1) for x in lens)  # as good as any longer one
+    # 2^31 - 1 is as good as any longer one; what is negative stays so
+    return _i32_array(max(-1, min(int(x), 2 ** 31 - 1)) for x in lens)
 
 
 def ua_status_string(status: int) -> str:
