@@ -520,13 +520,11 @@ class Plan:
     _slopes = None  # the forwards read the caller's tensor: kept as long as they may
     _slopes_streams = ()  # streams whose forwards the tensor's memory waits for
 
-    def __init__(self, cu_query_lens, kv_lens, num_q_heads, num_kv_heads, head_dim, *args, **kwargs):
-        self.handle = ua_plan_create(cu_query_lens, kv_lens, num_q_heads, num_kv_heads, head_dim,
-                                     *args, **kwargs)
-        self.num_q_heads = int(num_q_heads)
-        self.num_kv_heads = int(num_kv_heads)
-        self.head_dim = int(head_dim)
-        self.num_tokens = int(cu_query_lens[-1]) if len(cu_query_lens) else 0
+    def __init__(self, *args, **kwargs):
+        """Arguments as ua_plan_create."""
+        self.handle = ua_plan_create(*args, **kwargs)
+        self.num_tokens, self.num_q_heads, self.num_kv_heads, self.head_dim = (
+            ua_plan_get_batch(self.handle))
 
     @property
     def info(self) -> ua_plan_info:

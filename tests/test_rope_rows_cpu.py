@@ -127,3 +127,15 @@ def test_one_head_may_have_any_distance():
         ua._token_rows(torch.zeros(T, D, 2, dtype=bf16).transpose(1, 2)[:, :1], "k_new", T, -1, bf16)
     with pytest.raises(ValueError):
         ua._token_rows(torch.zeros(T, 2, 2 * D, dtype=bf16)[..., :D], "k_new", T, -1, bf16)
+
+
+@pytest.mark.parametrize("cu", [[0, T], iter([0, T]), (0, T, T + 9), [0, T, 0, 0], range(0, 2 * T, T)])
+def test_a_plans_tokens_are_those_of_its_sequences(library, cu):
+    """Whatever holds the offsets, and whatever follows the last sequence's."""
+    def create(handle, cu, kv, n, *rest):
+        handle._obj.value = 16
+        return ua.UA_OK
+    library.ua_plan_create_ex = create
+    library.ua_plan_destroy = lambda handle: ua.UA_OK
+    with ua.Plan(cu, [20], HQ, num_kv_heads=HKV, head_dim=D, block_size=16, max_blocks_per_seq=2) as plan:
+        assert (plan.num_tokens, plan.num_q_heads, plan.num_kv_heads, plan.head_dim) == (T, HQ, HKV, D)
