@@ -365,12 +365,26 @@ struct RowSoftmax {
       }
     }
     if constexpr (kBias) {
-      const float mult = kCap ? 1.f : c, rel = static_cast<float>(rel0);
-      // (the rounding of the constant moves every score of the row alike)
-      const float slope2 = bias.slope2, own = slope2 * static_cast<float>(bias.shift);
+      // Key tiles with no key after its row, most of them, take the bias in
+      // pairs, slope * (rel + shift), as above (head_dim 192, 6 prompts of 1500
+      // tokens after 1500, 32 heads: 1005 us, 1251 with the distances one by one).
+      const float mult = kCap ? 1.f : c, slope2 = bias.slope2;
+      if (__all_sync(0xffffffffu, rel0 + N <= 1)) {
+        const float first = static_cast<float>(rel0 + bias.shift);
+        const uint64_t m2 = f2_pack(mult, mult), step2 = f2_pack(slope2, slope2);
+        const uint64_t base = f2_pack(first * slope2, (first + 1.f) * slope2);
 #pragma unroll
-      for (int i = 0; i < N; ++i)
-        x[i] = fmaf(x[i], mult, fmaf(-slope2, fabsf(rel + static_cast<float>(i)), own));
+        for (int i = 0; i < N; i += 2) {
+          const float f = static_cast<float>(i);
+          f2_unpack(f2_fma(f2_pack(x[i], x[i + 1]), m2, f2_fma(f2_pack(f, f), step2, base)), x[i],
+                    x[i + 1]);
+        }
+      } else {
+        const float rel = static_cast<float>(rel0), shift = static_cast<float>(bias.shift);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          x[i] = fmaf(x[i], mult, -slope2 * (fabsf(rel + static_cast<float>(i)) - shift));
+      }
     }
     // a prefix alone leaves the scores raw until the exponents
     const bool raw = !kCap && !kBias, flip = raw && c < 0.f;
