@@ -109,11 +109,13 @@ cudaError_t launch_stage(const StageParams& p, int sms, cudaStream_t stream) {
   // eight CTAs to a page leave it two, sixteen one. Measured with one / eight /
   // sixteen: 8 heads of 128, 8 pages 20.6 / 8.0 / 6.8 us, 81 pages 27.3 / 17.9 /
   // 17.8, 649 pages 132.9 / 90.2 / 96.0; 32 heads, 16 pages 71 / 17 / 16, 64
-  // pages 66 / 49 / 46, 192 pages 157 / 124 / 119. Only with wide rows (several
-  // load rounds each) and pages for most of the SMs is one CTA to a page the
-  // faster: 128 pages of 32 heads 75 / 86 / 83, of 24 heads 61 / 65 / 64.
+  // pages 66 / 50 / 45, 192 pages 157 / 124 / 119. Only with wide rows (several
+  // load rounds each) and pages for most of the SMs, in one wave, is one CTA to a
+  // page the faster, with one / sixteen: 32 heads, 102 pages 70.5 / 66.7, 108 pages
+  // 71.5 / 71.0, 116 pages 73.1 / 78.6, 152 pages 81 / 98, 156 pages 144 / 99; 24
+  // heads, 108 pages 59.2 / 54.2, 116 pages 59.4 / 59.1, 128 pages 61.9 / 62.4.
   const bool wide_rows = p.row_elems / 16 > 32 * kUnroll;
-  const bool fills = 3 * p.num_tiles > 2 * sms && p.num_tiles <= sms;
+  const bool fills = 4 * p.num_tiles > 3 * sms && p.num_tiles <= sms;
   const int parts = !wide_rows ? 8 : (fills ? 1 : 16);
   stage_kernel<<<p.num_tiles * parts, kStageWarps * 32, 0, stream>>>(p, parts);
   return cudaGetLastError();
