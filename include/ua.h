@@ -45,9 +45,11 @@
  *
  * Supported: every head_dim that is a multiple of 32 from 32 to 256 in the
  * decode kernel, which also runs any prefill no prefill kernel takes; a
- * tcgen05 prefill kernel at head_dim 64 and 128 (256-row tiles, 128-key
- * tiles) and one at head_dim 192 and 256 (one 128-row query tile and 64-key
- * tiles at a time, block sizes that 64 divides or that divide 64);
+ * tcgen05 prefill kernel at head_dim 64 and 128 (tiles of one or two 128-row
+ * query tiles, 128-key tiles) and one at head_dim 192 and 256 (one 128-row
+ * query tile and 64-key tiles at a time, block sizes that 64 divides or that
+ * divide 64), which take shaped scores at the other head dims too
+ * (ua_plan_set_scores, ua_plan_create_prefix);
  * block_size a multiple of 16; any GQA ratio (the prefill kernels take ratios
  * dividing 128; sequences they cannot take run in the decode kernel).
  *
