@@ -1411,6 +1411,10 @@ ua_status ua_plan_set_profiling(ua_plan* plan, int32_t enable) {
       return UA_ERR_CUDA;
     plan->d_span = static_cast<unsigned long long*>(ptr);
     if (span_reset(plan, kSpanSlots, plan->last_stream) != cudaSuccess) return UA_ERR_CUDA;
+    // a shaped plan's first forward waits for this too
+    if (plan->uploaded != nullptr &&
+        cudaEventRecord(plan->uploaded, plan->last_stream) != cudaSuccess)
+      return UA_ERR_CUDA;
   }
   plan->profiling = enable != 0;
   return plan->shaped != nullptr ? ua_plan_set_profiling(plan->shaped, enable) : UA_OK;

@@ -97,6 +97,19 @@ def test_settings_made_before_the_scores_hold_for_them():
         assert plan.last_device_error() == 0
 
 
+def test_profiling_from_before_the_first_shaped_forward():
+    """Enabled after the scores are shaped: the spans are reset before the kernels write them."""
+    b = tu.to_device(_case(8))
+    for _ in range(10):
+        with tu.make_plan(b, decode_rows_max=32) as plan:
+            plan.set_scores(12.0)
+            ua.ua_plan_set_profiling(plan.handle, True)
+            tu.forward(plan, b)
+            times = ua.ua_plan_kernel_times(plan.handle)
+            for kind in ("prefill", "decode"):
+                assert times[kind][1] == 1 and 0 < times[kind][0] < 1000, times
+
+
 def test_scores_shaped_while_the_gpu_is_busy_and_used_on_another_stream():
     """The second schedule's lists are there before a forward on any stream reads them."""
     case = _case(3)
