@@ -159,3 +159,21 @@ def test_prefill_tiles_have_one_query_tile_where_that_fills_more_sms(d):
     assert rows([0, 576], [576]) == 128                     # 9 tiles of 256 rows a head, 72 in all
     assert rows([0, 600], [600]) == (128 if d > 128 else 256)   # 80 of 152
     assert rows([0, 576, 577], [576, 10000]) == (128 if d > 128 else 256)  # a decode step beside it
+
+
+def test_cap_polynomial_keeps_its_error_bound():
+    """The kernels' odd polynomial for tanh, in binary32 as they evaluate it (each multiply-add rounded
+    once), on |a| <= 1/2: 5.5e-7 by its fit, four roundings of at most 2^-24 each by Horner's steps,
+    whose later terms are below a quarter of the first."""
+    import os
+    import re
+    src = open(os.path.join(os.path.dirname(ua.__file__), "csrc", "score_shape.cuh")).read()
+    coef = [float(re.search(rf"\ba{i} = c \* (-?[0-9.]+)f", src).group(1)) for i in range(4)]
+    f = np.float32
+    a = np.linspace(-0.5, 0.5, 200001)
+    a = a[np.abs(a) > 1e-6].astype(f)
+    fma = lambda x, y, z: f(x.astype(np.float64) * y + z)  # noqa: E731
+    sq = f(a * a)
+    poly = fma(fma(fma(np.full_like(a, f(coef[3])), sq, f(coef[2])), sq, f(coef[1])), sq, f(coef[0]))
+    got, exact = f(a * poly).astype(np.float64), np.tanh(a.astype(np.float64))
+    assert np.max(np.abs(got / exact - 1)) <= 5.5e-7 + 4 * 2.0 ** -24
