@@ -28,12 +28,15 @@
  * Query i of s sits at position pos = kv_len(s) - q_len(s) + i; key t is
  * visible iff t < kv_len(s), and (causal == 0 or t <= pos), and
  * (window <= 0 or t > pos - window). A plan may add a prefix mask
- * (ua_plan_create_prefix), a cap on the scores and a distance bias
+ * (ua_plan_create_prefix), first keys that stay visible under the window
+ * (ua_plan_create_sinks), a cap on the scores and a distance bias
  * (ua_plan_set_scores).
  *
  * fp8 e4m3 caches hold per-tensor scaled values: the key is code * k_scale,
  * the value code * v_scale ("vllm_triton_unified_attention_notes", the load
  * and quantisation branch). k_scale / v_scale are ignored for bf16 caches.
+ * They may have a scale for each physical block and KV head instead
+ * (ua_plan_set_block_scales).
  *
  * Work split. A plan (ua_plan_create) is built on the host from host copies of
  * the lengths: a CPU scheduler turns (sequence, KV head, row block) programs
@@ -233,6 +236,43 @@ ua_status ua_schedule_prefix(const int32_t* cu_query_lens_host, const int32_t* k
                              ua_combine_group* groups, int64_t groups_cap);
 
 /*
+ * ua_plan_create_sinks -- a plan whose window leaves the first sink_tokens keys
+ * of every sequence visible (the tokens that draw attention whatever follows;
+ * a session then goes on for ever in the keys of sinks and window). Key t is
+ * visible to the query at position pos iff t < kv_len, (causal == 0, or t <=
+ * pos, or t < prefix_len) and (window <= 0, or t > pos - window, or t <
+ * sink_tokens).
+ * sink_tokens: >= 0; without effect under window <= 0, where every key stays.
+ * prefix_lens_host: as ua_plan_create_prefix, or NULL (no prefix; causal 0 or 1).
+ * Keys that no query of a sequence sees -- from sink_tokens up to the first
+ * query's window -- are not read, and a page that holds only such keys is not
+ * looked up: its block-table entry may be anything (the page may have been given
+ * back). Positions stay those in the cache: block tables keep an entry per
+ * logical block. With sinks, sequences that are too long for the decode kernel
+ * run in a prefill kernel at every head dim (see ua_plan_set_scores). In the
+ * tile lists a range [kv_lo, kv_hi) holds the keys that its rows pass over.
+ * Other arguments, work and errors as ua_plan_create_ex; UA_ERR_INVALID_ARG for
+ * a negative sink_tokens too.
+ * ua_schedule_sinks -- its scheduler alone, as ua_schedule.
+ */
+ua_status ua_plan_create_sinks(ua_plan** out, const int32_t* cu_query_lens_host,
+                               const int32_t* kv_lens_host, const int32_t* prefix_lens_host,
+                               int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                               int32_t head_dim, int32_t block_size, int32_t max_blocks_per_seq,
+                               int32_t kv_dtype, int32_t causal, int32_t window,
+                               int32_t sink_tokens, int32_t num_splits, int32_t decode_rows_max,
+                               ua_stream_t stream);
+ua_status ua_schedule_sinks(const int32_t* cu_query_lens_host, const int32_t* kv_lens_host,
+                            const int32_t* prefix_lens_host, int32_t num_seqs,
+                            int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                            int32_t block_size, int32_t max_blocks_per_seq, int32_t kv_dtype,
+                            int32_t causal, int32_t window, int32_t sink_tokens,
+                            int32_t num_splits, int32_t num_sms, int32_t decode_rows_max,
+                            ua_plan_info* info, ua_tile* prefill_tiles, int64_t prefill_cap,
+                            ua_tile* decode_tiles, int64_t decode_cap, ua_combine_group* groups,
+                            int64_t groups_cap);
+
+/*
  * ua_forward -- attention for the batch the plan was built for: the boxed
  * O_{t+1} = softmax(q K^T) V equation of "flashatten takeaways EP2 工程" (kv
  * cache section) over the paged cache, evaluated tile by tile as
@@ -346,6 +386,8 @@ ua_status ua_forward_host(const void* q_host, void* out_host, const int32_t* cu_
  *   ignored).
  * A page id outside [0, num_blocks) (or a position past the page table) is
  * not written; UA_ERR_BOUNDS is recorded in the plan's error word.
+ * On a plan with block scales (ua_plan_set_block_scales) codes and scales are
+ * written by its rule instead.
  * Stream-ordered on `stream`; issue it before ua_forward on the same stream.
  * Returns UA_ERR_INVALID_ARG for null or misaligned pointers, a bad
  * num_blocks or scale, or a stream on another device than the plan's.
@@ -402,6 +444,21 @@ ua_status ua_rope_create(ua_rope** out, int32_t rotary_dim, int32_t layout,
 ua_status ua_rope_destroy(ua_rope* rope);
 
 /*
+ * ua_rope_create_axes -- a rope for positions of several axes (time, height and
+ * width of an image or video patch; text has the same position on all of them):
+ * pair i turns by p[pair_axes_host[i]] w_i. num_axes: 1..UA_ROPE_MAX_AXES;
+ * pair_axes_host: [rotary_dim / 2], each in 0..num_axes - 1, in any order (runs
+ * of pairs for each axis, or the axes in turn). Other arguments and errors as
+ * ua_rope_create. ua_rope_get_axes: a rope's number of axes (1 from
+ * ua_rope_create).
+ */
+#define UA_ROPE_MAX_AXES 4
+ua_status ua_rope_create_axes(ua_rope** out, int32_t rotary_dim, int32_t layout,
+                              const double* inv_freq_host, float amplitude, int32_t num_axes,
+                              const int32_t* pair_axes_host);
+ua_status ua_rope_get_axes(const ua_rope* rope, int32_t* num_axes);
+
+/*
  * ua_rope_append_kv -- ua_append_kv with rotary positions: rotates the step's
  * queries and new keys, leaves the queries in q_out (for ua_forward) and
  * writes keys and values into the paged cache, in one launch.
@@ -416,7 +473,9 @@ ua_status ua_rope_destroy(ua_rope* rope);
  *   NULL: the token's logical position in the cache, kv_len - q_len + i.
  *   (Positions differ from it when, say, older tokens were dropped from the
  *   cache.) They only enter the angle; any value is allowed. The angle's
- *   error stays below 2^-22 of a turn for |position| up to 2^24.
+ *   error stays below 2^-22 of a turn for |position| up to 2^24. A rope of
+ *   several axes takes NULL here (every axis at the logical position), or its
+ *   positions through ua_rope_append_kv_axes.
  * k_cache, v_cache, block_tables, num_blocks, k_scale, v_scale: as for
  *   ua_append_kv, but the scales of an e4m3 cache are normal numbers. The
  *   rotated key is rounded once: to bf16, or as e4m3(k' / k_scale) from the
@@ -436,6 +495,19 @@ ua_status ua_rope_append_kv(const ua_plan* plan, const ua_rope* rope, const void
                             void* v_cache, const int32_t* block_tables, int64_t num_blocks,
                             const int32_t* positions, float k_scale, float v_scale,
                             ua_stream_t stream);
+
+/*
+ * ua_rope_append_kv_axes -- the same with a position of each axis of the rope:
+ * positions: device int32, the position of token j on axis a at
+ *   positions[a * positions_stride + j] (positions_stride >= total_q; with one
+ *   axis it is not used), or NULL: the logical position on every axis.
+ */
+ua_status ua_rope_append_kv_axes(const ua_plan* plan, const ua_rope* rope, const void* q,
+                                 int64_t q_stride, const void* k_new, int64_t k_stride,
+                                 const void* v_new, int64_t v_stride, void* q_out, void* k_cache,
+                                 void* v_cache, const int32_t* block_tables, int64_t num_blocks,
+                                 const int32_t* positions, int64_t positions_stride, float k_scale,
+                                 float v_scale, ua_stream_t stream);
 
 /* Counts and sizes of a plan (host memory only). */
 ua_status ua_plan_get_info(const ua_plan* plan, ua_plan_info* info);
@@ -525,6 +597,47 @@ ua_status ua_plan_set_prefill_ctas(ua_plan* plan, int32_t num_ctas);
 #define UA_MAX_SOFTCAP 4096.f
 ua_status ua_plan_set_scores(ua_plan* plan, float softcap, const float* alibi_slopes);
 
+/* Block scales of an e4m3 cache, for later calls on this plan: the key of
+ * physical block b, slot t and KV head g is code * k_scales[b * num_kv_heads + g]
+ * and its value code * v_scales[...]; the k_scale and v_scale arguments of those
+ * calls are ignored.
+ * k_scales, v_scales: device float [num_blocks][num_kv_heads] on the plan's
+ *   device, two arrays that do not overlap; or both NULL: one scale per
+ *   tensor again. Not copied: the caller keeps them until the last call that
+ *   uses them (or graph that captured one) has run. num_blocks: as the calls'
+ *   (another one is refused there).
+ * ua_forward reads scales of the blocks whose keys it reads: normal positive
+ *   numbers, any from UA_MIN_BLOCK_SCALE to UA_MAX_BLOCK_SCALE (else the rows
+ *   that see the block are undefined). Decode tiles apply them in binary32.
+ *   Prefill tiles read a staged copy code * scale rounded to bf16, exact for
+ *   powers of two; they have no fp8 products.
+ * ua_append_kv, ua_rope_append_kv and ua_rope_append_kv_axes set the scales of
+ *   the blocks they write to. With A the largest finite magnitude among the
+ *   step's new elements of a block and head (keys after their rotation, in
+ *   binary32):
+ *     first new slot 0: scale = 2^k, the least k with A <= 448 2^k, within the
+ *       two limits (UA_MIN_BLOCK_SCALE for nothing but zeros);
+ *     else: scale = old 2^n, the least n >= 0 with A <= 448 old 2^n (448 old
+ *       rounded to binary32; the upper limit holds), and the codes of the
+ *       earlier slots are divided by 2^n, rounded to nearest even (exact but for
+ *       subnormal codes). An old scale outside the limits counts as none: the
+ *       first rule, with the earlier codes as they are.
+ *   code = e4m3(x / scale) as ua_rope_append_kv rounds. Codes and scales depend
+ *   on how a block's tokens are shared out over steps, and on nothing else; the
+ *   same step again changes nothing. A block is written by one sequence of a
+ *   step (as ever), and slots behind the new tokens stay as they are.
+ * May be called while a stream is being captured; nothing of it is captured.
+ * ua_forward_oneshot, ua_forward_host and ua_forward_static_scratch, which take
+ * no plan, have one scale per tensor.
+ * Returns UA_ERR_UNSUPPORTED for a bf16 cache or a plan with fp8 products (which
+ * a plan with block scales refuses in turn), UA_ERR_INVALID_ARG for a null plan,
+ * one array alone, arrays that overlap, a bad num_blocks, or memory that is
+ * misaligned or not of the plan's device. After an error the plan is as it was. */
+#define UA_MIN_BLOCK_SCALE 7.888609052210118e-31f /* 2^-100 */
+#define UA_MAX_BLOCK_SCALE 1.2676506002282294e30f /* 2^100 */
+ua_status ua_plan_set_block_scales(ua_plan* plan, float* k_scales, float* v_scales,
+                                   int64_t num_blocks);
+
 /* fp8 tensor-core products for the prefill tiles of an fp8 (e4m3) cache:
  * the low-precision path of the "Fused Attention" notes (Q.K^T on fp8
  * operands, P cast to fp8 ahead of P.V; the block-quantised FP8 path of
@@ -538,7 +651,7 @@ ua_status ua_plan_set_scores(ua_plan* plan, float softcap, const float* alibi_sl
  * cache; decode tiles keep their f16 products. enable = 0 restores the
  * staged path. Returns UA_ERR_UNSUPPORTED unless the plan has an e4m3 cache,
  * head_dim 128, 128 % qpk == 0 and a block size that divides or is divided
- * by 128 (and at least 16); UA_ERR_INVALID_ARG for a null plan or an enable
+ * by 128 (and at least 16), and no block scales; UA_ERR_INVALID_ARG for a null plan or an enable
  * other than 0 / 1. */
 ua_status ua_plan_set_fp8_products(ua_plan* plan, int32_t enable);
 

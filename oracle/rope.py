@@ -6,6 +6,7 @@ is the complex number a + ib turned by p w and stretched by the amplitude:
 
   a' + i b' = m e^{i p w} (a + i b)
 
+(with positions of several axes: p the position on the pair's axis)
 over the pairs (x[i], x[i + rotary_dim / 2]) (half layout) or (x[2i], x[2i + 1])
 (interleaved), i < rotary_dim / 2; elements from rotary_dim on are unchanged.
 Frequencies of a configuration with context length L stretched by `factor`:
@@ -25,14 +26,18 @@ import math
 import numpy as np
 
 
-def rotate(x: np.ndarray, positions, inv_freq, interleaved: bool, amplitude: float = 1.0) -> np.ndarray:
-    """x [tokens, heads, d] (any float type) rotated, in binary64."""
+def rotate(x: np.ndarray, positions, inv_freq, interleaved: bool, amplitude: float = 1.0,
+           pair_axes=None) -> np.ndarray:
+    """x [tokens, heads, d] (any float type) rotated, in binary64. pair_axes: the
+    axis of each pair, of positions [axes, tokens]."""
     y = np.array(x, dtype=np.float64)
     w = np.asarray(inv_freq, dtype=np.float64)
     n = w.size
     a = np.arange(n) * 2 if interleaved else np.arange(n)
     b = a + 1 if interleaved else a + n
-    angle = np.asarray(positions, dtype=np.float64)[:, None] * w[None, :]
+    p = np.asarray(positions, dtype=np.float64)
+    p = p[:, None] if pair_axes is None else p[np.asarray(pair_axes)].T  # [tokens, 1 or pairs]
+    angle = p * w[None, :]
     turn = amplitude * np.exp(1j * angle)[:, None, :]
     z = (y[..., a] + 1j * y[..., b]) * turn
     y[..., a], y[..., b] = z.real, z.imag

@@ -36,6 +36,9 @@ UA_ROPE_LINEAR = 1
 UA_ROPE_NTK = 2
 UA_ROPE_BANDS = 3
 UA_ROPE_YARN = 4
+UA_ROPE_MAX_AXES = 4
+UA_MIN_BLOCK_SCALE = 2.0 ** -100
+UA_MAX_BLOCK_SCALE = 2.0 ** 100
 
 # Every symbol include/ua.h declares.
 EXPORTS = (
@@ -46,6 +49,8 @@ EXPORTS = (
     "ua_plan_set_unified_max", "ua_plan_set_prefill_ctas", "ua_plan_set_fp8_products", "ua_forward_host",
     "ua_rope_frequencies", "ua_rope_create", "ua_rope_destroy", "ua_rope_append_kv",
     "ua_plan_set_scores", "ua_plan_create_prefix", "ua_schedule_prefix", "ua_plan_get_batch",
+    "ua_plan_create_sinks", "ua_schedule_sinks", "ua_rope_create_axes", "ua_rope_get_axes",
+    "ua_rope_append_kv_axes", "ua_plan_set_block_scales",
 )
 
 
@@ -112,6 +117,19 @@ _SIGS = {
                                   _I32, _I32, _I32, _I32, ctypes.POINTER(ua_plan_info),
                                   ctypes.POINTER(ua_tile), _I64, ctypes.POINTER(ua_tile), _I64,
                                   ctypes.POINTER(ua_combine_group), _I64]),
+    "ua_plan_create_sinks": (_I32, [ctypes.POINTER(_P), _I32P, _I32P, _I32P, _I32, _I32, _I32,
+                                    _I32, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _P]),
+    "ua_schedule_sinks": (_I32, [_I32P, _I32P, _I32P, _I32, _I32, _I32, _I32, _I32, _I32, _I32,
+                                 _I32, _I32, _I32, _I32, _I32, _I32,
+                                 ctypes.POINTER(ua_plan_info), ctypes.POINTER(ua_tile), _I64,
+                                 ctypes.POINTER(ua_tile), _I64,
+                                 ctypes.POINTER(ua_combine_group), _I64]),
+    "ua_rope_create_axes": (_I32, [ctypes.POINTER(_P), _I32, _I32, ctypes.POINTER(_D), _F, _I32,
+                                   _I32P]),
+    "ua_rope_get_axes": (_I32, [_P, _I32P]),
+    "ua_rope_append_kv_axes": (_I32, [_P, _P, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P, _I64,
+                                      _P, _I64, _F, _F, _P]),
+    "ua_plan_set_block_scales": (_I32, [_P, _P, _P, _I64]),
     "ua_plan_get_info": (_I32, [_P, ctypes.POINTER(ua_plan_info)]),
     "ua_plan_get_batch": (_I32, [_P, ctypes.POINTER(_I64), _I32P, _I32P, _I32P]),
     "ua_last_device_error": (_I32, [_P, _I32P]),
@@ -167,23 +185,33 @@ def _prefix_array(prefix_lens, num_seqs, causal):
     return _i32_array(max(-1, min(int(x), 2 ** 31 - 1)) for x in lens)
 
 
+def _sinks(sink_tokens):
+    # 2^31 - 1 is as good as any more; what is negative stays so
+    return max(-1, min(int(sink_tokens), 2 ** 31 - 1))
+
+
 def ua_status_string(status: int) -> str:
     return lib().ua_status_string(int(status)).decode()
 
 
 def ua_schedule(cu_query_lens, kv_lens, num_q_heads, num_kv_heads, head_dim, block_size,
                 max_blocks_per_seq, kv_dtype=UA_KV_BF16, causal=1, window=0, num_splits=0,
-                num_sms=152, decode_rows_max=-1, prefix_lens=None):
+                num_sms=152, decode_rows_max=-1, prefix_lens=None, sink_tokens=0):
     """Run the CPU scheduler alone; returns (info, prefill, decode, groups) as
-    lists of dicts. prefix_lens: a prefix mask (ua_schedule_prefix). Raises
-    UAError on a rejected problem."""
+    lists of dicts. prefix_lens: a prefix mask (ua_schedule_prefix);
+    sink_tokens: first keys that stay visible under the window
+    (ua_schedule_sinks). Raises UAError on a rejected problem."""
     cu, kv = _i32_array(cu_query_lens), _i32_array(kv_lens)
     n = len(list(kv_lens))
     info = ua_plan_info()
     args = (cu, kv, n, num_q_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq,
             kv_dtype, causal, window, num_splits, num_sms, decode_rows_max)
     fn = lib().ua_schedule
-    if prefix_lens is not None:
+    if sink_tokens:
+        prefix = None if prefix_lens is None else _prefix_array(prefix_lens, n, causal)
+        args = (cu, kv, prefix) + args[2:11] + (_sinks(sink_tokens),) + args[11:]
+        fn = lib().ua_schedule_sinks
+    elif prefix_lens is not None:
         args = (cu, kv, _prefix_array(prefix_lens, n, causal)) + args[2:9] + args[10:]
         fn = lib().ua_schedule_prefix
     _check(fn(*args, ctypes.byref(info), None, 0, None, 0, None, 0), "ua_schedule")
@@ -211,13 +239,22 @@ def _stream_handle(stream) -> int:
 
 def ua_plan_create(cu_query_lens, kv_lens, num_q_heads, num_kv_heads, head_dim, block_size,
                    max_blocks_per_seq, kv_dtype=UA_KV_BF16, causal=1, window=0, num_splits=0,
-                   decode_rows_max=-1, stream=None, prefix_lens=None) -> int:
+                   decode_rows_max=-1, stream=None, prefix_lens=None, sink_tokens=0) -> int:
     """Create a plan from host lengths; returns the opaque plan handle.
     prefix_lens: keys of each sequence that all its queries see (a prefix
-    mask, ua_plan_create_prefix)."""
+    mask, ua_plan_create_prefix). sink_tokens: first keys of each sequence that
+    stay visible under the window (ua_plan_create_sinks)."""
     cu, kv = _i32_array(cu_query_lens), _i32_array(kv_lens)
     n = len(list(kv_lens))
     h = ctypes.c_void_p()
+    if sink_tokens:
+        prefix = None if prefix_lens is None else _prefix_array(prefix_lens, n, causal)
+        _check(lib().ua_plan_create_sinks(ctypes.byref(h), cu, kv, prefix, n, num_q_heads,
+                                          num_kv_heads, head_dim, block_size,
+                                          max_blocks_per_seq, kv_dtype, causal, window,
+                                          _sinks(sink_tokens), num_splits, decode_rows_max,
+                                          _stream_handle(stream)), "ua_plan_create_sinks")
+        return h.value
     if prefix_lens is not None:
         _check(lib().ua_plan_create_prefix(ctypes.byref(h), cu, kv,
                                            _prefix_array(prefix_lens, n, causal), n, num_q_heads,
@@ -272,15 +309,35 @@ def ua_rope_frequencies(rotary_dim, base=10000.0, scaling=UA_ROPE_PLAIN, factor=
     return list(w), m.value
 
 
-def ua_rope_create(inv_freq, interleaved=False, amplitude=1.0) -> int:
-    """A rope over 2 * len(inv_freq) elements of each head; returns its handle."""
+def ua_rope_create(inv_freq, interleaved=False, amplitude=1.0, axes=None) -> int:
+    """A rope over 2 * len(inv_freq) elements of each head; returns its handle.
+    axes: the position axis of each pair (0 to the number of axes less one;
+    None: one axis)."""
     w = [float(x) for x in inv_freq]
     h = ctypes.c_void_p()
+    if axes is not None:
+        axes = [int(a) for a in axes]
+        if len(axes) != len(w):
+            raise ValueError(f"axes has {len(axes)} entries for {len(w)} pairs")
+        # (an entry out of range stays so)
+        _check(lib().ua_rope_create_axes(
+            ctypes.byref(h), 2 * len(w), UA_ROPE_INTERLEAVED if interleaved else UA_ROPE_HALF,
+            (ctypes.c_double * max(1, len(w)))(*w), float(amplitude),
+            min(max(axes, default=0) + 1, 2 ** 31 - 1),
+            _i32_array(max(-1, min(a, 2 ** 31 - 1)) for a in axes)), "ua_rope_create_axes")
+        return h.value
     _check(lib().ua_rope_create(ctypes.byref(h), 2 * len(w),
                                 UA_ROPE_INTERLEAVED if interleaved else UA_ROPE_HALF,
                                 (ctypes.c_double * max(1, len(w)))(*w), float(amplitude)),
            "ua_rope_create")
     return h.value
+
+
+def ua_rope_get_axes(rope: int) -> int:
+    """The number of position axes of a rope."""
+    n = ctypes.c_int32(0)
+    _check(lib().ua_rope_get_axes(rope, ctypes.byref(n)), "ua_rope_get_axes")
+    return n.value
 
 
 def ua_rope_destroy(rope: int):
@@ -308,7 +365,9 @@ def ua_rope_append_kv(plan, rope, q, k_new, v_new, q_out, k_cache, v_cache, bloc
     """Rotate the step's q into q_out (q itself: in place), and its new keys
     and values into the paged cache, on `stream`. q, k_new and v_new are
     [tokens, heads, head_dim] CUDA tensors of the plan's heads and at least its
-    tokens, whose token rows may be strided."""
+    tokens, whose token rows may be strided. positions: int32 [tokens], or
+    [axes, tokens] with a row for each axis of the rope (the rows' distance is
+    free)."""
     _rope_append(plan, None, rope, q, k_new, v_new, q_out, k_cache, v_cache, block_tables,
                  num_blocks, positions, k_scale, v_scale, stream)
 
@@ -326,8 +385,18 @@ def _rope_append(plan, batch, rope, q, k_new, v_new, q_out, k_cache, v_cache, bl
     if q_out.shape != shape or q_out.dtype != bf16 or q_out.get_device() != dev or (
             not q_out.is_contiguous()):
         raise ValueError("q_out: a contiguous tensor of q's shape, type and device is needed")
-    pp = None
-    if positions is not None:
+    pp, p_stride = None, 0
+    if positions is not None and positions.dim() == 2:
+        if positions.shape != (ua_rope_get_axes(rope), n) or positions.dtype != torch.int32 or (
+                positions.get_device() != dev or (n > 1 and positions.stride(1) != 1)):
+            raise ValueError("positions: an int32 tensor [axes of the rope, tokens of q] with "
+                             f"contiguous rows, on q's device, is needed ({positions.dtype}, shape "
+                             f"{tuple(positions.shape)}, {ua_rope_get_axes(rope)} axes, {n} tokens)")
+        # (the distance of one row, or of rows of one token, says nothing)
+        pp, p_stride = positions.data_ptr(), positions.stride(0) if len(positions) > 1 else n
+        if p_stride < n:
+            raise ValueError("positions: rows that overlap (expand() gives such; copy them)")
+    elif positions is not None:
         if positions.shape != (n,) or not positions.is_contiguous() or (
                 positions.dtype != torch.int32 or positions.get_device() != dev):
             raise ValueError(f"positions: a contiguous int32 tensor of q's {n} tokens, on its "
@@ -340,6 +409,15 @@ def _rope_append(plan, batch, rope, q, k_new, v_new, q_out, k_cache, v_cache, bl
         raise UAError(UA_ERR_INVALID_ARG, f"ua_rope_append_kv: q {tuple(shape)}, k_new "
                       f"{tuple(k_new.shape)}, v_new {tuple(v_new.shape)} on a plan of {tokens} "
                       f"tokens, {hq} query heads, {hkv} KV heads and head_dim {d}")
+    if p_stride:
+        _check(lib().ua_rope_append_kv_axes(
+            plan, rope, qp, qs, kp, ks, vp, vs, q_out.data_ptr(),
+            k_cache if isinstance(k_cache, int) else k_cache.data_ptr(),
+            v_cache if isinstance(v_cache, int) else v_cache.data_ptr(),
+            block_tables if isinstance(block_tables, int) else block_tables.data_ptr(),
+            int(num_blocks), pp, p_stride, float(k_scale), float(v_scale),
+            _stream_handle(stream)), "ua_rope_append_kv_axes")
+        return
     _check(lib().ua_rope_append_kv(
         plan, rope, qp, qs, kp, ks, vp, vs, q_out.data_ptr(),
         k_cache if isinstance(k_cache, int) else k_cache.data_ptr(),
@@ -451,6 +529,15 @@ def ua_plan_set_scores(plan: int, softcap=0.0, alibi_slopes=None):
            "ua_plan_set_scores")
 
 
+def ua_plan_set_block_scales(plan: int, k_scales=None, v_scales=None, num_blocks=0):
+    """An e4m3 cache's scales of each physical block and KV head (float32 CUDA
+    tensors [num_blocks, num_kv_heads], or raw device pointers; None: one scale
+    per tensor again), for later calls on this plan. They must outlive those."""
+    ptr = lambda t: t if t is None or isinstance(t, int) else t.data_ptr()
+    _check(lib().ua_plan_set_block_scales(plan, ptr(k_scales), ptr(v_scales), int(num_blocks)),
+           "ua_plan_set_block_scales")
+
+
 KERNEL_KINDS = ("prefill", "decode", "combine", "append", "stage")
 
 
@@ -482,19 +569,20 @@ def ua_forward_static_scratch(q, k_cache, v_cache, out, cu_query_lens, kv_lens, 
 
 class Rope:
     """RAII wrapper around a rope: rotary frequencies (radians per position,
-    one per pair), their layout and the amplitude of the rotated pairs."""
+    one per pair), their layout, the amplitude of the rotated pairs, and with
+    positions of several axes the axis of each pair."""
 
-    def __init__(self, inv_freq, interleaved=False, amplitude=1.0):
+    def __init__(self, inv_freq, interleaved=False, amplitude=1.0, axes=None):
         self.handle = None
-        self.handle = ua_rope_create(inv_freq, interleaved, amplitude)
+        self.handle = ua_rope_create(inv_freq, interleaved, amplitude, axes)
 
     @classmethod
     def scaled(cls, rotary_dim, base=10000.0, scaling=UA_ROPE_PLAIN, factor=1.0,
-               original_max_position=0.0, low=1.0, high=4.0, interleaved=False):
+               original_max_position=0.0, low=1.0, high=4.0, interleaved=False, axes=None):
         """The rope of a configuration (ua_rope_frequencies)."""
         w, m = ua_rope_frequencies(rotary_dim, base, scaling, factor, original_max_position,
                                    low, high)
-        return cls(w, interleaved, m)
+        return cls(w, interleaved, m, axes)
 
     def close(self):
         if self.handle:
@@ -519,6 +607,8 @@ class Plan:
 
     _slopes = None  # the forwards read the caller's tensor: kept as long as they may
     _slopes_streams = ()  # streams whose forwards the tensor's memory waits for
+    _scales = ()  # the same of the block scales, which the appends write too
+    _scales_streams = ()
 
     def __init__(self, *args, **kwargs):
         """Arguments as ua_plan_create."""
@@ -536,23 +626,45 @@ class Plan:
         ua_forward(self.handle, q, k_cache, v_cache, out, cu_query_lens, kv_lens, block_tables,
                    num_blocks, max_q, max_kv, scale, k_scale, v_scale, handle)
         if self._slopes is not None and handle not in self._slopes_streams:
-            import torch
-            if stream is None:
-                stream = torch.cuda.current_stream(self._slopes.device)
-            if isinstance(stream, torch.cuda.Stream):  # (a handle says nothing of its stream's life)
-                self._slopes.record_stream(stream)
+            if self._record(stream, self._slopes):
                 self._slopes_streams += (handle,)
+        if self._scales and handle not in self._scales_streams:
+            self._scales_used(stream, handle)
 
-    def append_kv(self, *args, **kwargs):
-        ua_append_kv(self.handle, *args, **kwargs)
+    @staticmethod
+    def _record(stream, *tensors) -> bool:
+        """The tensors' memory waits for the stream's work so far."""
+        import torch
+        if stream is None:
+            stream = torch.cuda.current_stream(tensors[0].device)
+        if not isinstance(stream, torch.cuda.Stream):  # (a handle says nothing of its stream's life)
+            return False
+        for t in tensors:
+            t.record_stream(stream)
+        return True
+
+    def _scales_used(self, stream, handle):
+        if self._record(stream, *self._scales):
+            self._scales_streams += (handle,)
+
+    def append_kv(self, k_new, v_new, k_cache, v_cache, block_tables, num_blocks, k_scale=1.0,
+                  v_scale=1.0, stream=None):
+        handle = _stream_handle(stream)
+        ua_append_kv(self.handle, k_new, v_new, k_cache, v_cache, block_tables, num_blocks,
+                     k_scale, v_scale, handle)
+        if self._scales and handle not in self._scales_streams:
+            self._scales_used(stream, handle)
 
     def rope_append_kv(self, rope, q, k_new, v_new, q_out, k_cache, v_cache, block_tables,
                        num_blocks, positions=None, k_scale=1.0, v_scale=1.0, stream=None):
         if len(q) < self.num_tokens:
             raise ValueError(f"q: {len(q)} tokens, the plan has {self.num_tokens}")
+        handle = _stream_handle(stream)
         _rope_append(self.handle, (self.num_tokens, self.num_q_heads, self.num_kv_heads, self.head_dim),
                      rope.handle if isinstance(rope, Rope) else rope, q, k_new, v_new, q_out, k_cache,
-                     v_cache, block_tables, num_blocks, positions, k_scale, v_scale, stream)
+                     v_cache, block_tables, num_blocks, positions, k_scale, v_scale, handle)
+        if self._scales and handle not in self._scales_streams:
+            self._scales_used(stream, handle)
 
     def set_scores(self, softcap=0.0, alibi_slopes=None):
         """ua_plan_set_scores; the plan holds the tensor until the next call, and
@@ -568,6 +680,26 @@ class Plan:
                              "slopes is needed")
         ua_plan_set_scores(self.handle, softcap, alibi_slopes)
         self._slopes, self._slopes_streams = alibi_slopes, ()
+
+    def set_block_scales(self, k_scales=None, v_scales=None):
+        """ua_plan_set_block_scales, of float32 tensors [num_blocks, num_kv_heads];
+        the plan holds them until the next call, and their memory is not given out
+        again before the plan's calls have run (as set_scores' slopes)."""
+        import torch
+        if (k_scales is None) != (v_scales is None):
+            raise ValueError("block scales: those of the keys and of the values, or neither")
+        if k_scales is None:
+            ua_plan_set_block_scales(self.handle)
+            self._scales = self._scales_streams = ()
+            return
+        for name, x in (("k_scales", k_scales), ("v_scales", v_scales)):
+            if x.dim() != 2 or x.shape[1] != self.num_kv_heads or x.shape != k_scales.shape or (
+                    x.dtype != torch.float32 or not x.is_contiguous()):
+                raise ValueError(f"{name}: a contiguous float32 tensor [num_blocks, "
+                                 f"{self.num_kv_heads}] is needed, the same for both ({x.dtype}, "
+                                 f"shape {tuple(x.shape)}, strides {x.stride()})")
+        ua_plan_set_block_scales(self.handle, k_scales, v_scales, k_scales.shape[0])
+        self._scales, self._scales_streams = (k_scales, v_scales), ()
 
     def last_device_error(self) -> int:
         return ua_last_device_error(self.handle)

@@ -51,7 +51,8 @@ _KERNEL_SOURCES = {
     "prefill": ("prefill.cu",),
     "prefill_wide": ("prefill_wide.cu",),
     "append": ("append.cu",),
-    "rope": ("rope.cu",),
+    "rope": ("rope.cu", "rope_device.cuh"),
+    "fill": ("fill.cu", "rope_device.cuh"),
     "stage": ("stage.cu",),
 }
 _SHARED_SOURCES = ("sm100.cuh", "score_shape.cuh", "ua_device.cuh", "ua_kernels.h", "tma_host.cu", "planner.cpp",

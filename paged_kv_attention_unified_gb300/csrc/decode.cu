@@ -31,6 +31,12 @@
 // leaves its normalised partial and base-2 lse in the workspace; with arrival
 // counters given, the last piece of a group to finish merges the group in the
 // same launch (otherwise the combine kernel does).
+// Over an e4m3 cache with block scales every step lies in one page, so the key
+// scale multiplies the step's scores, and the value scale vs goes into the
+// exponent: with x' = x + log2 vs the weights 2^(x' - m) of the stored codes are
+// what O accumulates, and l accumulates 2^(x' - m) / vs in binary32. One
+// exponential a score as before, and the f16 weights keep the range that they have
+// without scales, whatever the scales of a row's pages.
 #include "score_shape.cuh"
 #include "sm100.cuh"
 #include "ua_device.cuh"
@@ -211,6 +217,7 @@ struct StepMask {
   int last[2];     // last key the causal mask leaves them (pos, or the prefix's last key)
   int causal;
   int window;
+  int sinks;       // (SHAPED instances) keys below it stay visible under the window
   float phi2;      // unified max in log2 units of the scaled score; NaN: off
   // Score shape (SHAPED instances): the cap, 0 for none, with its argument's
   // multiplier, and the distance biases of the two rows.
@@ -218,11 +225,23 @@ struct StepMask {
   RowBias bias[2];
 };
 
-template <int D, bool FP8, bool SHAPED>
+// The block scales of a step's page (SCALED instances): keys, values.
+struct StepScale {
+  float k, v;
+};
+
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <int D, bool FP8, bool SHAPED, bool SCALED>
 __device__ __forceinline__ void compute_step(WarpState<D>& st, StepRegs<D, FP8>& r,
                                              const uint8_t* vp, int kv_hi,
-                                             const uint32_t (&qb)[D / 16][2], const float (&cc)[2],
-                                             const StepMask& mk, int base, int g, int t) {
+                                             const uint32_t (&qb)[D / 16][2], const float (&cq)[2],
+                                             const StepMask& mk, const StepScale& scale, int base,
+                                             int g, int t) {
   using C = DecodeCfg<D, FP8>;
   // S^T = K Q^T for the 16 keys of this step, in two independent accumulation
   // chains (even and odd head-dim chunks) that are added at the end: half the
@@ -241,6 +260,13 @@ __device__ __forceinline__ void compute_step(WarpState<D>& st, StepRegs<D, FP8>&
       a[3] = r.k[1][2 * c + 1];
     }
     mma16816<FP8>(s[c & 1], a, qb[c][0], qb[c][1]);
+  }
+  float cc[2] = {cq[0], cq[1]}, v_log2 = 0.f, v_inv = 1.f;
+  if constexpr (SCALED) {
+    cc[0] *= scale.k;
+    cc[1] *= scale.k;
+    v_log2 = lg2(scale.v);
+    v_inv = rcp_approx(scale.v);
   }
   float x[4];
   x[0] = (s[0][0] + s[1][0]) * cc[0];
@@ -261,6 +287,10 @@ __device__ __forceinline__ void compute_step(WarpState<D>& st, StepRegs<D, FP8>&
       x[e] = fmaf(-b.slope2, static_cast<float>(abs(mk.pos[e & 1] - key) - b.shift), x[e]);
     }
   }
+  if constexpr (SCALED) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] += v_log2;
+  }
   // Masking (a select, so that nothing read from outside the visible set can
   // reach the result) only on steps that straddle a bound.
   if (base < mk.lo_full || base + 16 > mk.hi_full) {
@@ -270,7 +300,7 @@ __device__ __forceinline__ void compute_step(WarpState<D>& st, StepRegs<D, FP8>&
       const int pos = mk.pos[e & 1];
       bool ok = key < mk.kv_hi;
       if (mk.causal) ok = ok && key <= (SHAPED ? mk.last[e & 1] : pos);
-      if (mk.window > 0) ok = ok && key > pos - mk.window;
+      if (mk.window > 0) ok = ok && (key > pos - mk.window || (SHAPED && key < mk.sinks));
       x[e] = ok ? x[e] : -INFINITY;
     }
   }
@@ -305,7 +335,8 @@ __device__ __forceinline__ void compute_step(WarpState<D>& st, StepRegs<D, FP8>&
     alpha[j] = grow ? ex2(st.m[j] - sub) : 1.f;
     p[j] = ex2(x[j] - sub);
     p[j + 2] = ex2(x[j + 2] - sub);
-    st.l[j] = st.l[j] * alpha[j] + p[j] + p[j + 2];
+    if constexpr (SCALED) st.l[j] = fmaf(p[j] + p[j + 2], v_inv, st.l[j] * alpha[j]);
+    else st.l[j] = st.l[j] * alpha[j] + p[j] + p[j + 2];
     st.m[j] = m_use;
   }
   if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
@@ -362,7 +393,7 @@ struct Ring {
   static_assert(kWarps * UA_DECODE_ROWS * (D + 2) * 4 <= kRing, "merge buffers alias the ring");
 };
 
-template <int D, bool FP8, bool SHAPED>
+template <int D, bool FP8, bool SHAPED, bool SCALED>
 __global__ void __launch_bounds__(kThreads, Ring<D, FP8>::kCtasPerSm)
     decode_kernel(const __grid_constant__ CUtensorMap map_k,
                   const __grid_constant__ CUtensorMap map_v, const KernelParams p) {
@@ -485,6 +516,7 @@ __global__ void __launch_bounds__(kThreads, Ring<D, FP8>::kCtasPerSm)
     mk.hi_full = p.causal ? min(kv_hi, min_pos + 1) : kv_hi;
     mk.lo_full = p.window > 0 ? max_pos - p.window + 1 : INT_MIN;
     if constexpr (SHAPED) {
+      mk.sinks = p.shape.sinks;
       const int prefix = p.shape.prefix_lens ? p.shape.prefix_lens[tile.seq] : 0;
       mk.cap_log2 = p.shape.cap_log2;
       mk.cap_arg = p.shape.cap_arg;
@@ -496,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, Ring<D, FP8>::kCtasPerSm)
         if (p.shape.slopes && n < nrows)
           mk.bias[j] = row_bias(
               p.shape.slopes[tile.kv_head * p.qpk + (tile.row0 + n) % p.qpk],
-              p.window > 0 ? min(mk.pos[j], p.window - 1) : mk.pos[j],
+              p.window > 0 && p.shape.sinks <= 0 ? min(mk.pos[j], p.window - 1) : mk.pos[j],
               (p.causal ? min(kv_len - 1, mk.last[j]) : kv_len - 1) - mk.pos[j]);
       }
       if (p.causal) mk.hi_full = min(kv_hi, max(min_pos + 1, prefix));
@@ -513,18 +545,54 @@ __global__ void __launch_bounds__(kThreads, Ring<D, FP8>::kCtasPerSm)
 
   // ---- Stream the key range: warp w takes steps w, w+4, w+8, ...; each step
   // is one TMA box of K and one of V (16 keys of one page) into the warp's ring.
-  const int nsteps = kv_hi > kv_lo ? (kv_hi - kv_lo + 15) / 16 : 0;
+  int nsteps = kv_hi > kv_lo ? (kv_hi - kv_lo + 15) / 16 : 0;
+  int gap_lo = INT_MAX, gap = 0;  // a range that spans the keys behind the sinks passes over them
+  if constexpr (SHAPED) {
+    const KeyGap no_row = key_gap(p.shape.sinks, p.window, ctx + tile.row0 / p.qpk, kKeyStep);
+    if (no_row.hi > no_row.lo && kv_lo < no_row.lo && kv_hi > no_row.hi) {
+      gap_lo = no_row.lo;
+      gap = no_row.hi - no_row.lo;
+      nsteps -= gap / 16;
+    }
+  }
   const int my_n = nsteps > warp ? (nsteps - warp + kWarps - 1) / kWarps : 0;
-  auto step_base = [&](int k) { return kv_lo + 16 * (warp + kWarps * k); };
+  auto step_base = [&](int k) {
+    const int at = kv_lo + 16 * (warp + kWarps * k);
+    return SHAPED && at >= gap_lo ? at + gap : at;
+  };
   uint8_t* ring = dsm + warp * R * RC::kStage;
   uint64_t* wbar = bars + warp * R;
   // Page ids, 32 steps at a time: lane l holds the page of step 32c + l.
+  // SCALED: and the page's scales, of this chunk of steps and of the one before
+  // (a step is computed at most a ring after it was issued). The copy at a refill
+  // waits for loads that are a chunk old; the new ones are waited for by the first
+  // step that needs them.
   int32_t ids = -1;
+  StepScale of_issue{1.f, 1.f}, of_before{1.f, 1.f};
+  int issue_chunk = 0;
   auto refill_ids = [&](int c) {
     const int k = 32 * c + lane;
     ids = k < my_n ? p.block_tables[static_cast<int64_t>(tile.seq) * p.max_blocks_per_seq +
                                     step_base(k) / p.block_size]
                    : -1;
+    if constexpr (SCALED) {
+      of_before = of_issue;
+      issue_chunk = c;
+      of_issue = StepScale{1.f, 1.f};
+      if (ids >= 0 && static_cast<int64_t>(ids) < p.num_blocks) {
+        const int64_t at = static_cast<int64_t>(ids) * p.num_kv_heads + tile.kv_head;
+        of_issue = StepScale{__ldg(p.k_scales + at), __ldg(p.v_scales + at)};
+      }
+    }
+  };
+  auto scale_of = [&](int k) {
+    StepScale s{1.f, 1.f};
+    if constexpr (SCALED) {
+      const bool issued_last = (k >> 5) == issue_chunk;
+      s.k = __shfl_sync(0xffffffffu, issued_last ? of_issue.k : of_before.k, k & 31);
+      s.v = __shfl_sync(0xffffffffu, issued_last ? of_issue.v : of_before.v, k & 31);
+    }
+    return s;
   };
   // Whole-warp call: every lane takes part in the shuffle, lane 0 issues.
   auto issue = [&](int k) {
@@ -565,7 +633,8 @@ __global__ void __launch_bounds__(kThreads, Ring<D, FP8>::kCtasPerSm)
       const uint8_t* vstage = stage + 16 * RC::kRowBytes;
       read_k<D, FP8>(r, stage, step_base(done), kv_hi, g, t);
       if constexpr (!kLateV<D>) read_v<D, FP8>(r, vstage, step_base(done), kv_hi, g, t);
-      compute_step<D, FP8, SHAPED>(st_state, r, vstage, kv_hi, qb, cc, mk, step_base(done), g, t);
+      compute_step<D, FP8, SHAPED, SCALED>(st_state, r, vstage, kv_hi, qb, cc, mk, scale_of(done),
+                                           step_base(done), g, t);
       __syncwarp();  // every lane has consumed the stage: it may be refilled
       if (issued < my_n) {
         if ((issued & 31) == 0) refill_ids(issued >> 5);
@@ -732,7 +801,7 @@ __global__ void __launch_bounds__(kThreads, Ring<D, FP8>::kCtasPerSm)
   stamp_end();
 }
 
-template <int D, bool FP8, bool SHAPED>
+template <int D, bool FP8, bool SHAPED, bool SCALED = false>
 cudaError_t launch_decode_as(const KernelParams& p, cudaStream_t stream, bool after_prefill) {
   CUtensorMap mk, mv;
   const int elt = FP8 ? 1 : 2;
@@ -746,10 +815,10 @@ cudaError_t launch_decode_as(const KernelParams& p, cudaStream_t stream, bool af
                            PL::kBoxDims, 16, PL::kSwizzle);
   if (e != cudaSuccess) return e;
   static std::atomic<uint64_t> smem_set{0};
-  e = set_smem_once(decode_kernel<D, FP8, SHAPED>, Ring<D, FP8>::kAlloc, smem_set);
+  e = set_smem_once(decode_kernel<D, FP8, SHAPED, SCALED>, Ring<D, FP8>::kAlloc, smem_set);
   if (e != cudaSuccess) return e;
   if (!after_prefill) {
-    decode_kernel<D, FP8, SHAPED>
+    decode_kernel<D, FP8, SHAPED, SCALED>
         <<<p.num_tiles, kThreads, Ring<D, FP8>::kAlloc, stream>>>(mk, mv, p);
     return cudaGetLastError();
   }
@@ -763,11 +832,17 @@ cudaError_t launch_decode_as(const KernelParams& p, cudaStream_t stream, bool af
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_kernel<D, FP8, SHAPED>, mk, mv, p);
+  return cudaLaunchKernelEx(&cfg, decode_kernel<D, FP8, SHAPED, SCALED>, mk, mv, p);
 }
 
 template <int D, bool FP8>
 cudaError_t launch_decode_d(const KernelParams& p, cudaStream_t stream, bool after_prefill) {
+  if constexpr (FP8) {
+    if (p.k_scales != nullptr)
+      return shape_of(p.shape) == kShapePlain
+                 ? launch_decode_as<D, FP8, false, true>(p, stream, after_prefill)
+                 : launch_decode_as<D, FP8, true, true>(p, stream, after_prefill);
+  }
   return shape_of(p.shape) == kShapePlain ? launch_decode_as<D, FP8, false>(p, stream, after_prefill)
                                           : launch_decode_as<D, FP8, true>(p, stream, after_prefill);
 }

@@ -18,7 +18,8 @@ inline int64_t round_down(int64_t a, int64_t b) { return (a / b) * b; }
 // mask it sees keys up to pos and those below the sequence's prefix length,
 // with a window only keys above pos - window.
 // lo is rounded down to the 16-token step; the kernels mask what lies below
-// the true bound.
+// the true bound. With sinks the range starts at key 0, with a gap (key_gap)
+// between them and the window.
 void key_range(const Problem& p, int32_t seq, int32_t ctx, int32_t kv_len, int32_t row0,
                int32_t nrows, int32_t* lo, int32_t* hi) {
   const int qpk = p.num_q_heads / p.num_kv_heads;
@@ -27,11 +28,16 @@ void key_range(const Problem& p, int32_t seq, int32_t ctx, int32_t kv_len, int32
   const int64_t prefix = p.prefix_lens ? p.prefix_lens[seq] : 0;
   int64_t h = p.causal ? std::min<int64_t>(kv_len, std::max(max_pos + 1, prefix)) : kv_len;
   int64_t l = 0;
-  if (p.window > 0) l = std::max<int64_t>(0, min_pos - p.window + 1);
+  if (p.window > 0 && p.sinks <= 0) l = std::max<int64_t>(0, min_pos - p.window + 1);
   l = round_down(l, kKeyStep);
   if (h < l) h = l;
   *lo = static_cast<int32_t>(l);
   *hi = static_cast<int32_t>(h);
+}
+
+// The gap of the packed rows from row0 on of a sequence with ctx earlier keys.
+KeyGap gap_of(const Problem& p, int32_t ctx, int32_t row0, int32_t step) {
+  return key_gap(p.sinks, p.window, ctx + row0 / (p.num_q_heads / p.num_kv_heads), step);
 }
 
 // Piece length for decode tiles of (nearly) one key length L: with pieces of
@@ -56,10 +62,15 @@ int64_t wave_fit_chunk(int64_t tiles, int64_t len, int64_t slots) {
   return best_size;
 }
 
-// Work of a tile: keys read x packed rows.
-inline int64_t work_of(const ua_tile& t) {
-  return static_cast<int64_t>(t.kv_hi - t.kv_lo) * t.nrows;
+// Keys a prefill tile reads.
+inline int64_t keys_of(const Problem& p, const ua_tile& t) {
+  const int32_t ctx = p.kv_lens[t.seq] - (p.cu_query_lens[t.seq + 1] - p.cu_query_lens[t.seq]);
+  const KeyGap gap = gap_of(p, ctx, t.row0, kPrefillKeyTile);
+  return static_cast<int64_t>(t.kv_hi - t.kv_lo) - (gap.hi - gap.lo);
 }
+
+// Work of a prefill tile: keys read x packed rows.
+inline int64_t work_of(const Problem& p, const ua_tile& t) { return keys_of(p, t) * t.nrows; }
 
 // Indices 0..n-1 ordered by the keys (a, b, c) ascending, ties by index: a
 // stable sort on precomputed keys (the lists are generated in (sequence, KV
@@ -100,6 +111,7 @@ ua_status validate(const Problem& p) {
   if (p.num_splits < 0 || p.num_splits > UA_MAX_SPLITS) return UA_ERR_INVALID_ARG;
   if (p.causal != 0 && p.causal != 1) return UA_ERR_INVALID_ARG;
   if (p.prefix_lens && p.causal == 0) return UA_ERR_INVALID_ARG;  // every key is visible already
+  if (p.sinks < 0) return UA_ERR_INVALID_ARG;
   if (p.num_seqs > 0 && (p.cu_query_lens == nullptr || p.kv_lens == nullptr))
     return UA_ERR_INVALID_ARG;
   if (p.head_dim < 32 || p.head_dim > 256 || p.head_dim % 32 != 0) return UA_ERR_UNSUPPORTED;
@@ -129,7 +141,7 @@ bool padded_prefill_pays(const Problem& p) {
     const int64_t ql = p.cu_query_lens[q + 1] - p.cu_query_lens[q];
     if (ql * qpk <= kDefaultDecodeRowsMax) continue;
     int64_t keys = p.kv_lens[q];
-    if (p.window > 0) keys = std::min<int64_t>(keys, static_cast<int64_t>(p.window) + ql);
+    if (p.window > 0) keys = std::min<int64_t>(keys, static_cast<int64_t>(p.window) + ql + p.sinks);
     tile_keys += static_cast<double>(ceil_div(ql * qpk, UA_DECODE_ROWS) * p.num_kv_heads * keys);
   }
   return tile_keys / std::min(31.0, 1900.0 / p.head_dim) > 22e3;
@@ -160,6 +172,15 @@ ua_status build_schedule(const Problem& p, Schedule* out) {
   // order).
   struct DecodeBlock {
     int32_t seq, row0, nrows, kv_lo, kv_hi;
+    KeyGap gap;
+    int64_t keys() const { return kv_hi - kv_lo - (gap.hi - gap.lo); }
+    // Position of the block's n-th key, as the first of a piece and as the end of one.
+    int32_t first_at(int64_t n) const {
+      return static_cast<int32_t>(kv_lo + n + (kv_lo + n < gap.lo ? 0 : gap.hi - gap.lo));
+    }
+    int32_t end_at(int64_t n) const {
+      return static_cast<int32_t>(kv_lo + n + (kv_lo + n <= gap.lo ? 0 : gap.hi - gap.lo));
+    }
   };
   std::vector<DecodeBlock> blocks;
   std::vector<int32_t> span_end;  // per decode sequence: end of its blocks
@@ -201,6 +222,7 @@ ua_status build_schedule(const Problem& p, Schedule* out) {
         b.row0 = static_cast<int32_t>(r0);
         b.nrows = static_cast<int32_t>(std::min<int64_t>(UA_DECODE_ROWS, rows - r0));
         key_range(p, q, ctx, kv, b.row0, b.nrows, &b.kv_lo, &b.kv_hi);
+        b.gap = gap_of(p, ctx, b.row0, kKeyStep);
         blocks.push_back(b);
       }
       span_end.push_back(static_cast<int32_t>(blocks.size()));
@@ -248,15 +270,38 @@ ua_status build_schedule(const Problem& p, Schedule* out) {
     }
   }
 
+  // Fill tiles: each sequence's new tokens by the page they go to.
+  if (p.kv_dtype == UA_KV_FP8_E4M3) {
+    for (int32_t q = 0; q < p.num_seqs; ++q) {
+      const int32_t q0 = p.cu_query_lens[q];
+      const int32_t ql = p.cu_query_lens[q + 1] - q0;
+      const int32_t ctx = p.kv_lens[q] - ql;
+      for (int32_t j = 0; j < ql;) {
+        ua_tile t;
+        t.seq = q;
+        t.kv_head = 0;
+        t.row0 = q0 + j;
+        t.nrows = std::min(p.block_size - (ctx + j) % p.block_size, ql - j);
+        t.kv_lo = ctx + j;
+        t.kv_hi = t.kv_lo + t.nrows;
+        t.slot = -1;
+        t.group = -1;
+        s.fill.push_back(t);
+        s.fill_rows = std::max(s.fill_rows, t.nrows);
+        j += t.nrows;
+      }
+    }
+  }
+
   // 2. Split-KV for decode tiles (FlashDecoding): one chunk length C for the
   // whole batch, so that pieces are equal-sized and load-balance well.
   const int64_t heads = p.num_kv_heads;
   const int64_t n_tiles = static_cast<int64_t>(blocks.size()) * heads;
   int64_t total = 0, longest = 0, shortest = INT64_MAX;
   for (const DecodeBlock& b : blocks) {
-    total += (b.kv_hi - b.kv_lo) * heads;
-    longest = std::max<int64_t>(longest, b.kv_hi - b.kv_lo);
-    shortest = std::min<int64_t>(shortest, b.kv_hi - b.kv_lo);
+    total += b.keys() * heads;
+    longest = std::max(longest, b.keys());
+    shortest = std::min(shortest, b.keys());
   }
   int64_t chunk = 0;  // 0: do not split
   const int64_t slots = static_cast<int64_t>(num_sms) * decode_ctas_per_sm(p.head_dim, p.kv_dtype == UA_KV_BF16 ? 2 : 1);
@@ -298,7 +343,7 @@ ua_status build_schedule(const Problem& p, Schedule* out) {
   const size_t nb = blocks.size();
   std::vector<Cut> plan(nb), late_plan(tail_k > 0 ? nb : 0);
   for (size_t i = 0; i < nb; ++i) {
-    const int64_t len = blocks[i].kv_hi - blocks[i].kv_lo;
+    const int64_t len = blocks[i].keys();
     if (p.num_splits > 0)
       plan[i] = cut(len, std::max<int64_t>(1, std::min<int64_t>(p.num_splits, ceil_div(len, kKeyStep))));
     else if (chunk > 0 && len > chunk)
@@ -319,7 +364,7 @@ ua_status build_schedule(const Problem& p, Schedule* out) {
   // work of a full piece and of the last piece of a tile of block b cut by c
   auto whole_work = [](const DecodeBlock& b, const Cut& c) { return c.size * b.nrows; };
   auto last_work = [](const DecodeBlock& b, const Cut& c) {
-    return (b.kv_hi - b.kv_lo - (c.pieces - 1) * c.size) * b.nrows;
+    return (b.keys() - (c.pieces - 1) * c.size) * b.nrows;
   };
   std::vector<int64_t> works;
   works.reserve(4 * nb);
@@ -429,12 +474,11 @@ ua_status build_schedule(const Problem& p, Schedule* out) {
         grp.nsplits = static_cast<int32_t>(c.pieces);
         grp.pad0 = grp.pad1 = 0;
         t.group = gid++;
-        const int32_t size = static_cast<int32_t>(c.size);
         for (int64_t k = 0; k + 1 < c.pieces; ++k) {
-          t.kv_hi = t.kv_lo + size;
+          t.kv_hi = b.end_at((k + 1) * c.size);
           t.slot = slot++;
           out_tiles[at[r.whole]++] = t;
-          t.kv_lo = t.kv_hi;
+          t.kv_lo = b.first_at((k + 1) * c.size);
         }
         t.kv_hi = b.kv_hi;
         t.slot = slot++;
@@ -454,18 +498,20 @@ ua_status build_schedule(const Problem& p, Schedule* out) {
     auto gi = [&](const ua_tile& t) {
       return static_cast<size_t>(t.seq) * p.num_kv_heads + t.kv_head;
     };
-    for (const ua_tile& t : s.prefill) group_work[gi(t)] += work_of(t);
+    for (const ua_tile& t : s.prefill) group_work[gi(t)] += work_of(p, t);
     std::vector<SortKey> keys(s.prefill.size());
     for (size_t i = 0; i < s.prefill.size(); ++i) {
       const ua_tile& t = s.prefill[i];
-      keys[i] = {-group_work[gi(t)], static_cast<int64_t>(gi(t)), -work_of(t),
+      keys[i] = {-group_work[gi(t)], static_cast<int64_t>(gi(t)), -work_of(p, t),
                  static_cast<int32_t>(i)};
     }
     permute(s.prefill, order_by(keys));
   }
   // Staging pages for an fp8 cache: per sequence with prefill tiles, the
   // logical pages of kStagePage keys from the lowest key any of its tiles
-  // reads to its last key.
+  // reads to its last key, but for those in the gap of its first tile (the
+  // others' gaps hold it). slot and group of a stage tile: the keys [slot, group)
+  // are seen by no query (their pages may be gone; zeros are staged).
   if (p.prefill_staged && !s.prefill.empty()) {
     std::vector<int64_t> lo(p.num_seqs, INT64_MAX);
     for (const ua_tile& t : s.prefill) lo[t.seq] = std::min<int64_t>(lo[t.seq], t.kv_lo);
@@ -480,7 +526,10 @@ ua_status build_schedule(const Problem& p, Schedule* out) {
     for (int32_t q = 0; q < p.num_seqs; ++q) {
       if (lo[q] == INT64_MAX) continue;
       const int64_t pages = ceil_div(p.kv_lens[q], kStagePage);
+      const int32_t ctx = p.kv_lens[q] - (p.cu_query_lens[q + 1] - p.cu_query_lens[q]);
+      const KeyGap gap = gap_of(p, ctx, 0, kStagePage), unseen = gap_of(p, ctx, 0, 1);
       for (int64_t i = lo[q] / kStagePage; i < pages; ++i) {
+        if (i * kStagePage >= gap.lo && i * kStagePage < gap.hi) continue;
         s.staged_table[static_cast<size_t>(q) * max_pages + i] = static_cast<int32_t>(next);
         ua_tile t;
         t.seq = q;
@@ -489,8 +538,8 @@ ua_status build_schedule(const Problem& p, Schedule* out) {
         t.nrows = static_cast<int32_t>(i);
         t.kv_lo = static_cast<int32_t>(i * kStagePage);
         t.kv_hi = static_cast<int32_t>(std::min<int64_t>(p.kv_lens[q], (i + 1) * kStagePage));
-        t.slot = -1;
-        t.group = -1;
+        t.slot = unseen.lo;
+        t.group = unseen.hi;
         s.stage.push_back(t);
         ++next;
       }
@@ -515,11 +564,13 @@ ua_status build_schedule(const Problem& p, Schedule* out) {
         const int32_t rows = std::min(kPrefillQueryTile, t.row0 + t.nrows - r0);
         key_range(p, t.seq, p.kv_lens[t.seq] - ql, p.kv_lens[t.seq], r0, rows, &lo, &hi);
         cost[i] += ceil_div(std::max<int64_t>(0, hi - t.kv_lo), kPrefillKeyTile);
+        cost[i] -= (t.kv_hi - t.kv_lo - keys_of(p, t)) / kPrefillKeyTile;
       }
       total_cost += cost[i];
     }
     int32_t longest = 0;
-    for (const ua_tile& t : s.prefill) longest = std::max(longest, t.kv_hi - t.kv_lo);
+    for (const ua_tile& t : s.prefill)
+      longest = std::max(longest, static_cast<int32_t>(keys_of(p, t)));
     const bool by_length = s.decode.empty() && (longest < kPrefillLongKeys ||
                                                 prefill_kv_bytes(p) <= kPrefillResidentBytes);
     const double tail_share = by_length ? 1.0 : kPrefillTailShare;

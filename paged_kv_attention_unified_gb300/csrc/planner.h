@@ -28,6 +28,7 @@ struct Problem {
   int32_t kv_dtype = UA_KV_BF16;
   int32_t causal = 1;
   int32_t window = 0;
+  int32_t sinks = 0;            // first keys that stay visible under the window
   int32_t num_splits = 0;       // 0: automatic
   int32_t num_sms = 152;
   int32_t decode_rows_max = -1; // < 0: default
@@ -61,12 +62,29 @@ struct Schedule {
   // sequence: seq, row0 = first token (row of k_new), nrows = tokens,
   // kv_lo = logical cache position of the first token, kv_hi = kv_lo + nrows.
   std::vector<ua_tile> append;
+  // fp8 caches, append with block scales: the new tokens of one page, fields as
+  // the append tiles'; the most tokens of one.
+  std::vector<ua_tile> fill;
+  int32_t fill_rows = 0;
   std::vector<ua_combine_group> groups;
   int64_t num_slots = 0;
   int32_t split_tokens = 0;
   int32_t max_q = 0;
   int32_t max_kv = 0;
 };
+
+// The keys between the sinks and a window that no row from position min_pos on
+// sees, in whole steps of `step` keys: [lo, hi), empty (lo == hi) without sinks.
+// A tile's key range [kv_lo, kv_hi) has them in it; the kernels, which find them
+// the same way, and the scheduler's work counts pass over them.
+struct KeyGap {
+  int32_t lo, hi;
+};
+constexpr KeyGap key_gap(int32_t sinks, int32_t window, int32_t min_pos, int32_t step) {
+  if (sinks <= 0 || window <= 0 || min_pos - window + 1 <= sinks) return {0, 0};
+  const int32_t lo = (sinks + step - 1) / step * step, hi = (min_pos - window + 1) / step * step;
+  return hi > lo ? KeyGap{lo, hi} : KeyGap{0, 0};
+}
 
 // Granularity of key ranges: one decode step reads 16 tokens, so split pieces
 // and decode ranges start on multiples of 16.

@@ -34,6 +34,7 @@
 // MMAs in flight and frees the tensor memory before the CTA exits.
 #include <cuda.h>
 
+#include "planner.h"
 #include "score_shape.cuh"
 #include "sm100.cuh"
 #include "ua_device.cuh"
@@ -64,7 +65,7 @@ constexpr float kRescaleThreshold = 8.0f;  // log2 units
 // next tile only when every role has started the current one, which keeps
 // the claims close to the order in which the CTAs run dry.
 constexpr int kItemSlots = 1;
-constexpr int kItemBytes = 64;  // one descriptor in shared memory
+constexpr int kItemBytes = 80;  // one descriptor in shared memory
 // Arrivals that free a descriptor slot: the two producer threads, the MMA
 // thread and the eight softmax warps (one lane each).
 constexpr int kItemConsumers = 3 + 8;
@@ -142,6 +143,11 @@ struct Geometry {
   int rows[kTilesPerCta];    // valid rows of each query tile
   int ntiles[kTilesPerCta];  // key tiles each query tile needs
   int nmax;                  // key tiles loaded
+  int nsink, skip;           // key tiles before the keys that no row sees, and how many those are
+  // First key of key tile j.
+  __device__ __forceinline__ int key_of(int j) const {
+    return kv_lo + j * kKeys + (j >= nsink ? skip : 0);
+  }
 };
 
 // One work tile as the scheduler warp hands it to the other roles.
@@ -164,6 +170,9 @@ __device__ __forceinline__ Geometry geometry_of(const PrefillParams& p, const ua
   g.kv_hi = min(min(tile.kv_hi, kv_len), p.max_blocks_per_seq * p.block_size);
   g.kv_lo = tile.kv_lo;
   g.prefix = p.shape.prefix_lens ? p.shape.prefix_lens[tile.seq] : 0;
+  const KeyGap gap = key_gap(p.shape.sinks, p.window, g.ctx + tile.row0 / p.qpk, kKeys);
+  g.nsink = gap.lo / kKeys;
+  g.skip = gap.hi - gap.lo;
   g.nmax = 0;
 #pragma unroll
   for (int t = 0; t < kTilesPerCta; ++t) {
@@ -173,7 +182,7 @@ __device__ __forceinline__ Geometry geometry_of(const PrefillParams& p, const ua
       const int last = tile.row0 + t * kRows + g.rows[t] - 1;
       const int hi =
           p.causal ? min(g.kv_hi, max(g.ctx + last / p.qpk + 1, g.prefix)) : g.kv_hi;
-      g.ntiles[t] = hi > g.kv_lo ? (hi - g.kv_lo + kKeys - 1) / kKeys : 0;
+      g.ntiles[t] = hi > g.kv_lo + g.skip ? (hi - g.kv_lo - g.skip + kKeys - 1) / kKeys : 0;
     }
     g.nmax = max(g.nmax, g.ntiles[t]);
   }
@@ -242,7 +251,9 @@ __device__ __forceinline__ bool take_item(const PrefillParams& p, const Bars<D, 
 // Key tile j of a work tile into one ring slot: one TMA box per page (or per
 // 128 rows of a larger page) and 64-wide panel. Every page id is read from
 // the block table and checked; a missing or out-of-range page is loaded from
-// an out-of-range block coordinate, which TMA fills with zeros.
+// an out-of-range block coordinate, which TMA fills with zeros. So is one
+// whose keys lie between the sinks and the first query's window: a session may
+// have given such pages back.
 template <int D, bool F8>
 __device__ __forceinline__ void load_key_tile(const CUtensorMap* map, const PrefillParams& p,
                                               const Item& tile, const Geometry& g, int j,
@@ -250,7 +261,7 @@ __device__ __forceinline__ void load_key_tile(const CUtensorMap* map, const Pref
   using L = Smem<D, F8>;
   constexpr int kPanels = L::kPanels;
   const int boxes = kKeys / p.rows_per_box;
-  const int base = g.kv_lo + j * kKeys;
+  const int base = g.key_of(j);
   mbar_arrive_expect_tx(full, L::kTile);
   if (boxes == 1) {
     // Pages of at least a key tile: one box (and one page-table load).
@@ -271,11 +282,12 @@ __device__ __forceinline__ void load_key_tile(const CUtensorMap* map, const Pref
       tma_load_4d(dst + pn * L::kPanel, map, full, pn * L::kPanelDims, tile.kv_head, slot, blk);
     return;
   }
+  const KeyGap unseen = key_gap(p.shape.sinks, p.window, g.ctx, 1);
   for (int b = 0; b < boxes; ++b) {
     const int key0 = base + b * p.rows_per_box;
     int32_t blk = static_cast<int32_t>(p.num_blocks);  // out of range: zero fill
     int32_t slot = 0;
-    if (key0 < g.kv_hi) {
+    if (key0 < g.kv_hi && !(key0 >= unseen.lo && key0 + p.rows_per_box <= unseen.hi)) {
       const int32_t id =
           p.block_tables[static_cast<int64_t>(tile.seq) * p.max_blocks_per_seq + key0 / p.block_size];
       if (id >= 0 && static_cast<int64_t>(id) < p.num_blocks) {
@@ -506,7 +518,7 @@ __device__ __forceinline__ void mma_role(const PrefillParams& p, const uint8_t* 
 // What the softmax of one query tile needs of a work tile, as scalars (a
 // runtime index into the descriptor would put it in local memory).
 struct SoftmaxTile {
-  int kv_head, row0, q_start, ctx, kv_lo, kv_hi, prefix, nmax;
+  int kv_head, row0, q_start, ctx, kv_lo, kv_hi, prefix, nmax, nsink, skip;
   int n_t;     // key tiles of this query tile
   int rows_t;  // valid rows of this query tile
 };
@@ -591,7 +603,7 @@ __device__ __forceinline__ bool softmax_tile(const PrefillParams& p, const Softm
   RowBias bias;
   if constexpr ((SHAPE & kShapeBias) != 0)
     bias = row_bias(p.shape.slopes[g.kv_head * p.qpk + row % p.qpk],
-                    p.window > 0 ? min(pos, p.window - 1) : pos,
+                    p.window > 0 && p.shape.sinks <= 0 ? min(pos, p.window - 1) : pos,
                     (p.causal ? min(g.kv_hi - 1, last_key) : g.kv_hi - 1) - pos);
   RowSoftmax<SHAPE, F8, kKeys> shaped(c, p.shape.cap_log2, bias);
   float m = -INFINITY, l = 0.f;
@@ -599,7 +611,7 @@ __device__ __forceinline__ bool softmax_tile(const PrefillParams& p, const Softm
     if (!__all_sync(0xffffffffu, mbar_wait(bar.s_full(t), (done + j) & 1, abort, p.timeout_ns)))
       return false;
     tc_fence_after();
-    const int base = g.kv_lo + j * kKeys;
+    const int base = g.kv_lo + j * kKeys + (kShaped && j >= g.nsink ? g.skip : 0);
     const int hi_col = min(g.kv_hi, p.causal ? last_key + 1 : g.kv_hi) - base;
     const int lo_col = p.window > 0 ? pos - p.window + 1 - base : INT_MIN;
     // P packed for the P V products: bf16 pairs, or e4m3 quadruples (F8:
@@ -609,7 +621,7 @@ __device__ __forceinline__ bool softmax_tile(const PrefillParams& p, const Softm
     uint32_t pk[kPk];
     float alpha = 1.f;
     if constexpr (kShaped) {
-      alpha = shaped.tile(s_tmem, base - pos, lo_col, hi_col);
+      alpha = shaped.tile(s_tmem, base - pos, lo_col, hi_col, p.shape.sinks - base);
       l = shaped.l;
     } else {
       // Raw scores; the scale is folded into one fma per pair below.
@@ -787,6 +799,8 @@ __device__ __forceinline__ void softmax_role(const PrefillParams& p, const uint8
     st.kv_hi = it.g.kv_hi;
     st.prefix = it.g.prefix;
     st.nmax = it.g.nmax;
+    st.nsink = it.g.nsink;
+    st.skip = it.g.skip;
     st.n_t = t ? it.g.ntiles[1] : it.g.ntiles[0];
     st.rows_t = t ? it.g.rows[1] : it.g.rows[0];
     if (st.n_t > 0) {

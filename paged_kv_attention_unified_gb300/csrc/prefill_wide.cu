@@ -103,6 +103,7 @@ struct Item {
   int seq, kv_head, row0, rows;  // packed rows [row0, row0 + rows) of the KV head
   int q_start, ctx, kv_lo, kv_hi;
   int ntiles;                    // key tiles of 64 from kv_lo
+  int nsink, skip;               // key tiles before the keys that no row sees, and how many those are
   int end;                       // 1: no more items for this CTA
   int prefix;                    // keys below it are visible to every row (0: none)
 };
@@ -164,7 +165,10 @@ __device__ __forceinline__ void scheduler_role(const PrefillParams& p, const Bar
     const int last = it.row0 + it.rows - 1;
     it.prefix = p.shape.prefix_lens ? p.shape.prefix_lens[tile.seq] : 0;
     const int hi = p.causal ? min(kv_hi, max(it.ctx + last / p.qpk + 1, it.prefix)) : kv_hi;
-    it.ntiles = hi > it.kv_lo ? (hi - it.kv_lo + kKeys - 1) / kKeys : 0;
+    const KeyGap gap = key_gap(p.shape.sinks, p.window, it.ctx + it.row0 / p.qpk, kKeys);
+    it.nsink = gap.lo / kKeys;
+    it.skip = gap.hi - gap.lo;
+    it.ntiles = hi > it.kv_lo + it.skip ? (hi - it.kv_lo - it.skip + kKeys - 1) / kKeys : 0;
     if (it.ntiles > 0) ok = publish(it);
   }
   if (!ok) give_up(p, abort);
@@ -185,7 +189,7 @@ __device__ __forceinline__ void load_key_tile(const CUtensorMap* map, const Pref
                                               const Item& it, int j, uint8_t* dst, uint32_t full) {
   constexpr int kPanels = Geo<D>::kPanels, kStage = Geo<D>::kStage;
   const int boxes = kKeys / p.rows_per_box;
-  const int base = it.kv_lo + j * kKeys;
+  const int base = it.kv_lo + j * kKeys + (j >= it.nsink ? it.skip : 0);
   mbar_arrive_expect_tx(full, kStage);
   if (boxes == 1) {
     // Pages of at least a key tile: one box (and one page-table load).
@@ -206,11 +210,13 @@ __device__ __forceinline__ void load_key_tile(const CUtensorMap* map, const Pref
       tma_load_4d(dst + pn * kPanelKV, map, full, pn * 64, it.kv_head, slot, blk);
     return;
   }
+  const KeyGap unseen = key_gap(p.shape.sinks, p.window, it.ctx, 1);
   for (int b = 0; b < boxes; ++b) {
     const int key0 = base + b * p.rows_per_box;
     int32_t blk = static_cast<int32_t>(p.num_blocks);  // out of range: zero fill
     int32_t slot = 0;
-    if (key0 < it.kv_hi) {
+    // (pages between the sinks and the first query's window may have been given back)
+    if (key0 < it.kv_hi && !(key0 >= unseen.lo && key0 + p.rows_per_box <= unseen.hi)) {
       const int32_t id =
           p.block_tables[static_cast<int64_t>(it.seq) * p.max_blocks_per_seq + key0 / p.block_size];
       if (id >= 0 && static_cast<int64_t>(id) < p.num_blocks) {
@@ -403,7 +409,7 @@ __device__ __forceinline__ bool softmax_item(const PrefillParams& p, const Item&
   RowBias bias;
   if constexpr ((SHAPE & kShapeBias) != 0)
     bias = row_bias(p.shape.slopes[it.kv_head * p.qpk + row % p.qpk],
-                    p.window > 0 ? min(pos, p.window - 1) : pos,
+                    p.window > 0 && p.shape.sinks <= 0 ? min(pos, p.window - 1) : pos,
                     (p.causal ? min(it.kv_hi - 1, last_key) : it.kv_hi - 1) - pos);
   RowSoftmax<SHAPE, false, kKeys> shaped(c, p.shape.cap_log2, bias);
   float m = -INFINITY, l = 0.f;
@@ -414,13 +420,13 @@ __device__ __forceinline__ bool softmax_item(const PrefillParams& p, const Item&
     if (!__all_sync(0xffffffffu, mbar_wait(bar.s_full(g % 2), (g / 2) & 1, abort, p.timeout_ns)))
       return false;
     tc_fence_after();
-    const int base = it.kv_lo + j * kKeys;
+    const int base = it.kv_lo + j * kKeys + (kShaped && j >= it.nsink ? it.skip : 0);
     const int hi_col = min(it.kv_hi, p.causal ? last_key + 1 : it.kv_hi) - base;
     const int lo_col = p.window > 0 ? pos - p.window + 1 - base : INT_MIN;
     uint32_t pk[kKeys / 2];
     float alpha = 1.f;
     if constexpr (kShaped) {
-      alpha = shaped.tile(s_tmem, base - pos, lo_col, hi_col);
+      alpha = shaped.tile(s_tmem, base - pos, lo_col, hi_col, p.shape.sinks - base);
       l = shaped.l;
     } else {
       float x[kKeys];

@@ -1,12 +1,13 @@
 // Score shapes of the attention kernels: a tanh cap, a bias that falls with the
-// distance between query and key, and a prefix every query sees.
+// distance between query and key, a prefix every query sees, and first keys
+// (sinks) that stay visible under a window.
 //
 // With x = scale * q.k (times k_scale for an e4m3 cache), all in units of the
 // argument of softmax's exp:
 //
 //   x <- cap * tanh(x / cap)             cap > 0
 //   x <- x - slope[head] * |pos - t|     slopes given
-//   key t visible iff t <= pos or t < prefix (both within kv_len and window)
+//   key t visible iff (t <= pos or t < prefix) and (t > pos - window or t < sinks)
 //
 // The kernels hold scores in base 2 (y = x * log2 e). tanh comes from
 // tanh(a) = 1 - 2 / (1 + e^(2a)): with u = 2 a log2 e = raw * cap_arg,
@@ -36,14 +37,15 @@
 namespace ua {
 
 // What a kernel instance applies (template argument): nothing, or at least
-// the prefix mask, plus the cap and / or the bias.
+// the prefix mask and the sinks, plus the cap and / or the bias.
 constexpr int kShapePlain = 0;
 constexpr int kShapePrefix = 1;
 constexpr int kShapeCap = 2;
 constexpr int kShapeBias = 4;
 
 inline int shape_of(const ScoreShape& s) {
-  if (s.cap_log2 <= 0.f && s.slopes == nullptr && s.prefix_lens == nullptr) return kShapePlain;
+  if (s.cap_log2 <= 0.f && s.slopes == nullptr && s.prefix_lens == nullptr && s.sinks <= 0)
+    return kShapePlain;
   return kShapePrefix | (s.cap_log2 > 0.f ? kShapeCap : 0) | (s.slopes ? kShapeBias : 0);
 }
 
@@ -144,7 +146,8 @@ struct RowSoftmax {
   // A row's place in a key tile.
   struct Place {
     int rel0;            // first key, relative to the row
-    int lo_col, hi_col;  // visible columns
+    int lo_col, hi_col;  // visible columns ...
+    int sink_col;        // ... and those below it (0: none)
     bool after;          // (bias) the warp has visible keys after their rows
   };
 
@@ -207,8 +210,8 @@ struct RowSoftmax {
     if constexpr (!OPEN) {
       static_assert(N == 32, "one bit per column");
       const int lo = at.lo_col - ch, hi = at.hi_col - ch;
-      uint32_t seen = hi >= N ? ~0u : (hi <= 0 ? 0u : (1u << hi) - 1u);
-      seen &= lo <= 0 ? ~0u : (lo >= N ? 0u : ~0u << lo);
+      auto below = [](int n) { return n >= N ? ~0u : (n <= 0 ? 0u : (1u << n) - 1u); };
+      const uint32_t seen = below(hi) & (~below(lo) | below(at.sink_col - ch));
 #pragma unroll
       for (int i = 0; i < N; ++i)
         if (!(seen & (1u << i))) x[i] = -INFINITY;
@@ -280,19 +283,21 @@ struct RowSoftmax {
   }
 
   // One key tile: scores at s_tmem, keys from pos + rel0 on, columns [lo_col,
-  // hi_col) visible, to P. Returns the factor for what was accumulated before.
-  // Whole warps call it together.
-  __device__ __forceinline__ float tile(uint32_t s_tmem, int rel0, int lo_col, int hi_col) {
+  // hi_col) and those below sink_col and hi_col visible, to P. Returns the factor
+  // for what was accumulated before. Whole warps call it together.
+  __device__ __forceinline__ float tile(uint32_t s_tmem, int rel0, int lo_col, int hi_col,
+                                        int sink_col) {
     using namespace sm100;
+    if (sink_col >= lo_col) lo_col = 0;  // one run
     uint64_t sum[4];
 #pragma unroll
     for (int a = 0; a < 4; ++a) sum[a] = f2_pack(0.f, 0.f);
     float alpha;
     if constexpr (KEYS == N) {
-      alpha = whole_tile(s_tmem, rel0, lo_col, hi_col, sum);
+      alpha = whole_tile(s_tmem, rel0, lo_col, hi_col, sink_col, sum);
     } else {
       const bool after = kBias && __any_sync(0xffffffffu, rel0 + min(hi_col, KEYS) > 1);
-      alpha = tile_by_columns(s_tmem, Place{rel0, max(lo_col, 0), hi_col, after}, sum);
+      alpha = tile_by_columns(s_tmem, Place{rel0, max(lo_col, 0), hi_col, sink_col, after}, sum);
     }
     sum[0] = f2_add(f2_add(sum[0], sum[1]), f2_add(sum[2], sum[3]));
     float lo, hi;
@@ -342,7 +347,7 @@ struct RowSoftmax {
   }
 
   __device__ __forceinline__ float whole_tile(uint32_t s_tmem, int rel0, int lo_col, int hi_col,
-                                              uint64_t (&sum)[4]) {
+                                              int sink_col, uint64_t (&sum)[4]) {
     using namespace sm100;
     float x[N];
     load(s_tmem, x);
@@ -391,6 +396,16 @@ struct RowSoftmax {
     if (flip) {
 #pragma unroll
       for (int i = 0; i < N; ++i) x[i] = -x[i];
+    }
+    if (sink_col > 0 && lo_col > 0) {  // sinks, then keys that the window has passed
+      if (lo_col >= N) {
+        hi_col = min(hi_col, sink_col);
+      } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          if (i >= sink_col && i < lo_col) x[i] = -INFINITY;
+      }
+      lo_col = 0;
     }
     if (hi_col < N || lo_col > 0) {
 #pragma unroll

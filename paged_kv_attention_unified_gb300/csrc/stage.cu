@@ -14,7 +14,11 @@
 // row (all KV heads, contiguous in both caches) per warp at a time, 16-byte loads
 // (four in flight per lane and cache) before the stores; source pages
 // through the block table; rows past the sequence's length are not written
-// (the prefill kernel masks those keys and zeroes those value rows).
+// (the prefill kernel masks those keys and zeroes those value rows); keys that no
+// query sees (between the sinks and the first window) are staged as zeros, their
+// pages not looked up.
+// A cache with block scales is staged as code * scale, rounded to bf16 (exact for
+// powers of two), with a scale of each row's page and head.
 // HBM-bound: per staged key Hkv * d bytes read per cache, twice that written.
 #include <cstdint>
 #include <cuda_fp16.h>
@@ -38,21 +42,31 @@ __device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t h2) {
   return b2;
 }
 
+template <bool SCALED>
+__device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t h2, float scale) {
+  if constexpr (!SCALED) return f16x2_to_bf16x2(h2);
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+  return pack2<false>(f.x * scale, f.y * scale);
+}
+
 // Sixteen codes (16 bytes, lowest first) -> sixteen bf16 values (2 x 16 bytes).
-__device__ __forceinline__ void widen16(uint4 c, uint4& lo, uint4& hi) {
+template <bool SCALED>
+__device__ __forceinline__ void widen16(uint4 c, float scale, uint4& lo, uint4& hi) {
   uint32_t h[8];
   e4m3x4_to_f16x2x2(c.x, h[0], h[1]);
   e4m3x4_to_f16x2x2(c.y, h[2], h[3]);
   e4m3x4_to_f16x2x2(c.z, h[4], h[5]);
   e4m3x4_to_f16x2x2(c.w, h[6], h[7]);
-  lo = make_uint4(f16x2_to_bf16x2(h[0]), f16x2_to_bf16x2(h[1]), f16x2_to_bf16x2(h[2]),
-                  f16x2_to_bf16x2(h[3]));
-  hi = make_uint4(f16x2_to_bf16x2(h[4]), f16x2_to_bf16x2(h[5]), f16x2_to_bf16x2(h[6]),
-                  f16x2_to_bf16x2(h[7]));
+  uint32_t b[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) b[i] = f16x2_to_bf16x2<SCALED>(h[i], scale);
+  lo = make_uint4(b[0], b[1], b[2], b[3]);
+  hi = make_uint4(b[4], b[5], b[6], b[7]);
 }
 
 constexpr int kUnroll = 4;  // 16-byte loads per lane in flight per cache
 
+template <bool SCALED>
 __global__ void __launch_bounds__(kStageWarps * 32) stage_kernel(const StageParams p, int parts) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const ua_tile tile = p.tiles[blockIdx.x / parts];
@@ -62,6 +76,14 @@ __global__ void __launch_bounds__(kStageWarps * 32) stage_kernel(const StagePara
   const int32_t* table = p.block_tables + static_cast<int64_t>(tile.seq) * p.max_blocks_per_seq;
   for (int t = first + w; t < last; t += kStageWarps) {
     if (t / p.block_size >= p.max_blocks_per_seq) break;
+    if (t >= tile.slot && t < tile.group) {  // seen by no query
+      const int64_t row = (static_cast<int64_t>(tile.row0) * kStagePage + (t - tile.kv_lo)) * 2 * chunks;
+      for (int c = lane; c < 2 * chunks; c += 32) {
+        reinterpret_cast<uint4*>(p.k_dst)[row + c] = make_uint4(0u, 0u, 0u, 0u);
+        reinterpret_cast<uint4*>(p.v_dst)[row + c] = make_uint4(0u, 0u, 0u, 0u);
+      }
+      continue;
+    }
     const int32_t blk = table[t / p.block_size];
     if (blk < 0 || static_cast<int64_t>(blk) >= p.num_blocks) {
       if (lane == 0) record_error(p.err, UA_ERR_BOUNDS);
@@ -87,11 +109,17 @@ __global__ void __launch_bounds__(kStageWarps * 32) stage_kernel(const StagePara
       for (int u = 0; u < kUnroll; ++u) {
         const int c = c0 + u * 32 + lane;
         if (c >= chunks) continue;
+        float k_scale = 1.f, v_scale = 1.f;
+        if constexpr (SCALED) {
+          const int64_t at = static_cast<int64_t>(blk) * p.num_kv_heads + c / p.head_chunks;
+          k_scale = __ldg(p.k_scales + at);
+          v_scale = __ldg(p.v_scales + at);
+        }
         uint4 lo, hi;
-        widen16(kc[u], lo, hi);
+        widen16<SCALED>(kc[u], k_scale, lo, hi);
         kd[2 * c] = lo;
         kd[2 * c + 1] = hi;
-        widen16(vc[u], lo, hi);
+        widen16<SCALED>(vc[u], v_scale, lo, hi);
         vd[2 * c] = lo;
         vd[2 * c + 1] = hi;
       }
@@ -117,7 +145,10 @@ cudaError_t launch_stage(const StageParams& p, int sms, cudaStream_t stream) {
   const bool wide_rows = p.row_elems / 16 > 32 * kUnroll;
   const bool fills = 4 * p.num_tiles > 3 * sms && p.num_tiles <= sms;
   const int parts = !wide_rows ? 8 : (fills ? 1 : 16);
-  stage_kernel<<<p.num_tiles * parts, kStageWarps * 32, 0, stream>>>(p, parts);
+  if (p.k_scales)
+    stage_kernel<true><<<p.num_tiles * parts, kStageWarps * 32, 0, stream>>>(p, parts);
+  else
+    stage_kernel<false><<<p.num_tiles * parts, kStageWarps * 32, 0, stream>>>(p, parts);
   return cudaGetLastError();
 }
 

@@ -17,6 +17,7 @@
 struct ua_rope {
   int32_t rotary_dim = 0;
   int32_t layout = UA_ROPE_HALF;
+  int32_t axes = 1;
   ua::RopeTable table{};
 };
 
@@ -34,6 +35,7 @@ struct ua_plan {
   int32_t* d_counters = nullptr;   // per combine group, zero between calls
   int32_t* d_prefill_counters = nullptr;  // [2] persistent prefill tile queue, zero between calls
   ua_tile* d_append = nullptr;            // append-KV tiles
+  ua_tile* d_fill = nullptr;              // append with block scales: new tokens by page
   int32_t* d_staged_table = nullptr;      // fp8 prefill: staging page table
   ua_tile* d_stage = nullptr;             // fp8 prefill: stage tiles
   void* d_staged_k = nullptr;             // fp8 prefill: bf16 staging caches
@@ -51,6 +53,9 @@ struct ua_plan {
   bool fp8_products = false;          // ua_plan_set_fp8_products
   float softcap = 0.f;                // ua_plan_set_scores
   const float* alibi_slopes = nullptr;
+  float* k_scales = nullptr;          // ua_plan_set_block_scales: [scale_blocks][Hkv]
+  float* v_scales = nullptr;
+  int64_t scale_blocks = 0;
   int32_t* d_prefix = nullptr;        // ua_plan_create_prefix: device prefix lengths (in d_meta)
   // For forwards with shaped scores, where those run prompts in a prefill
   // kernel that plain scores do not have (head dims padded to the next built
@@ -189,7 +194,7 @@ ua::Problem make_problem(const int32_t* cu, const int32_t* kv, int32_t num_seqs,
                          int32_t hkv, int32_t d, int32_t bs, int32_t max_blocks, int32_t dtype,
                          int32_t causal, int32_t window, int32_t num_splits, int32_t num_sms,
                          int32_t decode_rows_max, bool shaped = false,
-                         const int32_t* prefix = nullptr) {
+                         const int32_t* prefix = nullptr, int32_t sinks = 0) {
   ua::Problem p;
   p.cu_query_lens = cu;
   p.kv_lens = kv;
@@ -203,6 +208,7 @@ ua::Problem make_problem(const int32_t* cu, const int32_t* kv, int32_t num_seqs,
   p.kv_dtype = dtype;
   p.causal = causal;
   p.window = window;
+  p.sinks = sinks;
   p.num_splits = num_splits;
   p.num_sms = num_sms;
   p.decode_rows_max = decode_rows_max;
@@ -263,6 +269,13 @@ ua::KernelParams base_params(const ua_plan* plan, const void* q, const void* k, 
   kp.shape.cap_arg = plan->softcap > 0.f ? 2.f / plan->softcap : 0.f;
   kp.shape.slopes = plan->alibi_slopes;
   kp.shape.prefix_lens = plan->d_prefix;
+  kp.shape.sinks = pr.sinks;
+  if (plan->k_scales != nullptr) {  // the step's k_scale and v_scale play no part
+    kp.k_scales = plan->k_scales;
+    kp.v_scales = plan->v_scales;
+    kp.score_scale_log2 = scale * ua::kLog2e;
+    kp.v_scale = 1.f;
+  }
   return kp;
 }
 
@@ -313,7 +326,16 @@ cudaError_t span_reset(ua_plan* p, int slots, cudaStream_t cs) {
   return e;
 }
 
-// The scheduler behind ua_schedule and ua_schedule_prefix.
+// Sinks as the kernels take them: none without a window, and no more than there
+// can be keys (what is negative stays so).
+int32_t effective_sinks(int32_t sink_tokens, int32_t window, int32_t max_blocks, int32_t bs) {
+  if (sink_tokens < 0) return sink_tokens;
+  if (window <= 0) return 0;
+  return static_cast<int32_t>(std::min<int64_t>(
+      sink_tokens, std::max<int64_t>(0, static_cast<int64_t>(max_blocks) * bs)));
+}
+
+// The scheduler behind ua_schedule, ua_schedule_prefix and ua_schedule_sinks.
 ua_status schedule(const int32_t* cu_query_lens_host, const int32_t* kv_lens_host,
                    const int32_t* prefix_lens_host, int32_t num_seqs, int32_t num_q_heads,
                    int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
@@ -321,13 +343,13 @@ ua_status schedule(const int32_t* cu_query_lens_host, const int32_t* kv_lens_hos
                    int32_t num_splits, int32_t num_sms, int32_t decode_rows_max,
                    ua_plan_info* info, ua_tile* prefill_tiles, int64_t prefill_cap,
                    ua_tile* decode_tiles, int64_t decode_cap, ua_combine_group* groups,
-                   int64_t groups_cap) {
+                   int64_t groups_cap, int32_t sinks = 0) {
   if (info == nullptr) return UA_ERR_INVALID_ARG;
   const int sms = num_sms > 0 ? num_sms : 152;
   ua::Problem pr = make_problem(cu_query_lens_host, kv_lens_host, num_seqs, num_q_heads,
                                 num_kv_heads, head_dim, block_size, max_blocks_per_seq, kv_dtype,
                                 causal, window, num_splits, sms, decode_rows_max,
-                                prefix_lens_host != nullptr, prefix_lens_host);
+                                prefix_lens_host != nullptr || sinks > 0, prefix_lens_host, sinks);
   ua::Schedule s;
   try {
     ua_status st = ua::build_schedule(pr, &s);
@@ -396,6 +418,22 @@ ua_status ua_schedule_prefix(const int32_t* cu_query_lens_host, const int32_t* k
                   decode_tiles, decode_cap, groups, groups_cap);
 }
 
+ua_status ua_schedule_sinks(const int32_t* cu_query_lens_host, const int32_t* kv_lens_host,
+                            const int32_t* prefix_lens_host, int32_t num_seqs,
+                            int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                            int32_t block_size, int32_t max_blocks_per_seq, int32_t kv_dtype,
+                            int32_t causal, int32_t window, int32_t sink_tokens,
+                            int32_t num_splits, int32_t num_sms, int32_t decode_rows_max,
+                            ua_plan_info* info, ua_tile* prefill_tiles, int64_t prefill_cap,
+                            ua_tile* decode_tiles, int64_t decode_cap, ua_combine_group* groups,
+                            int64_t groups_cap) {
+  return schedule(cu_query_lens_host, kv_lens_host, prefix_lens_host, num_seqs, num_q_heads,
+                  num_kv_heads, head_dim, block_size, max_blocks_per_seq, kv_dtype, causal, window,
+                  num_splits, num_sms, decode_rows_max, info, prefill_tiles, prefill_cap,
+                  decode_tiles, decode_cap, groups, groups_cap,
+                  effective_sinks(sink_tokens, window, max_blocks_per_seq, block_size));
+}
+
 }  // extern "C"
 
 namespace {
@@ -415,7 +453,7 @@ ua_status create_plan(ua_plan** out, const int32_t* cu_query_lens_host,
                       int32_t window, int32_t num_splits, int32_t decode_rows_max,
                       ua_stream_t stream, const HostRange* extra, int n_extra,
                       void** extra_dev, bool shaped = false,
-                      const int32_t* prefix_lens_host = nullptr) {
+                      const int32_t* prefix_lens_host = nullptr, int32_t sinks = 0) {
   if (out == nullptr) return UA_ERR_INVALID_ARG;
   *out = nullptr;
   int dev = 0, sms = 0;
@@ -428,7 +466,7 @@ ua_status create_plan(ua_plan** out, const int32_t* cu_query_lens_host,
   plan->prob = make_problem(cu_query_lens_host, kv_lens_host, num_seqs, num_q_heads,
                             num_kv_heads, head_dim, block_size, max_blocks_per_seq, kv_dtype,
                             causal, window, num_splits, sms, decode_rows_max, shaped,
-                            prefix_lens_host);
+                            prefix_lens_host, sinks);
   ua_status st;
   try {
     st = ua::build_schedule(plan->prob, &plan->sched);
@@ -454,7 +492,9 @@ ua_status create_plan(ua_plan** out, const int32_t* cu_query_lens_host,
   const size_t n_app = s.append.size();
   const size_t off_app = (off_pc + 2 * sizeof(int32_t) + 15) & ~static_cast<size_t>(15);
   const size_t n_stage = s.stage.size(), n_st = s.staged_table.size();
-  const size_t off_stage = off_app + n_app * sizeof(ua_tile);
+  const size_t n_fill = s.fill.size();
+  const size_t off_fill = off_app + n_app * sizeof(ua_tile);
+  const size_t off_stage = off_fill + n_fill * sizeof(ua_tile);
   const size_t off_st = off_stage + n_stage * sizeof(ua_tile);
   const size_t off_prefix = off_st + n_st * sizeof(int32_t);
   const size_t n_prefix = prefix_lens_host && num_seqs > 0 ? static_cast<size_t>(num_seqs) : 0;
@@ -480,6 +520,7 @@ ua_status create_plan(ua_plan** out, const int32_t* cu_query_lens_host,
                          n_dec * sizeof(ua_tile));
   if (n_grp) std::memcpy(host + bytes_tiles, s.groups.data(), bytes_groups);
   if (n_app) std::memcpy(host + off_app, s.append.data(), n_app * sizeof(ua_tile));
+  if (n_fill) std::memcpy(host + off_fill, s.fill.data(), n_fill * sizeof(ua_tile));
   if (n_stage) std::memcpy(host + off_stage, s.stage.data(), n_stage * sizeof(ua_tile));
   if (n_st) std::memcpy(host + off_st, s.staged_table.data(), n_st * sizeof(int32_t));
   if (n_prefix) std::memcpy(host + off_prefix, prefix_lens_host, n_prefix * sizeof(int32_t));
@@ -506,6 +547,7 @@ ua_status create_plan(ua_plan** out, const int32_t* cu_query_lens_host,
   plan->d_counters = reinterpret_cast<int32_t*>(base + bytes_tiles + bytes_groups + 16);
   plan->d_prefill_counters = reinterpret_cast<int32_t*>(base + off_pc);
   plan->d_append = reinterpret_cast<ua_tile*>(base + off_app);
+  plan->d_fill = reinterpret_cast<ua_tile*>(base + off_fill);
   plan->d_stage = reinterpret_cast<ua_tile*>(base + off_stage);
   plan->d_staged_table = reinterpret_cast<int32_t*>(base + off_st);
   if (n_prefix) plan->d_prefix = reinterpret_cast<int32_t*>(base + off_prefix);
@@ -770,6 +812,9 @@ ua_status make_shaped(ua_plan* plan) {
     twin->prefill_ctas_override = plan->prefill_ctas_override;
     twin->unified_max_on = plan->unified_max_on;
     twin->unified_max = plan->unified_max;
+    twin->k_scales = plan->k_scales;
+    twin->v_scales = plan->v_scales;
+    twin->scale_blocks = plan->scale_blocks;
     if (plan->profiling) st = ua_plan_set_profiling(twin, 1);
     if (st == UA_OK) st = from_cuda(cudaEventCreateWithFlags(&twin->uploaded, cudaEventDisableTiming));
     if (st == UA_OK) st = from_cuda(cudaEventRecord(twin->uploaded, cs));
@@ -780,6 +825,56 @@ ua_status make_shaped(ua_plan* plan) {
     plan->shaped = twin;
   }
   plan->lens = std::vector<int32_t>();
+  return UA_OK;
+}
+
+// Whether floats that a plan is to read are aligned and on its device.
+ua_status check_floats(const ua_plan* plan, const float* x) {
+  if ((reinterpret_cast<uintptr_t>(x) & 3u) != 0) return UA_ERR_INVALID_ARG;
+  cudaPointerAttributes at;
+  if (cudaPointerGetAttributes(&at, x) != cudaSuccess) {
+    cudaGetLastError();  // not a later launch's error
+    return UA_ERR_CUDA;
+  }
+  const bool there = at.type == cudaMemoryTypeManaged ||
+                     (at.type == cudaMemoryTypeDevice && at.device == plan->device);
+  return there ? UA_OK : UA_ERR_INVALID_ARG;
+}
+
+// An append into a plan's cache with block scales: what both appends have of it,
+// and its launch.
+ua::FillParams fill_params(const ua_plan* plan, const void* k_new, const void* v_new,
+                           void* k_cache, void* v_cache, const int32_t* block_tables,
+                           int64_t num_blocks) {
+  ua::FillParams fp;
+  std::memset(&fp, 0, sizeof(fp));
+  fp.k_new = k_new;
+  fp.v_new = v_new;
+  fp.k_cache = k_cache;
+  fp.v_cache = v_cache;
+  fp.k_scales = plan->k_scales;
+  fp.v_scales = plan->v_scales;
+  fp.tiles = plan->d_fill;
+  fp.block_tables = block_tables;
+  fp.err = plan->d_err;
+  fp.num_blocks = num_blocks;
+  fp.num_tiles = static_cast<int32_t>(plan->sched.fill.size());
+  fp.max_rows = plan->sched.fill_rows;
+  fp.num_kv_heads = plan->prob.num_kv_heads;
+  fp.head_dim = plan->prob.head_dim;
+  fp.max_blocks_per_seq = plan->prob.max_blocks_per_seq;
+  fp.block_size = plan->prob.block_size;
+  return fp;
+}
+
+ua_status run_fill(const ua_plan* plan, const ua::RopeTable* rope, const ua::FillParams& fp,
+                   const ua::RopeAppendParams& q, ua_stream_t stream) {
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  ua_plan* mp = const_cast<ua_plan*>(plan);
+  mp->last_stream = cs;
+  auto* ev = timing_begin(mp, 3, cs);
+  if (ua::launch_fill(rope, fp, q, cs) != cudaSuccess) return UA_ERR_CUDA;
+  timing_end(ev, cs);
   return UA_OK;
 }
 
@@ -859,6 +954,26 @@ ua_status ua_plan_create_prefix(ua_plan** out, const int32_t* cu_query_lens_host
                      decode_rows_max, stream, nullptr, 0, nullptr, true, prefix_lens_host);
 }
 
+ua_status ua_plan_create_sinks(ua_plan** out, const int32_t* cu_query_lens_host,
+                               const int32_t* kv_lens_host, const int32_t* prefix_lens_host,
+                               int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                               int32_t head_dim, int32_t block_size, int32_t max_blocks_per_seq,
+                               int32_t kv_dtype, int32_t causal, int32_t window,
+                               int32_t sink_tokens, int32_t num_splits, int32_t decode_rows_max,
+                               ua_stream_t stream) {
+  if (out == nullptr) return UA_ERR_INVALID_ARG;
+  *out = nullptr;
+  const int32_t sinks = effective_sinks(sink_tokens, window, max_blocks_per_seq, block_size);
+  if (sinks == 0 && prefix_lens_host == nullptr)
+    return ua_plan_create_ex(out, cu_query_lens_host, kv_lens_host, num_seqs, num_q_heads,
+                             num_kv_heads, head_dim, block_size, max_blocks_per_seq, kv_dtype,
+                             causal, window, num_splits, decode_rows_max, stream);
+  return create_plan(out, cu_query_lens_host, kv_lens_host, num_seqs, num_q_heads, num_kv_heads,
+                     head_dim, block_size, max_blocks_per_seq, kv_dtype, causal, window,
+                     num_splits, decode_rows_max, stream, nullptr, 0, nullptr, true,
+                     prefix_lens_host, sinks);
+}
+
 ua_status ua_plan_get_info(const ua_plan* plan, ua_plan_info* info) {
   if (plan == nullptr || info == nullptr) return UA_ERR_INVALID_ARG;
   *info = serving(plan)->info;
@@ -905,8 +1020,12 @@ ua_status ua_forward(const ua_plan* plan, const void* q, const void* k_cache,
     return UA_ERR_INVALID_ARG;
   if (num_blocks <= 0 || max_q < s.max_q || max_kv < s.max_kv) return UA_ERR_INVALID_ARG;
   if (!std::isfinite(scale)) return UA_ERR_INVALID_ARG;
-  if (plan->prob.kv_dtype == UA_KV_FP8_E4M3 && (!std::isfinite(k_scale) || !std::isfinite(v_scale)))
+  if (plan->k_scales != nullptr) {
+    if (num_blocks != plan->scale_blocks) return UA_ERR_INVALID_ARG;
+  } else if (plan->prob.kv_dtype == UA_KV_FP8_E4M3 &&
+             (!std::isfinite(k_scale) || !std::isfinite(v_scale))) {
     return UA_ERR_INVALID_ARG;
+  }
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess) return UA_ERR_CUDA;
   if (dev != plan->device) return UA_ERR_INVALID_ARG;
@@ -943,6 +1062,10 @@ ua_status ua_forward(const ua_plan* plan, const void* q, const void* k_cache,
       sp.num_blocks = num_blocks;
       sp.row_elems = plan->prob.num_kv_heads * plan->prob.head_dim;
       sp.err = plan->d_err;
+      sp.k_scales = kp.k_scales;
+      sp.v_scales = kp.v_scales;
+      sp.num_kv_heads = plan->prob.num_kv_heads;
+      sp.head_chunks = plan->prob.head_dim / 16;
       auto* sev = timing_begin(mp, 4, cs);
       if (ua::launch_stage(sp, plan->info.num_sms, cs) != cudaSuccess) return UA_ERR_CUDA;
       timing_end(sev, cs);
@@ -1038,12 +1161,20 @@ ua_status ua_append_kv(const ua_plan* plan, const void* k_new, const void* v_new
     return UA_ERR_INVALID_ARG;
   if (num_blocks <= 0 || num_blocks >= INT32_MAX) return UA_ERR_INVALID_ARG;
   const bool fp8 = plan->prob.kv_dtype == UA_KV_FP8_E4M3;
-  if (fp8 && (!std::isfinite(k_scale) || !std::isfinite(v_scale) || k_scale == 0.f ||
-              v_scale == 0.f))
+  if (plan->k_scales != nullptr) {
+    if (num_blocks != plan->scale_blocks) return UA_ERR_INVALID_ARG;
+  } else if (fp8 && (!std::isfinite(k_scale) || !std::isfinite(v_scale) || k_scale == 0.f ||
+                     v_scale == 0.f)) {
     return UA_ERR_INVALID_ARG;
+  }
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess) return UA_ERR_CUDA;
   if (dev != plan->device) return UA_ERR_INVALID_ARG;
+  if (plan->k_scales != nullptr) {
+    ua::FillParams fp = fill_params(plan, k_new, v_new, k_cache, v_cache, block_tables, num_blocks);
+    fp.k_stride = fp.v_stride = int64_t{plan->prob.num_kv_heads} * plan->prob.head_dim;
+    return run_fill(plan, nullptr, fp, ua::RopeAppendParams{}, stream);
+  }
   ua::AppendParams ap;
   std::memset(&ap, 0, sizeof(ap));
   ap.k_new = k_new;
@@ -1145,6 +1276,30 @@ ua_status ua_rope_create(ua_rope** out, int32_t rotary_dim, int32_t layout,
   return UA_OK;
 }
 
+ua_status ua_rope_create_axes(ua_rope** out, int32_t rotary_dim, int32_t layout,
+                              const double* inv_freq_host, float amplitude, int32_t num_axes,
+                              const int32_t* pair_axes_host) {
+  if (out == nullptr) return UA_ERR_INVALID_ARG;
+  *out = nullptr;
+  if (num_axes < 1 || num_axes > UA_ROPE_MAX_AXES || pair_axes_host == nullptr)
+    return UA_ERR_INVALID_ARG;
+  if (rotary_dim < 2 || rotary_dim > 256 || rotary_dim % 2 != 0) return UA_ERR_INVALID_ARG;
+  for (int32_t i = 0; i < rotary_dim / 2; ++i)
+    if (pair_axes_host[i] < 0 || pair_axes_host[i] >= num_axes) return UA_ERR_INVALID_ARG;
+  const ua_status st = ua_rope_create(out, rotary_dim, layout, inv_freq_host, amplitude);
+  if (st != UA_OK) return st;
+  (*out)->axes = num_axes;
+  for (int32_t i = 0; i < rotary_dim / 2; ++i)
+    (*out)->table.axis[i] = static_cast<uint8_t>(pair_axes_host[i]);
+  return UA_OK;
+}
+
+ua_status ua_rope_get_axes(const ua_rope* rope, int32_t* num_axes) {
+  if (rope == nullptr || num_axes == nullptr) return UA_ERR_INVALID_ARG;
+  *num_axes = rope->axes;
+  return UA_OK;
+}
+
 ua_status ua_rope_destroy(ua_rope* rope) {
   delete rope;
   return UA_OK;
@@ -1156,6 +1311,19 @@ ua_status ua_rope_append_kv(const ua_plan* plan, const ua_rope* rope, const void
                             void* v_cache, const int32_t* block_tables, int64_t num_blocks,
                             const int32_t* positions, float k_scale, float v_scale,
                             ua_stream_t stream) {
+  // one row of positions, which says nothing of a second axis
+  if (rope != nullptr && rope->axes > 1 && positions != nullptr) return UA_ERR_INVALID_ARG;
+  return ua_rope_append_kv_axes(plan, rope, q, q_stride, k_new, k_stride, v_new, v_stride, q_out,
+                                k_cache, v_cache, block_tables, num_blocks, positions,
+                                plan != nullptr ? plan->total_q : 0, k_scale, v_scale, stream);
+}
+
+ua_status ua_rope_append_kv_axes(const ua_plan* plan, const ua_rope* rope, const void* q,
+                                 int64_t q_stride, const void* k_new, int64_t k_stride,
+                                 const void* v_new, int64_t v_stride, void* q_out, void* k_cache,
+                                 void* v_cache, const int32_t* block_tables, int64_t num_blocks,
+                                 const int32_t* positions, int64_t positions_stride, float k_scale,
+                                 float v_scale, ua_stream_t stream) {
   if (plan == nullptr || rope == nullptr) return UA_ERR_INVALID_ARG;
   const ua::Problem& pr = plan->prob;
   if (rope->rotary_dim > pr.head_dim) return UA_ERR_INVALID_ARG;
@@ -1166,6 +1334,7 @@ ua_status ua_rope_append_kv(const ua_plan* plan, const ua_rope* rope, const void
                         static_cast<const void*>(k_cache), static_cast<const void*>(v_cache)})
     if (!aligned16(x)) return UA_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(positions) & 3u) != 0) return UA_ERR_INVALID_ARG;
+  if (positions != nullptr && positions_stride < plan->total_q) return UA_ERR_INVALID_ARG;
   const int64_t q_row = static_cast<int64_t>(pr.num_q_heads) * pr.head_dim;
   const int64_t kv_row = static_cast<int64_t>(pr.num_kv_heads) * pr.head_dim;
   if (q_stride < q_row || k_stride < kv_row || v_stride < kv_row || q_stride % 8 != 0 ||
@@ -1183,7 +1352,11 @@ ua_status ua_rope_append_kv(const ua_plan* plan, const ua_rope* rope, const void
   if (!apart(k_new, k_stride, kv_row) || !apart(v_new, v_stride, kv_row)) return UA_ERR_INVALID_ARG;
   if (num_blocks <= 0 || num_blocks >= INT32_MAX) return UA_ERR_INVALID_ARG;
   const bool fp8 = pr.kv_dtype == UA_KV_FP8_E4M3;
-  if (fp8 && (!std::isnormal(k_scale) || !std::isnormal(v_scale))) return UA_ERR_INVALID_ARG;
+  if (plan->k_scales != nullptr) {
+    if (num_blocks != plan->scale_blocks) return UA_ERR_INVALID_ARG;
+  } else if (fp8 && (!std::isnormal(k_scale) || !std::isnormal(v_scale))) {
+    return UA_ERR_INVALID_ARG;
+  }
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess) return UA_ERR_CUDA;
   if (dev != plan->device) return UA_ERR_INVALID_ARG;
@@ -1201,6 +1374,8 @@ ua_status ua_rope_append_kv(const ua_plan* plan, const ua_rope* rope, const void
   rp.tiles = plan->d_append;
   rp.block_tables = block_tables;
   rp.positions = positions;
+  rp.positions_stride = positions_stride;
+  rp.axes = rope->axes;
   rp.err = plan->d_err;
   rp.num_blocks = num_blocks;
   rp.num_tiles = static_cast<int32_t>(plan->sched.append.size());
@@ -1214,6 +1389,17 @@ ua_status ua_rope_append_kv(const ua_plan* plan, const ua_rope* rope, const void
   rp.fp8 = fp8 ? 1 : 0;
   rp.k_scale = k_scale;
   rp.v_scale = v_scale;
+  if (plan->k_scales != nullptr) {
+    ua::FillParams fp = fill_params(plan, k_new, v_new, k_cache, v_cache, block_tables, num_blocks);
+    fp.k_stride = k_stride;
+    fp.v_stride = v_stride;
+    fp.positions = positions;
+    fp.positions_stride = positions_stride;
+    fp.axes = rope->axes;
+    fp.rotary_dim = rope->rotary_dim;
+    fp.interleaved = rp.interleaved;
+    return run_fill(plan, &rope->table, fp, rp, stream);
+  }
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   ua_plan* mp = const_cast<ua_plan*>(plan);
   mp->last_stream = cs;
@@ -1483,6 +1669,7 @@ ua_status ua_plan_set_fp8_products(ua_plan* plan, int32_t enable) {
   if (plan == nullptr || (enable != 0 && enable != 1)) return UA_ERR_INVALID_ARG;
   if (enable) {
     const ua::Problem& pr = plan->prob;
+    if (plan->k_scales != nullptr) return UA_ERR_UNSUPPORTED;
     if (pr.kv_dtype != UA_KV_FP8_E4M3 || !pr.prefill_staged ||
         !ua::prefill_fp8_products_supported(pr.head_dim, pr.num_q_heads / pr.num_kv_heads,
                                             pr.block_size))
@@ -1505,15 +1692,8 @@ ua_status ua_plan_set_scores(ua_plan* plan, float softcap, const float* alibi_sl
   if (softcap != 0.f && !(softcap >= UA_MIN_SOFTCAP && softcap <= UA_MAX_SOFTCAP))
     return UA_ERR_INVALID_ARG;  // NaN too
   if (alibi_slopes != nullptr) {
-    if ((reinterpret_cast<uintptr_t>(alibi_slopes) & 3u) != 0) return UA_ERR_INVALID_ARG;
-    cudaPointerAttributes at;
-    if (cudaPointerGetAttributes(&at, alibi_slopes) != cudaSuccess) {
-      cudaGetLastError();  // not a later launch's error
-      return UA_ERR_CUDA;
-    }
-    if (at.type != cudaMemoryTypeManaged &&
-        !(at.type == cudaMemoryTypeDevice && at.device == plan->device))
-      return UA_ERR_INVALID_ARG;
+    const ua_status st = check_floats(plan, alibi_slopes);
+    if (st != UA_OK) return st;
   }
   if (!plan->lens.empty() && (softcap > 0.f || alibi_slopes != nullptr)) {
     int cur = 0;
@@ -1527,6 +1707,29 @@ ua_status ua_plan_set_scores(ua_plan* plan, float softcap, const float* alibi_sl
     if (p == nullptr) continue;
     p->softcap = softcap;
     p->alibi_slopes = alibi_slopes;
+  }
+  return UA_OK;
+}
+
+ua_status ua_plan_set_block_scales(ua_plan* plan, float* k_scales, float* v_scales,
+                                   int64_t num_blocks) {
+  if (plan == nullptr || (k_scales == nullptr) != (v_scales == nullptr)) return UA_ERR_INVALID_ARG;
+  if (k_scales != nullptr) {
+    if (plan->prob.kv_dtype != UA_KV_FP8_E4M3 || plan->fp8_products) return UA_ERR_UNSUPPORTED;
+    if (num_blocks <= 0 || num_blocks >= INT32_MAX) return UA_ERR_INVALID_ARG;
+    const auto k0 = reinterpret_cast<uintptr_t>(k_scales), v0 = reinterpret_cast<uintptr_t>(v_scales);
+    const uintptr_t bytes = static_cast<uintptr_t>(num_blocks) * plan->prob.num_kv_heads * sizeof(float);
+    if ((k0 > v0 ? k0 - v0 : v0 - k0) < bytes) return UA_ERR_INVALID_ARG;
+    for (const float* x : {k_scales, v_scales}) {
+      const ua_status st = check_floats(plan, x);
+      if (st != UA_OK) return st;
+    }
+  }
+  for (ua_plan* p : {plan, plan->shaped}) {
+    if (p == nullptr) continue;
+    p->k_scales = k_scales;
+    p->v_scales = v_scales;
+    p->scale_blocks = k_scales != nullptr ? num_blocks : 0;
   }
   return UA_OK;
 }

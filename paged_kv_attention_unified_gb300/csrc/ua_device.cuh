@@ -21,6 +21,7 @@ struct ScoreShape {
   float cap_arg;               // base-2 scaled score -> argument u of the cap: 2 log2(e) / cap_log2
   const float* slopes;         // device [num_q_heads], or null: no distance bias
   const int32_t* prefix_lens;  // device [num_seqs], or null: no prefix
+  int32_t sinks;               // first keys that stay visible under the window
 };
 
 struct KernelParams {
@@ -46,6 +47,9 @@ struct KernelParams {
   int32_t window;
   float score_scale_log2;  // scale * log2(e) (* k_scale for fp8)
   float v_scale;           // 1 for bf16
+  // e4m3 cache with block scales: device [num_blocks][num_kv_heads], or null.
+  const float* k_scales;
+  const float* v_scales;
   // Fused split combine: per-group arrival counters (zero between calls) and
   // the groups; null counters leave the merge to the combine kernel.
   int32_t* split_counters;

@@ -146,6 +146,7 @@ struct RopeTable {
   float hi[128];
   float lo[128];
   float amplitude;
+  uint8_t axis[128];             // the position axis each pair turns with (0 with one axis)
 };
 
 struct RopeAppendParams {
@@ -158,10 +159,13 @@ struct RopeAppendParams {
   int64_t q_stride, k_stride, v_stride;
   const ua_tile* tiles;          // append tiles of the plan
   const int32_t* block_tables;   // device [num_seqs][max_blocks_per_seq]
-  const int32_t* positions;      // device [total_tokens], or null: the slots' positions
+  const int32_t* positions;      // device, axis a of row j at a * positions_stride + j; null: the
+                                 // slots' positions
+  int64_t positions_stride;
   int32_t* err;                  // error word (UA_ERR_BOUNDS)
   int64_t num_blocks;
   int32_t num_tiles;
+  int32_t axes;                  // position axes of the rope
   int32_t num_q_heads;
   int32_t num_kv_heads;
   int32_t head_dim;
@@ -176,6 +180,40 @@ struct RopeAppendParams {
 
 cudaError_t launch_rope_append(const RopeTable& rope, const RopeAppendParams& p,
                                cudaStream_t stream);
+
+// Append into an e4m3 cache with block scales (fill.cu).
+struct FillParams {
+  const void* k_new;             // [total_tokens] rows of Hkv * d bf16, k_stride elements apart
+  const void* v_new;
+  void* k_cache;                 // [num_blocks][block_size][Hkv][d] e4m3
+  void* v_cache;
+  float* k_scales;               // [num_blocks][Hkv]
+  float* v_scales;
+  int64_t k_stride, v_stride;
+  const ua_tile* tiles;          // fill tiles of the plan: the new tokens of one page each
+  const int32_t* block_tables;   // device [num_seqs][max_blocks_per_seq]
+  const int32_t* positions;      // as RopeAppendParams
+  int64_t positions_stride;
+  int32_t* err;                  // error word (UA_ERR_BOUNDS)
+  int64_t num_blocks;
+  int32_t num_tiles;
+  int32_t max_rows;              // new tokens of the fullest tile
+  int32_t axes;
+  int32_t num_kv_heads;
+  int32_t head_dim;
+  int32_t max_blocks_per_seq;
+  int32_t block_size;
+  int32_t rotary_dim;
+  int32_t interleaved;
+  // set by launch_fill: warps that share a head, heads of a CTA
+  int32_t warps_per_head;
+  int32_t heads_per_cta;
+};
+
+// rope null: keys as they are, q not used; else q holds the queries' part
+// (its cache fields are not used).
+cudaError_t launch_fill(const RopeTable* rope, FillParams p, RopeAppendParams q,
+                        cudaStream_t stream);
 
 // fp8 prefill staging: e4m3 pages of the prefill sequences -> bf16 staging
 // pages of 128 slots (exact, scale-free).
@@ -192,6 +230,11 @@ struct StageParams {
   int64_t num_blocks;
   int32_t row_elems;             // Hkv * d, a multiple of 8
   int32_t* err;                  // error word (UA_ERR_BOUNDS)
+  // Block scales [num_blocks][Hkv], or null; 16-code chunks of a head.
+  const float* k_scales;
+  const float* v_scales;
+  int32_t num_kv_heads;
+  int32_t head_chunks;
 };
 
 cudaError_t launch_stage(const StageParams& p, int sms, cudaStream_t stream);

@@ -10,7 +10,7 @@ from typing import Optional, Sequence
 
 import torch
 
-from . import (UA_KV_BF16, UA_KV_FP8_E4M3, Plan, Rope, ua_append_kv)
+from . import UA_KV_BF16, UA_KV_FP8_E4M3, Plan, Rope
 
 
 @dataclasses.dataclass
@@ -69,11 +69,20 @@ def to_device(case, device="cuda") -> DeviceBatch:
 
 
 def make_plan(b: DeviceBatch, num_splits: int = 0, decode_rows_max: int = -1,
-              stream=None, prefix_lens: Optional[Sequence[int]] = None) -> Plan:
+              stream=None, prefix_lens: Optional[Sequence[int]] = None,
+              sink_tokens: int = 0) -> Plan:
     return Plan(b.cu_host, b.kv_host, b.num_q_heads, b.num_kv_heads, b.head_dim, b.block_size,
                 int(b.block_tables.shape[1]), kv_dtype=b.kv_dtype, causal=b.causal,
                 window=b.window, num_splits=num_splits, decode_rows_max=decode_rows_max,
-                stream=stream, prefix_lens=prefix_lens)
+                stream=stream, prefix_lens=prefix_lens, sink_tokens=sink_tokens)
+
+
+def new_block_scales(b: DeviceBatch):
+    """Block scales for b's e4m3 caches (key scales, value scales), of a cache that
+    nothing has been written to."""
+    shape = (b.num_blocks, b.num_kv_heads)
+    return (torch.zeros(shape, dtype=torch.float32, device=b.k_cache.device),
+            torch.zeros(shape, dtype=torch.float32, device=b.k_cache.device))
 
 
 def forward(plan: Plan, b: DeviceBatch, out: Optional[torch.Tensor] = None,
@@ -88,8 +97,8 @@ def forward(plan: Plan, b: DeviceBatch, out: Optional[torch.Tensor] = None,
 def append_kv(plan: Plan, b: DeviceBatch, k_new: torch.Tensor, v_new: torch.Tensor,
               stream=None) -> None:
     """Write new K/V rows [total_q, Hkv, d] (bf16, device) into b's caches."""
-    ua_append_kv(plan.handle, k_new, v_new, b.k_cache, b.v_cache, b.block_tables, b.num_blocks,
-                 b.k_scale, b.v_scale, stream)
+    plan.append_kv(k_new, v_new, b.k_cache, b.v_cache, b.block_tables, b.num_blocks,
+                   b.k_scale, b.v_scale, stream)
 
 
 def rope_append_kv(plan: Plan, b: DeviceBatch, rope: Rope, q: torch.Tensor, k_new: torch.Tensor,
