@@ -37,6 +37,8 @@
 // what O accumulates, and l accumulates 2^(x' - m) / vs in binary32. One
 // exponential a score as before, and the f16 weights keep the range that they have
 // without scales, whatever the scales of a row's pages.
+#include <type_traits>
+
 #include "score_shape.cuh"
 #include "sm100.cuh"
 #include "ua_device.cuh"
@@ -236,12 +238,11 @@ __device__ __forceinline__ float lg2(float x) {
   return y;
 }
 
-template <int D, bool FP8, bool SHAPED, bool SCALED>
+template <int D, bool FP8, bool SHAPED>
 __device__ __forceinline__ void compute_step(WarpState<D>& st, StepRegs<D, FP8>& r,
                                              const uint8_t* vp, int kv_hi,
-                                             const uint32_t (&qb)[D / 16][2], const float (&cq)[2],
-                                             const StepMask& mk, const StepScale& scale, int base,
-                                             int g, int t) {
+                                             const uint32_t (&qb)[D / 16][2], const float (&cc)[2],
+                                             const StepMask& mk, int base, int g, int t) {
   using C = DecodeCfg<D, FP8>;
   // S^T = K Q^T for the 16 keys of this step, in two independent accumulation
   // chains (even and odd head-dim chunks) that are added at the end: half the
@@ -261,13 +262,6 @@ __device__ __forceinline__ void compute_step(WarpState<D>& st, StepRegs<D, FP8>&
     }
     mma16816<FP8>(s[c & 1], a, qb[c][0], qb[c][1]);
   }
-  float cc[2] = {cq[0], cq[1]}, v_log2 = 0.f, v_inv = 1.f;
-  if constexpr (SCALED) {
-    cc[0] *= scale.k;
-    cc[1] *= scale.k;
-    v_log2 = lg2(scale.v);
-    v_inv = rcp_approx(scale.v);
-  }
   float x[4];
   x[0] = (s[0][0] + s[1][0]) * cc[0];
   x[1] = (s[0][1] + s[1][1]) * cc[1];
@@ -286,10 +280,6 @@ __device__ __forceinline__ void compute_step(WarpState<D>& st, StepRegs<D, FP8>&
       const RowBias& b = mk.bias[e & 1];
       x[e] = fmaf(-b.slope2, static_cast<float>(abs(mk.pos[e & 1] - key) - b.shift), x[e]);
     }
-  }
-  if constexpr (SCALED) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] += v_log2;
   }
   // Masking (a select, so that nothing read from outside the visible set can
   // reach the result) only on steps that straddle a bound.
@@ -335,8 +325,7 @@ __device__ __forceinline__ void compute_step(WarpState<D>& st, StepRegs<D, FP8>&
     alpha[j] = grow ? ex2(st.m[j] - sub) : 1.f;
     p[j] = ex2(x[j] - sub);
     p[j + 2] = ex2(x[j + 2] - sub);
-    if constexpr (SCALED) st.l[j] = fmaf(p[j] + p[j + 2], v_inv, st.l[j] * alpha[j]);
-    else st.l[j] = st.l[j] * alpha[j] + p[j] + p[j + 2];
+    st.l[j] = st.l[j] * alpha[j] + p[j] + p[j + 2];
     st.m[j] = m_use;
   }
   if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
@@ -372,6 +361,189 @@ __device__ __forceinline__ void compute_step(WarpState<D>& st, StepRegs<D, FP8>&
   }
 }
 
+// Steps a warp takes at a time over a cache with block scales. The e4m3 path
+// waits for its own chain (shared memory, conversions, products, row maximum,
+// exponentials, products) more than for memory; two steps in one chain share the
+// maximum and the rescale and leave twice as many independent instructions.
+template <bool SCALED>
+constexpr int kStepsAtOnce = SCALED ? 2 : 1;
+
+// Key slot of MMA row m of S^T over a cache with block scales: 0 5 2 7 4 1 6 3,
+// and 8 more. Rows of whole 128-byte panels arrive swizzled (chunk c of row r at
+// c ^ (r % 8)); a 16-byte shared-memory read takes its lanes eight at a time, two
+// lane groups g and all four t. Those read K rows that differ in bit 2, at chunks
+// t and 4 + t, and V rows 0, 2, 4, 6 (or 5, 7, 1, 3) at two neighbouring chunks:
+// eight different ones either way, so that no read has bank conflicts (with plain
+// rows and keys 4t .. 4t + 3 to a lane a step's reads take three times as many
+// wavefronts).
+__device__ __forceinline__ int scaled_key_of_row(int m) { return m ^ ((m & 1) << 2); }
+
+template <int D>
+struct ScaledPage {
+  using C = DecodeCfg<D, true>;
+  static constexpr bool kSwizzle = D % 128 == 0;
+  static constexpr int kBoxDims = kSwizzle ? 128 : D;  // elements per box row
+  static constexpr int kPanels = D / kBoxDims;
+  static constexpr int kRow = kBoxDims;                // bytes between rows of a panel
+  static constexpr int kPanelBytes = 16 * kRow;
+  __device__ static __forceinline__ int at(int key, int o) {
+    if constexpr (kSwizzle)
+      return (o >> 7) * kPanelBytes + key * 128 + ((((o >> 4) & 7) ^ (key & 7)) << 4) + (o & 15);
+    else
+      return key * D + o;
+  }
+  // This lane's reads of a step: K row scaled_key_of_row(g) (and 8 rows on), V rows
+  // scaled_key_of_row(2t) and (2t + 1) (and 8 rows on).
+  int k[C::NKL], v[2][C::NVL], k_key, v_key[2];
+  __device__ __forceinline__ ScaledPage(int g, int t) {
+    k_key = scaled_key_of_row(g);
+#pragma unroll
+    for (int l = 0; l < C::NKL; ++l) k[l] = at(k_key, l * 4 * C::KE + t * C::KE);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      v_key[j] = scaled_key_of_row(2 * t + j);
+#pragma unroll
+      for (int l = 0; l < C::NVL; ++l) v[j][l] = at(v_key[j], l * 8 * C::VE + g * C::VE);
+    }
+  }
+  // Rows at or beyond `rows` read as zero (the page may hold anything there); ALL: none is.
+  template <bool ALL>
+  __device__ __forceinline__ void read_k(StepRegs<D, true>& r, const uint8_t* page, int rows) const {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int l = 0; l < C::NKL; ++l)
+        lds_words<C::KE>(&r.k[h][l * (C::KE / 4)], page + k[l] + h * 8 * kRow,
+                         ALL || k_key + 8 * h < rows);
+  }
+  template <bool ALL>
+  __device__ __forceinline__ void read_v(StepRegs<D, true>& r, const uint8_t* page, int rows) const {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int l = 0; l < C::NVL; ++l)
+        lds_words<C::VLB>(&r.v[j][l * (C::VLB / 4)], page + v[j & 1][l] + (j >> 1) * 8 * kRow,
+                          ALL || v_key[j & 1] + 8 * (j >> 1) < rows);
+  }
+};
+
+// The two steps at base[0] and base[1] (their K and V rows at kp and vp): as
+// compute_step, with one reference for both. A step past kv_hi contributes nothing.
+template <int D, bool SHAPED>
+__device__ __forceinline__ void compute_two_scaled(WarpState<D>& st, const uint8_t* const (&kp)[2],
+                                                   const uint8_t* const (&vp)[2], int kv_hi,
+                                                   const uint32_t (&qb)[D / 16][2],
+                                                   const float (&cq)[2], const StepMask& mk,
+                                                   const StepScale (&scale)[2],
+                                                   const int (&base)[2], const ScaledPage<D>& page,
+                                                   int g) {
+  using C = DecodeCfg<D, true>;
+  StepRegs<D, true> r[2];
+  const bool all = base[1] + 16 <= kv_hi;  // (the second step is the later one)
+  auto read_v = [&]() {
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+      if (all) page.template read_v<true>(r[n], vp[n], 16);
+      else page.template read_v<false>(r[n], vp[n], kv_hi - base[n]);
+  };
+#pragma unroll
+  for (int n = 0; n < 2; ++n)
+    if (all) page.template read_k<true>(r[n], kp[n], 16);
+    else page.template read_k<false>(r[n], kp[n], kv_hi - base[n]);
+  float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+  for (int c = 0; c < C::NC; ++c) {
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      uint32_t a[4];
+      e4m3x4_to_f16x2x2(r[n].k[0][c], a[0], a[2]);
+      e4m3x4_to_f16x2x2(r[n].k[1][c], a[1], a[3]);
+      mma16816<true>(s[n], a, qb[c][0], qb[c][1]);
+    }
+  }
+  if constexpr (!kLateV<D>) read_v();
+  float x[2][4], v_inv[2];
+#pragma unroll
+  for (int n = 0; n < 2; ++n) {
+    const float cc[2] = {cq[0] * scale[n].k, cq[1] * scale[n].k};
+    const float v_log2 = lg2(scale[n].v);
+    v_inv[n] = rcp_approx(scale[n].v);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int key = base[n] + page.k_key + 8 * (e >> 1);
+      if constexpr (SHAPED) {
+        x[n][e] = s[n][e] * cc[e & 1];
+        if (mk.cap_log2 > 0.f) x[n][e] = cap_score(x[n][e] * mk.cap_arg, mk.cap_log2);
+        const RowBias& b = mk.bias[e & 1];
+        x[n][e] = fmaf(-b.slope2, static_cast<float>(abs(mk.pos[e & 1] - key) - b.shift), x[n][e]);
+        x[n][e] += v_log2;
+      } else {
+        x[n][e] = fmaf(s[n][e], cc[e & 1], v_log2);
+      }
+    }
+    if (base[n] < mk.lo_full || base[n] + 16 > mk.hi_full) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int key = base[n] + page.k_key + 8 * (e >> 1);
+        const int pos = mk.pos[e & 1];
+        bool ok = key < mk.kv_hi;
+        if (mk.causal) ok = ok && key <= (SHAPED ? mk.last[e & 1] : pos);
+        if (mk.window > 0) ok = ok && (key > pos - mk.window || (SHAPED && key < mk.sinks));
+        x[n][e] = ok ? x[n][e] : -INFINITY;
+      }
+    }
+  }
+  float p[2][4], alpha[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    float mx = fmaxf(fmaxf(x[0][j], x[0][j + 2]), fmaxf(x[1][j], x[1][j + 2]));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+    const bool first = st.m[j] == -INFINITY;
+    const float m_new = fmaxf(st.m[j], mx);
+    const bool grow = first || (m_new > st.m[j] + kRescaleThreshold);
+    float m_use = grow ? m_new : st.m[j];
+    if (first && mx <= mk.phi2 + kRescaleThreshold && mx >= mk.phi2 - kUnifiedAbove<true>)
+      m_use = mk.phi2;
+    const float sub = (m_use == -INFINITY) ? 0.f : m_use;
+    alpha[j] = grow ? ex2(st.m[j] - sub) : 1.f;
+    st.l[j] *= alpha[j];
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      p[n][j] = ex2(x[n][j] - sub);
+      p[n][j + 2] = ex2(x[n][j + 2] - sub);
+      st.l[j] = fmaf(p[n][j] + p[n][j + 2], v_inv[n], st.l[j]);
+    }
+    st.m[j] = m_use;
+  }
+  if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+#pragma unroll
+    for (int c = 0; c < C::NC; ++c) {
+      st.acc[c][0] *= alpha[0];
+      st.acc[c][2] *= alpha[0];
+      st.acc[c][1] *= alpha[1];
+      st.acc[c][3] *= alpha[1];
+    }
+  }
+  if constexpr (kLateV<D>) read_v();
+#pragma unroll
+  for (int n = 0; n < 2; ++n) {
+    const uint32_t pb0 = movmatrix_trans(pack2<true>(p[n][0], p[n][1]));
+    const uint32_t pb1 = movmatrix_trans(pack2<true>(p[n][2], p[n][3]));
+#pragma unroll
+    for (int c = 0; c < C::NC; ++c) {
+      uint32_t a[4];
+      const uint32_t sel = (c & 1) ? 0x7362u : 0x5140u;
+      const uint32_t lo = __byte_perm(r[n].v[0][c >> 1], r[n].v[1][c >> 1], sel);
+      const uint32_t hi = __byte_perm(r[n].v[2][c >> 1], r[n].v[3][c >> 1], sel);
+      e4m3x4_to_f16x2x2(lo, a[0], a[1]);
+      e4m3x4_to_f16x2x2(hi, a[2], a[3]);
+      mma16816<true>(st.acc[c], a, pb0, pb1);
+    }
+  }
+}
+
 // Shared memory of one CTA: a ring of R stages per warp, each holding the K
 // and V rows (16 x head_dim, in the page layout above) of one 16-key step as
 // TMA lands them; then one mbarrier per stage. After the loop the ring is
@@ -392,6 +564,9 @@ struct Ring {
   static_assert(kAlloc == decode_smem_bytes(D, kElt), "decode shared memory");
   static_assert(kWarps * UA_DECODE_ROWS * (D + 2) * 4 <= kRing, "merge buffers alias the ring");
 };
+
+template <int D, bool FP8, bool SCALED>
+using KernelPage = std::conditional_t<SCALED, ScaledPage<D>, PageLayout<D, FP8>>;
 
 template <int D, bool FP8, bool SHAPED, bool SCALED>
 __global__ void __launch_bounds__(kThreads, Ring<D, FP8>::kCtasPerSm)
@@ -606,7 +781,7 @@ __global__ void __launch_bounds__(kThreads, Ring<D, FP8>::kCtasPerSm)
       uint8_t* stage = ring + st * RC::kStage;
       sm100::fence_proxy_async_smem();
       sm100::mbar_arrive_expect_tx(&wbar[st], RC::kStage);
-      using PL = PageLayout<D, FP8>;
+      using PL = KernelPage<D, FP8, SCALED>;
 #pragma unroll
       for (int pn = 0; pn < PL::kPanels; ++pn) {
         sm100::tma_load_4d(stage + pn * PL::kPanelBytes, &map_k, &wbar[st], pn * PL::kBoxDims,
@@ -620,8 +795,37 @@ __global__ void __launch_bounds__(kThreads, Ring<D, FP8>::kCtasPerSm)
   if (my_n > 0) {
     refill_ids(0);
     for (; issued < my_n && issued < R; ++issued) issue(issued);
+    constexpr int N = kStepsAtOnce<SCALED>;
+    [[maybe_unused]] const ScaledPage<D> page(g, t);
+    static_assert(N == 1 || N == 2, "one step or two");
+    for (; N == 2 && done < my_n; done += 2) {
+      const int more = min(done + 1, my_n - 1);  // (the last step's place where there is no second)
+      const bool ok = __all_sync(
+          0xffffffffu,
+          sm100::mbar_wait(&wbar[done % R], (done / R) & 1, never, p.timeout_ns) &&
+              sm100::mbar_wait(&wbar[more % R], (more / R) & 1, never, p.timeout_ns));
+      if (!ok) {
+        record_error(p.err, UA_ERR_DEVICE_TIMEOUT);
+        break;
+      }
+      if constexpr (N == 2) {
+        const uint8_t* const kp[2] = {ring + done % R * RC::kStage, ring + more % R * RC::kStage};
+        const uint8_t* const vp[2] = {kp[0] + 16 * RC::kRowBytes, kp[1] + 16 * RC::kRowBytes};
+        const int base[2] = {step_base(done), done + 1 < my_n ? step_base(done + 1) : kv_hi};
+        const StepScale scale[2] = {scale_of(done), scale_of(more)};
+        compute_two_scaled<D, SHAPED>(st_state, kp, vp, kv_hi, qb, cc, mk, scale, base, page, g);
+      }
+      __syncwarp();  // every lane has consumed the stages: they may be refilled
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        if (issued >= my_n) break;
+        if ((issued & 31) == 0) refill_ids(issued >> 5);
+        issue(issued);
+        ++issued;
+      }
+    }
     StepRegs<D, FP8> r;
-    for (; done < my_n; ++done) {
+    for (; N == 1 && done < my_n; ++done) {
       const int st = done % R;
       const bool ok = __all_sync(0xffffffffu, sm100::mbar_wait(&wbar[st], (done / R) & 1, never,
                                                                 p.timeout_ns));
@@ -633,8 +837,7 @@ __global__ void __launch_bounds__(kThreads, Ring<D, FP8>::kCtasPerSm)
       const uint8_t* vstage = stage + 16 * RC::kRowBytes;
       read_k<D, FP8>(r, stage, step_base(done), kv_hi, g, t);
       if constexpr (!kLateV<D>) read_v<D, FP8>(r, vstage, step_base(done), kv_hi, g, t);
-      compute_step<D, FP8, SHAPED, SCALED>(st_state, r, vstage, kv_hi, qb, cc, mk, scale_of(done),
-                                           step_base(done), g, t);
+      compute_step<D, FP8, SHAPED>(st_state, r, vstage, kv_hi, qb, cc, mk, step_base(done), g, t);
       __syncwarp();  // every lane has consumed the stage: it may be refilled
       if (issued < my_n) {
         if ((issued & 31) == 0) refill_ids(issued >> 5);
@@ -805,7 +1008,7 @@ template <int D, bool FP8, bool SHAPED, bool SCALED = false>
 cudaError_t launch_decode_as(const KernelParams& p, cudaStream_t stream, bool after_prefill) {
   CUtensorMap mk, mv;
   const int elt = FP8 ? 1 : 2;
-  using PL = PageLayout<D, FP8>;
+  using PL = KernelPage<D, FP8, SCALED>;
   // one box = the 16 key rows of one KV head in one page, one 128-byte panel
   // of head dims (swizzled) or the whole row
   cudaError_t e = encode_kv_page_map(&mk, p.k_cache, elt, D, p.num_kv_heads, p.block_size,
