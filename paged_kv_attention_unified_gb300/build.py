@@ -48,8 +48,8 @@ _SOURCE_SUFFIXES = (".cu", ".cuh", ".cpp", ".h")
 # headers, the scheduler (the tiles it launches) and the TMA map encoding.
 _KERNEL_SOURCES = {
     "decode": ("decode.cu",),
-    "prefill": ("prefill.cu",),
-    "prefill_wide": ("prefill_wide.cu",),
+    "prefill": ("prefill.cu", "tile_pages.cuh"),
+    "prefill_wide": ("prefill_wide.cu", "tile_pages.cuh"),
     "append": ("append.cu",),
     "rope": ("rope.cu", "rope_device.cuh"),
     "fill": ("fill.cu", "rope_device.cuh"),

@@ -37,6 +37,7 @@
 #include "planner.h"
 #include "score_shape.cuh"
 #include "sm100.cuh"
+#include "tile_pages.cuh"
 #include "ua_device.cuh"
 #include "ua_kernels.h"
 
@@ -248,78 +249,30 @@ __device__ __forceinline__ bool take_item(const PrefillParams& p, const Bars<D, 
 }
 
 // ------------------------------------------------------------------ producers
-// Key tile j of a work tile into one ring slot: one TMA box per page (or per
-// 128 rows of a larger page) and 64-wide panel. Every page id is read from
-// the block table and checked; a missing or out-of-range page is loaded from
-// an out-of-range block coordinate, which TMA fills with zeros. So is one
-// whose keys lie between the sinks and the first query's window: a session may
-// have given such pages back.
-template <int D, bool F8>
-__device__ __forceinline__ void load_key_tile(const CUtensorMap* map, const PrefillParams& p,
-                                              const Item& tile, const Geometry& g, int j,
-                                              uint8_t* dst, uint32_t full) {
-  using L = Smem<D, F8>;
-  constexpr int kPanels = L::kPanels;
-  const int boxes = kKeys / p.rows_per_box;
-  const int base = g.key_of(j);
-  mbar_arrive_expect_tx(full, L::kTile);
-  if (boxes == 1) {
-    // Pages of at least a key tile: one box (and one page-table load).
-    int32_t blk = static_cast<int32_t>(p.num_blocks);  // out of range: zero fill
-    int32_t slot = 0;
-    if (base < g.kv_hi) {
-      const int32_t id =
-          p.block_tables[static_cast<int64_t>(tile.seq) * p.max_blocks_per_seq + base / p.block_size];
-      if (id >= 0 && static_cast<int64_t>(id) < p.num_blocks) {
-        blk = id;
-        slot = base % p.block_size;
-      } else {
-        record_error(p.err, UA_ERR_BOUNDS);
-      }
-    }
-#pragma unroll
-    for (int pn = 0; pn < kPanels; ++pn)
-      tma_load_4d(dst + pn * L::kPanel, map, full, pn * L::kPanelDims, tile.kv_head, slot, blk);
-    return;
-  }
-  const KeyGap unseen = key_gap(p.shape.sinks, p.window, g.ctx, 1);
-  for (int b = 0; b < boxes; ++b) {
-    const int key0 = base + b * p.rows_per_box;
-    int32_t blk = static_cast<int32_t>(p.num_blocks);  // out of range: zero fill
-    int32_t slot = 0;
-    if (key0 < g.kv_hi && !(key0 >= unseen.lo && key0 + p.rows_per_box <= unseen.hi)) {
-      const int32_t id =
-          p.block_tables[static_cast<int64_t>(tile.seq) * p.max_blocks_per_seq + key0 / p.block_size];
-      if (id >= 0 && static_cast<int64_t>(id) < p.num_blocks) {
-        blk = id;
-        slot = key0 % p.block_size;
-      } else {
-        record_error(p.err, UA_ERR_BOUNDS);
-      }
-    }
-    const int row_off = b * p.rows_per_box * 128;
-#pragma unroll
-    for (int pn = 0; pn < kPanels; ++pn)
-      tma_load_4d(dst + pn * L::kPanel + row_off, map, full, pn * L::kPanelDims, tile.kv_head,
-                  slot, blk);
-  }
-}
-
-// One thread of warp 0: per work tile, Q of query tile 0, the K ring, and Q
-// of query tile 1 after the first key tile (a Q buffer is refilled once the
-// last S MMA of the previous work tile has read it). One thread of warp 2
-// (kIsV): the V ring. Ring positions run on across the CTA's work tiles.
+// Warp 0: per work tile, Q of query tile 0, the K ring, and Q of query tile 1
+// after the first key tile (a Q buffer is refilled once the last S MMA of the
+// previous work tile has read it). Warp 2 (kIsV): the V ring. The first lane
+// loads Q; every lane looks up and copies its part of a key tile (tile_pages.cuh).
+// Ring positions run on across the CTA's work tiles.
 template <int D, bool F8, bool kIsV>
 __device__ __forceinline__ void producer_role(const CUtensorMap* map_q, const CUtensorMap* map_kv,
                                               const PrefillParams& p, const uint8_t* ring,
                                               uint8_t* sQ, uint8_t* sRing, uint32_t full,
                                               uint32_t empty, const Bars<D, F8>& bar,
-                                              volatile int32_t* abort, volatile int32_t* never) {
+                                              int lane, volatile int32_t* abort,
+                                              volatile int32_t* never) {
   using L = Smem<D, F8>;
   constexpr int kPanels = L::kPanels;
   constexpr int kStages = kIsV ? L::kVStages : L::kKStages;
-  prefetch_tmap(map_kv);
-  if (!kIsV && !F8) prefetch_tmap(map_q);
+  if (lane == 0) {
+    prefetch_tmap(map_kv);
+    if (!kIsV && !F8) prefetch_tmap(map_q);
+  }
+  // Whether the first lane's wait succeeded, for the whole warp.
+  auto all = [](bool first_ok) {
+    __syncwarp();
+    return __shfl_sync(0xffffffffu, first_ok ? 1 : 0, 0) != 0;
+  };
   const bool idle = (p.debug_flags & kDebugProducerIdle) != 0;
   int last_phase[kStages];
 #pragma unroll
@@ -344,29 +297,38 @@ __device__ __forceinline__ void producer_role(const CUtensorMap* map_q, const CU
     int step = 0;  // position in the ring sequence
     for (int k = 0; ok; ++k) {
       Item tile;
-      if (!take_item<D, F8>(p, bar, ring, k, tile, abort)) {
+      if (!__all_sync(0xffffffffu, take_item<D, F8>(p, bar, ring, k, tile, abort))) {
         ok = false;
         break;
       }
-      mbar_arrive(bar.item_empty(k % kItemSlots));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar.item_empty(k % kItemSlots));
       if (tile.end) break;
       const Geometry& g = tile.g;
       if (g.nmax <= 0) continue;
-      if (!kIsV) ok = load_q(tile, g, 0);
+      TilePages<kKeys, kPanels> pages;
+      if (!kIsV) ok = all(lane != 0 || load_q(tile, g, 0));
       for (int j = 0; ok && j < g.nmax; ++j, ++step) {
         const int s = step % kStages;
-        if (step >= kStages &&
-            !mbar_wait(empty + 8u * s, ((step / kStages) - 1) & 1, abort, p.timeout_ns)) {
+        const bool free = step < kStages ||
+                 mbar_wait(empty + 8u * s, ((step / kStages) - 1) & 1, abort, p.timeout_ns);
+        if (!__all_sync(0xffffffffu, free)) {
           ok = false;
           break;
         }
-        load_key_tile<D, F8>(map_kv, p, tile, g, j, sRing + s * L::kTile, full + 8u * s);
+        if (lane == 0) mbar_arrive_expect_tx(full + 8u * s, L::kTile);
+        __syncwarp();
+        pages.fetch(p, lane, tile.seq, g.ctx, g.key_of(j), g.kv_hi);
+        pages.copy(map_kv, p, lane, tile.kv_head, sRing + s * L::kTile, L::kPanel, L::kPanelDims,
+                   full + 8u * s);
         last_phase[s] = step / kStages;
-        if (!kIsV && j == 0) ok = load_q(tile, g, 1);
+        if (!kIsV && j == 0) ok = all(lane != 0 || load_q(tile, g, 1));
       }
     }
     if (!ok) give_up(p, abort);
   }
+  __syncwarp();  // the lanes' copies are issued
+  if (lane != 0) return;
   // Drain: every load issued completes before the CTA may exit.
 #pragma unroll
   for (int s = 0; s < kStages; ++s)
@@ -877,12 +839,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(
         SHAPE == kShapePlain ? kCtrlRegs : kShapedCtrlRegs));
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
       producer_role<D, F8, false>(&map_q, &map_k, p, ring, sQ, sK, bar.kfull(0), bar.kempty(0), bar,
-                              abort, never);
-    } else if (warp == 2 && lane == 0) {
+                                  lane, abort, never);
+    } else if (warp == 2) {
       producer_role<D, F8, true>(&map_q, &map_v, p, ring, sQ, sV, bar.vfull(0), bar.vempty(0), bar,
-                             abort, never);
+                                 lane, abort, never);
     } else if (warp == 1 && lane == 0) {
       mma_role<D, F8>(p, ring, sQ, sK, sV, tmem, bar, abort, never);
     } else if (warp == 3 && lane == 0) {

@@ -29,6 +29,7 @@
 #include "planner.h"
 #include "score_shape.cuh"
 #include "sm100.cuh"
+#include "tile_pages.cuh"
 #include "ua_device.cuh"
 #include "ua_kernels.h"
 
@@ -106,6 +107,10 @@ struct Item {
   int nsink, skip;               // key tiles before the keys that no row sees, and how many those are
   int end;                       // 1: no more items for this CTA
   int prefix;                    // keys below it are visible to every row (0: none)
+  // First key of key tile j.
+  __device__ __forceinline__ int key_of(int j) const {
+    return kv_lo + j * kKeys + (j >= nsink ? skip : 0);
+  }
 };
 static_assert(sizeof(Item) <= kItemBytes, "item descriptor too large");
 
@@ -180,70 +185,25 @@ __device__ __forceinline__ void scheduler_role(const PrefillParams& p, const Bar
 }
 
 // ------------------------------------------------------------------ producers
-// Key tile j of an item into one ring stage: one TMA box per page (or per 64
-// rows of a larger page) and 64-wide panel. Every page id is read from the
-// block table and checked; a missing or out-of-range page is loaded from an
-// out-of-range block coordinate, which TMA fills with zeros.
-template <int D>
-__device__ __forceinline__ void load_key_tile(const CUtensorMap* map, const PrefillParams& p,
-                                              const Item& it, int j, uint8_t* dst, uint32_t full) {
-  constexpr int kPanels = Geo<D>::kPanels, kStage = Geo<D>::kStage;
-  const int boxes = kKeys / p.rows_per_box;
-  const int base = it.kv_lo + j * kKeys + (j >= it.nsink ? it.skip : 0);
-  mbar_arrive_expect_tx(full, kStage);
-  if (boxes == 1) {
-    // Pages of at least a key tile: one box (and one page-table load).
-    int32_t blk = static_cast<int32_t>(p.num_blocks);  // out of range: zero fill
-    int32_t slot = 0;
-    if (base < it.kv_hi) {
-      const int32_t id =
-          p.block_tables[static_cast<int64_t>(it.seq) * p.max_blocks_per_seq + base / p.block_size];
-      if (id >= 0 && static_cast<int64_t>(id) < p.num_blocks) {
-        blk = id;
-        slot = base % p.block_size;
-      } else {
-        record_error(p.err, UA_ERR_BOUNDS);
-      }
-    }
-#pragma unroll
-    for (int pn = 0; pn < kPanels; ++pn)
-      tma_load_4d(dst + pn * kPanelKV, map, full, pn * 64, it.kv_head, slot, blk);
-    return;
-  }
-  const KeyGap unseen = key_gap(p.shape.sinks, p.window, it.ctx, 1);
-  for (int b = 0; b < boxes; ++b) {
-    const int key0 = base + b * p.rows_per_box;
-    int32_t blk = static_cast<int32_t>(p.num_blocks);  // out of range: zero fill
-    int32_t slot = 0;
-    // (pages between the sinks and the first query's window may have been given back)
-    if (key0 < it.kv_hi && !(key0 >= unseen.lo && key0 + p.rows_per_box <= unseen.hi)) {
-      const int32_t id =
-          p.block_tables[static_cast<int64_t>(it.seq) * p.max_blocks_per_seq + key0 / p.block_size];
-      if (id >= 0 && static_cast<int64_t>(id) < p.num_blocks) {
-        blk = id;
-        slot = key0 % p.block_size;
-      } else {
-        record_error(p.err, UA_ERR_BOUNDS);
-      }
-    }
-    const int row_off = b * p.rows_per_box * 128;
-#pragma unroll
-    for (int pn = 0; pn < kPanels; ++pn)
-      tma_load_4d(dst + pn * kPanelKV + row_off, map, full, pn * 64, it.kv_head, slot, blk);
-  }
-}
-
-// One thread of warp 0 (Q and the K ring) or of warp 2 (kIsV: the V ring).
+// Warp 0 (Q and the K ring) or warp 2 (kIsV: the V ring): the first lane loads Q,
+// every lane looks up and copies its part of a key tile (tile_pages.cuh).
 // Ring positions run on across items.
 template <int D, bool kIsV>
 __device__ __forceinline__ void producer_role(const CUtensorMap* map_q, const CUtensorMap* map_kv,
                                               const PrefillParams& p, const uint8_t* slot,
-                                              uint8_t* sQ, uint8_t* sRing, const Bars& bar,
+                                              uint8_t* sQ, uint8_t* sRing, const Bars& bar, int lane,
                                               volatile int32_t* abort, volatile int32_t* never) {
   constexpr int kPanels = Geo<D>::kPanels, kQBytes = Geo<D>::kQBytes, kStage = Geo<D>::kStage;
   constexpr int kStages = kIsV ? VS : KS;
-  prefetch_tmap(map_kv);
-  if (!kIsV) prefetch_tmap(map_q);
+  if (lane == 0) {
+    prefetch_tmap(map_kv);
+    if (!kIsV) prefetch_tmap(map_q);
+  }
+  // Whether the first lane's wait succeeded, for the whole warp.
+  auto all = [](bool first_ok) {
+    __syncwarp();
+    return __shfl_sync(0xffffffffu, first_ok ? 1 : 0, 0) != 0;
+  };
   const bool idle = (p.debug_flags & kDebugProducerIdle) != 0;
   int last_phase[kStages];
 #pragma unroll
@@ -254,39 +214,54 @@ __device__ __forceinline__ void producer_role(const CUtensorMap* map_q, const CU
     int step = 0;  // ring position
     for (int k = 0; ok; ++k) {
       Item it;
-      if (!take_item(p, bar, slot, k, it, abort)) {
+      if (!__all_sync(0xffffffffu, take_item(p, bar, slot, k, it, abort))) {
         ok = false;
         break;
       }
-      mbar_arrive(bar.item_empty());
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar.item_empty());
       if (it.end) break;
+      TilePages<kKeys, kPanels> pages;
       if (!kIsV) {
         // Q of this item, once the last S MMA of the previous item has read Q
-        if (q_loads > 0 && !mbar_wait(bar.q_empty(), (q_loads - 1) & 1, abort, p.timeout_ns)) {
+        bool free = true;
+        if (lane == 0) {
+          free = q_loads == 0 || mbar_wait(bar.q_empty(), (q_loads - 1) & 1, abort, p.timeout_ns);
+          if (free) {
+            mbar_arrive_expect_tx(bar.q_full(), kQBytes);
+#pragma unroll
+            for (int pn = 0; pn < kPanels; ++pn)
+              tma_load_3d(sQ + pn * kPanelQ, map_q, bar.q_full(), pn * 64, it.kv_head * p.qpk,
+                          it.q_start + it.row0 / p.qpk);
+          }
+        }
+        if (!all(free)) {
           ok = false;
           break;
         }
-        mbar_arrive_expect_tx(bar.q_full(), kQBytes);
-#pragma unroll
-        for (int pn = 0; pn < kPanels; ++pn)
-          tma_load_3d(sQ + pn * kPanelQ, map_q, bar.q_full(), pn * 64, it.kv_head * p.qpk,
-                      it.q_start + it.row0 / p.qpk);
         ++q_loads;
       }
       for (int j = 0; j < it.ntiles; ++j, ++step) {
         const int s = step % kStages;
         const uint32_t empty = kIsV ? bar.vempty(s) : bar.kempty(s);
-        if (step >= kStages &&
-            !mbar_wait(empty, ((step / kStages) - 1) & 1, abort, p.timeout_ns)) {
+        const uint32_t full = kIsV ? bar.vfull(s) : bar.kfull(s);
+        const bool free =
+            step < kStages || mbar_wait(empty, ((step / kStages) - 1) & 1, abort, p.timeout_ns);
+        if (!__all_sync(0xffffffffu, free)) {
           ok = false;
           break;
         }
-        load_key_tile<D>(map_kv, p, it, j, sRing + s * kStage, kIsV ? bar.vfull(s) : bar.kfull(s));
+        if (lane == 0) mbar_arrive_expect_tx(full, kStage);
+        __syncwarp();
+        pages.fetch(p, lane, it.seq, it.ctx, it.key_of(j), it.kv_hi);
+        pages.copy(map_kv, p, lane, it.kv_head, sRing + s * kStage, kPanelKV, 64, full);
         last_phase[s] = step / kStages;
       }
     }
     if (!ok) give_up(p, abort);
   }
+  __syncwarp();  // the lanes' copies are issued
+  if (lane != 0) return;
   // Drain: every load issued completes before the CTA may exit.
 #pragma unroll
   for (int s = 0; s < kStages; ++s) {
@@ -641,11 +616,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
 
   if (warp == 0) {
-    if (lane == 0) producer_role<D, false>(&map_q, &map_k, p, slot, sQ, sK, bar, abort, never);
+    producer_role<D, false>(&map_q, &map_k, p, slot, sQ, sK, bar, lane, abort, never);
   } else if (warp == 1) {
     if (lane == 0) mma_role<D>(p, slot, sQ, sK, sV, tmem, bar, abort, never);
   } else if (warp == 2) {
-    if (lane == 0) producer_role<D, true>(&map_q, &map_v, p, slot, sQ, sV, bar, abort, never);
+    producer_role<D, true>(&map_q, &map_v, p, slot, sQ, sV, bar, lane, abort, never);
   } else if (warp == 3) {
     if (lane == 0) scheduler_role(p, bar, slot, abort);
   } else {
