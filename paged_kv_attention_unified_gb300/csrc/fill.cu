@@ -18,10 +18,9 @@
 // head, or a part of one head's tokens where pages are long or heads are few: as
 // many tokens at a time as its 32 lanes hold, a lane owning the same 32 bytes of
 // a head as in the rotary append (rope_device.cuh), four such steps in flight.
-// The largest magnitude needs all of a page's new elements before the first is
-// written: they stay in registers where one round holds them, else they are read
-// a second time (from L2). (cos, sin) come from a table in shared memory, filled
-// once a round for the CTA's heads.
+// A page that takes several rounds is written under the scale so far, and what came
+// before its last growth once more at the end. (cos, sin) come from a table in shared
+// memory, filled once a round for the CTA's heads.
 // HBM-bound: 2 B read and 1 B written per new element of K and V, 4 B per element of q.
 #include <cstdint>
 
@@ -38,9 +37,16 @@ constexpr int kSteps = 4;  // token steps a warp holds in registers
 // Tokens one warp holds in a round.
 __host__ __device__ constexpr int warp_tokens(int head_dim) { return kSteps * (32 / (head_dim / 16)); }
 
-// (cos, sin) of a round: at most 4 warps' tokens, 512 / head_dim * 4 of them, and
-// head_dim / 2 pairs each.
-constexpr int kMostSmem = kWarps * kSteps * 512 / 2 * static_cast<int>(sizeof(float2));
+// The table of a round's (cos, sin): pair i of a token at 8 units of pairs by
+// remainder, so that lanes of neighbouring units read neighbouring places, and a row
+// to a token with as much again between rows as the lanes of one token read.
+__host__ __device__ constexpr int turn_units(int pairs) { return (pairs + 7) / 8; }
+__host__ __device__ constexpr int turn_row(int pairs) { return 9 * turn_units(pairs); }
+__device__ __forceinline__ int turn_at(int i, int pairs) {
+  return (i & 7) * turn_units(pairs) + (i >> 3);
+}
+// At most 4 warps' tokens, 512 / head_dim * 4 of them, of head_dim / 2 pairs.
+constexpr int kMostSmem = kWarps * kSteps * 512 / 16 * 9 * static_cast<int>(sizeof(float2));
 
 constexpr uint32_t kLeastScale = (127u - 100u) << 23, kMostScale = (127u + 100u) << 23;
 
@@ -70,7 +76,8 @@ template <Turn TURN>
 __device__ __forceinline__ void fill_block(const RopeTable& rope, const FillParams& p, int block) {
   extern __shared__ float2 turn[];  // [tokens of a round][pairs]
   __shared__ uint32_t copy[TURN == kTurnHalfOdd ? kWarps * 32 * kUnitWords : 1];
-  __shared__ float largest[kWarps];
+  __shared__ float largest[2][kWarps];
+  __shared__ int rounds_again[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const bool is_v = block & 1;
   const int groups = (p.num_kv_heads + p.heads_per_cta - 1) / p.heads_per_cta;
@@ -148,8 +155,9 @@ __device__ __forceinline__ void fill_block(const RopeTable& rope, const FillPara
         __syncthreads();  // the round before has been read
         for (int n = threadIdx.x; n < tokens * pairs; n += kThreads) {
           const int t = n / pairs, i = n - t * pairs, tok = r * round_tokens + t;
-          turn[n] = pair_turn(rope, p.positions, p.positions_stride, p.axes, tile.row0 + tok,
-                              tile.kv_lo + tok, i);
+          turn[t * turn_row(pairs) + turn_at(i, pairs)] =
+              pair_turn(rope, p.positions, p.positions_stride, p.axes, tile.row0 + tok,
+                        tile.kv_lo + tok, i);
         }
         __syncthreads();
       }
@@ -175,11 +183,11 @@ __device__ __forceinline__ void fill_block(const RopeTable& rope, const FillPara
         }
         const int tok = r * round_tokens + lane_token + i * at_once;
         if (!mine || !turns || tok >= tile.nrows) continue;
-        const float2* cs = turn + (lane_token + i * at_once) * pairs;
+        const float2* cs = turn + (lane_token + i * at_once) * turn_row(pairs);
         if constexpr (TURN == kTurnHalf) {
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            const float2 t = cs[8 * u + k];
+            const float2 t = cs[turn_at(8 * u + k, pairs)];
             const float a = y[k], b = y[8 + k];
             y[k] = fmaf(a, t.x, -b * t.y);
             y[8 + k] = fmaf(b, t.x, a * t.y);
@@ -188,7 +196,7 @@ __device__ __forceinline__ void fill_block(const RopeTable& rope, const FillPara
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             if (8 * u + k >= pairs) continue;
-            const float2 t = cs[8 * u + k];
+            const float2 t = cs[turn_at(8 * u + k, pairs)];
             const float a = y[2 * k], b = y[2 * k + 1];
             y[2 * k] = fmaf(a, t.x, -b * t.y);
             y[2 * k + 1] = fmaf(b, t.x, a * t.y);
@@ -204,7 +212,7 @@ __device__ __forceinline__ void fill_block(const RopeTable& rope, const FillPara
             for (int e = 0; e < 2; ++e) {
               const int at = 16 * u + 2 * k + e;
               if (at >= 2 * pairs) continue;
-              const float2 t = cs[at < pairs ? at : at - pairs];
+              const float2 t = cs[turn_at(at < pairs ? at : at - pairs, pairs)];
               const float partner = e ? bf16_hi(b) : bf16_lo(b);
               y[2 * k + e] = fmaf(y[2 * k + e], t.x, partner * (at < pairs ? -t.y : t.y));
             }
@@ -214,34 +222,13 @@ __device__ __forceinline__ void fill_block(const RopeTable& rope, const FillPara
     }
   };
 
-  float amax = 0.f;
-  for (int r = 0; r < rounds; ++r) {
-    take(r);
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i)
-#pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const float a = fabsf(x[i][k]);
-        amax = fmaxf(amax, a < INFINITY ? a : 0.f);
-      }
-  }
-  amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
-  if (share > 1) {
-    if (lane == 0) largest[warp] = amax;
-    __syncthreads();  // (also: every warp of a head has read the old scale)
-    for (int w = 0; w < share; ++w) amax = fmaxf(amax, largest[in_cta * share + w]);
-  }
-  const int n = old > 0.f ? doublings(amax, old) : 0;
-  const float scale = old > 0.f ? __uint_as_float(__float_as_uint(old) + (n << 23)) : fresh_scale(amax);
-  const uint32_t scale_bits = __float_as_uint(scale);
+  // Round after round: the scale so far, and the round's codes under it. Rounds
+  // written before the scale grew for the last time are written again after the
+  // last (they come from L2, most pages have none: a page's first tokens are
+  // nearly as loud as all of them).
+  float scale = 0.f, amax = 0.f;
   RopeScale div;
-  div.shift = __uint_as_float((254u << 23) - (scale_bits & 0x7f800000u));
-  div.mant = __uint_as_float((scale_bits & 0x7fffffu) | 0x3f800000u);
-  div.inv = __frcp_rn(div.mant);
-  if (active && part == 0 && lane == 0) *scale_at = scale;
-
-  for (int r = 0; r < rounds; ++r) {
-    if (rounds > 1) take(r);
+  auto write = [&](int r) {
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       const int tok = r * round_tokens + lane_token + i * at_once;
@@ -249,7 +236,16 @@ __device__ __forceinline__ void fill_block(const RopeTable& rope, const FillPara
       float lo[8], hi[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) lo[k] = x[i][k], hi[k] = x[i][8 + k];
-      const uint2 a = quantize8(lo, div), b = quantize8(hi, div);
+      uint2 a, b;
+      if (div.mant == 1.f) {  // a power of two, as the rule makes them: an exact product
+#pragma unroll
+        for (int k = 0; k < 8; ++k) lo[k] *= div.shift, hi[k] *= div.shift;
+        a = make_uint2(to_e4m3x4(lo[0], lo[1], lo[2], lo[3]), to_e4m3x4(lo[4], lo[5], lo[6], lo[7]));
+        b = make_uint2(to_e4m3x4(hi[0], hi[1], hi[2], hi[3]), to_e4m3x4(hi[4], hi[5], hi[6], hi[7]));
+      } else {
+        a = quantize8(lo, div);
+        b = quantize8(hi, div);
+      }
       uint8_t* row = dst + (first + tok) * dst_stride;
       if (off1 == off0 + 8) {
         *reinterpret_cast<uint4*>(row + off0) = make_uint4(a.x, a.y, b.x, b.y);
@@ -258,7 +254,61 @@ __device__ __forceinline__ void fill_block(const RopeTable& rope, const FillPara
         *reinterpret_cast<uint2*>(row + off1) = b;
       }
     }
+  };
+  // The largest finite magnitude of the round's elements of this warp.
+  auto warp_max = [&]() {
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+      for (int k = 0; k < 16; k += 2)
+        top = sm100::fmax3(top, fabsf(x[i][k]), fabsf(x[i][k + 1]));  // (passes over NaN)
+    top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+    if (top < INFINITY) return top;
+    top = 0.f;
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+      for (int k = 0; k < 16; ++k) top = fmaxf(top, fabsf(x[i][k]) < INFINITY ? fabsf(x[i][k]) : 0.f);
+    return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+  };
+  int grown = 0;  // rounds before the last growth
+  for (int r = 0; r < rounds; ++r) {
+    take(r);
+    float top = warp_max();
+    if (share > 1) {
+      if (lane == 0) largest[r & 1][warp] = top;
+      __syncthreads();  // (also: every warp of a head has read the old scale)
+      for (int w = 0; w < share; ++w) top = fmaxf(top, largest[r & 1][in_cta * share + w]);
+    }
+    amax = fmaxf(amax, top);
+    const float now = old > 0.f
+                          ? __uint_as_float(__float_as_uint(old) + (doublings(amax, old) << 23))
+                          : fresh_scale(amax);
+    if (now != scale) {
+      scale = now;
+      grown = r;
+      const uint32_t bits = __float_as_uint(scale);
+      div.shift = __uint_as_float((254u << 23) - (bits & 0x7f800000u));
+      div.mant = __uint_as_float((bits & 0x7fffffu) | 0x3f800000u);
+      div.inv = __frcp_rn(div.mant);
+    }
+    write(r);
   }
+  if (active && part == 0 && lane == 0) *scale_at = scale;
+  if (rounds > 1) {
+    // every warp of the CTA takes part in a round that one of them needs (`take` waits for all)
+    if (lane == 0) rounds_again[warp] = grown;
+    __syncthreads();
+    int again = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) again = max(again, rounds_again[w]);
+    for (int r = 0; r < again; ++r) {
+      take(r);
+      if (r < grown) write(r);
+    }
+  }
+  const int n = old > 0.f ? doublings(amax, old) : 0;
   // Earlier tokens of a page whose scale grew.
   if (n > 0 && mine) {
     const float down = __uint_as_float(static_cast<uint32_t>(127 - min(n, 126)) << 23);
@@ -278,7 +328,7 @@ __device__ __forceinline__ void fill_block(const RopeTable& rope, const FillPara
 }
 
 template <Turn TURN>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
     fill_kernel(const __grid_constant__ RopeTable rope, const FillParams p, const RopeAppendParams q,
                 int fill_blocks) {
   const int block = blockIdx.x;
@@ -307,20 +357,22 @@ cudaError_t launch(const RopeTable& rope, const FillParams& p, const RopeAppendP
 
 }  // namespace
 
-cudaError_t launch_fill(const RopeTable* rope, FillParams p, RopeAppendParams q,
+cudaError_t launch_fill(const RopeTable* rope, FillParams p, RopeAppendParams q, int sms,
                         cudaStream_t stream) {
   if (p.num_tiles <= 0) return cudaSuccess;
   if (p.tiles == nullptr || p.head_dim % 32 != 0 || p.head_dim > 256) return cudaErrorInvalidValue;
-  // Warps to a head: as few as hold a page's new tokens in one round.
+  // A head to a warp, but for heads that leave warps without one, and for so few
+  // CTAs that SMs go without: then a head's tokens are shared out, in fewer rounds.
   const int per_warp = warp_tokens(p.head_dim);
-  int share = 1;
-  while (share < kWarps && share * per_warp < p.max_rows) share *= 2;
+  int share = p.num_kv_heads == 1 ? 4 : (p.num_kv_heads == 2 ? 2 : 1);
+  auto ctas = [&]() { return int64_t{2} * p.num_tiles * ((p.num_kv_heads * share + kWarps - 1) / kWarps); };
+  while (share < kWarps && share * per_warp < p.max_rows && ctas() < 2 * sms) share *= 2;
   p.warps_per_head = share;
   p.heads_per_cta = kWarps / share < p.num_kv_heads ? kWarps / share : p.num_kv_heads;
   if (rope == nullptr) return launch<kTurnNone>(RopeTable{}, p, q, 0, stream);
   if (p.rotary_dim > 2 * kMaxPairs || p.rotary_dim > p.head_dim) return cudaErrorInvalidValue;
   const int tokens = per_warp * share < p.max_rows ? per_warp * share : p.max_rows;
-  const int smem = tokens * (p.rotary_dim / 2) * static_cast<int>(sizeof(float2));
+  const int smem = tokens * turn_row(p.rotary_dim / 2) * static_cast<int>(sizeof(float2));
   if (smem > kMostSmem) return cudaErrorInvalidValue;
   q.num_kv_heads = 0;
   if (p.interleaved) return launch<kTurnInterleaved>(*rope, p, q, smem, stream);

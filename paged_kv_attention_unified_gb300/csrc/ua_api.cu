@@ -873,7 +873,7 @@ ua_status run_fill(const ua_plan* plan, const ua::RopeTable* rope, const ua::Fil
   ua_plan* mp = const_cast<ua_plan*>(plan);
   mp->last_stream = cs;
   auto* ev = timing_begin(mp, 3, cs);
-  if (ua::launch_fill(rope, fp, q, cs) != cudaSuccess) return UA_ERR_CUDA;
+  if (ua::launch_fill(rope, fp, q, plan->info.num_sms, cs) != cudaSuccess) return UA_ERR_CUDA;
   timing_end(ev, cs);
   return UA_OK;
 }

@@ -212,7 +212,7 @@ struct FillParams {
 
 // rope null: keys as they are, q not used; else q holds the queries' part
 // (its cache fields are not used).
-cudaError_t launch_fill(const RopeTable* rope, FillParams p, RopeAppendParams q,
+cudaError_t launch_fill(const RopeTable* rope, FillParams p, RopeAppendParams q, int sms,
                         cudaStream_t stream);
 
 // fp8 prefill staging: e4m3 pages of the prefill sequences -> bf16 staging
