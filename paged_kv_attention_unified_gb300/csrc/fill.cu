@@ -153,11 +153,16 @@ __device__ __forceinline__ void fill_block(const RopeTable& rope, const FillPara
       if (!is_v) {
         const int tokens = min(round_tokens, tile.nrows - r * round_tokens);
         __syncthreads();  // the round before has been read
-        for (int n = threadIdx.x; n < tokens * pairs; n += kThreads) {
-          const int t = n / pairs, i = n - t * pairs, tok = r * round_tokens + t;
-          turn[t * turn_row(pairs) + turn_at(i, pairs)] =
-              pair_turn(rope, p.positions, p.positions_stride, p.axes, tile.row0 + tok,
-                        tile.kv_lo + tok, i);
+        // a pair to a thread, or two threads and more
+        const int wide = 32 - __clz(max(pairs - 1, 1));  // threads to a token, as a power of two
+        const int i = threadIdx.x & ((1 << wide) - 1);
+        const int at = turn_at(i, pairs);
+        if (i < pairs) {
+          const PairFrequency f(rope, p.positions, p.positions_stride, p.axes, i);
+          for (int t = threadIdx.x >> wide; t < tokens; t += kThreads >> wide) {
+            const int tok = r * round_tokens + t;
+            turn[t * turn_row(pairs) + at] = f.at(tile.row0 + tok, tile.kv_lo + tok);
+          }
         }
         __syncthreads();
       }
@@ -228,7 +233,54 @@ __device__ __forceinline__ void fill_block(const RopeTable& rope, const FillPara
   // nearly as loud as all of them).
   float scale = 0.f, amax = 0.f;
   RopeScale div;
-  auto write = [&](int r) {
+  int grown = 0;  // rounds before the last growth
+  int turns_left = rounds;
+  for (int it = 0; it < turns_left; ++it) {
+    const bool again = it >= rounds;
+    const int r = again ? it - rounds : it;
+    take(r);
+    if (!again) {
+      // The largest finite magnitude of the round's elements (fmax3 passes over NaN).
+      float top = 0.f;
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+        for (int k = 0; k < 16; k += 2) top = sm100::fmax3(top, fabsf(x[i][k]), fabsf(x[i][k + 1]));
+      top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+      if (top == INFINITY) {
+        top = 0.f;
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+          for (int k = 0; k < 16; ++k) top = fmaxf(top, fabsf(x[i][k]) < INFINITY ? fabsf(x[i][k]) : 0.f);
+        top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+      }
+      if (share > 1) {
+        if (lane == 0) largest[r & 1][warp] = top;
+        __syncthreads();  // (also: every warp of a head has read the old scale)
+        for (int w = 0; w < share; ++w) top = fmaxf(top, largest[r & 1][in_cta * share + w]);
+      }
+      amax = fmaxf(amax, top);
+      const float now = old > 0.f
+                            ? __uint_as_float(__float_as_uint(old) + (doublings(amax, old) << 23))
+                            : fresh_scale(amax);
+      if (now != scale) {
+        scale = now;
+        grown = r;
+        const uint32_t bits = __float_as_uint(scale);
+        div.shift = __uint_as_float((254u << 23) - (bits & 0x7f800000u));
+        div.mant = __uint_as_float((bits & 0x7fffffu) | 0x3f800000u);
+        div.inv = __frcp_rn(div.mant);
+      }
+      if (r == rounds - 1 && rounds > 1) {
+        // a round that one warp needs again is one for the whole CTA (`take` waits for all)
+        if (lane == 0) rounds_again[warp] = grown;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) turns_left = max(turns_left, rounds + rounds_again[w]);
+      }
+    }
+    if (again && r >= grown) continue;
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       const int tok = r * round_tokens + lane_token + i * at_once;
@@ -254,60 +306,8 @@ __device__ __forceinline__ void fill_block(const RopeTable& rope, const FillPara
         *reinterpret_cast<uint2*>(row + off1) = b;
       }
     }
-  };
-  // The largest finite magnitude of the round's elements of this warp.
-  auto warp_max = [&]() {
-    float top = 0.f;
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i)
-#pragma unroll
-      for (int k = 0; k < 16; k += 2)
-        top = sm100::fmax3(top, fabsf(x[i][k]), fabsf(x[i][k + 1]));  // (passes over NaN)
-    top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
-    if (top < INFINITY) return top;
-    top = 0.f;
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i)
-#pragma unroll
-      for (int k = 0; k < 16; ++k) top = fmaxf(top, fabsf(x[i][k]) < INFINITY ? fabsf(x[i][k]) : 0.f);
-    return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
-  };
-  int grown = 0;  // rounds before the last growth
-  for (int r = 0; r < rounds; ++r) {
-    take(r);
-    float top = warp_max();
-    if (share > 1) {
-      if (lane == 0) largest[r & 1][warp] = top;
-      __syncthreads();  // (also: every warp of a head has read the old scale)
-      for (int w = 0; w < share; ++w) top = fmaxf(top, largest[r & 1][in_cta * share + w]);
-    }
-    amax = fmaxf(amax, top);
-    const float now = old > 0.f
-                          ? __uint_as_float(__float_as_uint(old) + (doublings(amax, old) << 23))
-                          : fresh_scale(amax);
-    if (now != scale) {
-      scale = now;
-      grown = r;
-      const uint32_t bits = __float_as_uint(scale);
-      div.shift = __uint_as_float((254u << 23) - (bits & 0x7f800000u));
-      div.mant = __uint_as_float((bits & 0x7fffffu) | 0x3f800000u);
-      div.inv = __frcp_rn(div.mant);
-    }
-    write(r);
   }
   if (active && part == 0 && lane == 0) *scale_at = scale;
-  if (rounds > 1) {
-    // every warp of the CTA takes part in a round that one of them needs (`take` waits for all)
-    if (lane == 0) rounds_again[warp] = grown;
-    __syncthreads();
-    int again = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) again = max(again, rounds_again[w]);
-    for (int r = 0; r < again; ++r) {
-      take(r);
-      if (r < grown) write(r);
-    }
-  }
   const int n = old > 0.f ? doublings(amax, old) : 0;
   // Earlier tokens of a page whose scale grew.
   if (n > 0 && mine) {

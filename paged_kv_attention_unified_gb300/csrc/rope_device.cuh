@@ -71,6 +71,22 @@ __device__ __forceinline__ float2 pair_turn(const RopeTable& rope, const int32_t
   return make_float2(cs.x * rope.amplitude, cs.y * rope.amplitude);
 }
 
+// The same for one pair at many tokens.
+struct PairFrequency {
+  float hi, lo, amplitude;
+  const int32_t* row;  // the pair's axis of the positions, or null
+  __device__ __forceinline__ PairFrequency(const RopeTable& rope, const int32_t* positions,
+                                           int64_t stride, int axes, int i)
+      : hi(ld_param(rope.hi + i)), lo(ld_param(rope.lo + i)), amplitude(rope.amplitude),
+        row(positions) {
+    if (positions && axes > 1) row += ld_param(rope.axis + i) * stride;
+  }
+  __device__ __forceinline__ float2 at(int token, int slot_pos) const {
+    const float2 cs = rotation(row ? row[token] : slot_pos, hi, lo);
+    return make_float2(cs.x * amplitude, cs.y * amplitude);
+  }
+};
+
 // Eight values of a chunk as binary32, and back.
 __device__ __forceinline__ void widen8(uint4 w, float (&x)[8]) {
   x[0] = bf16_lo(w.x), x[1] = bf16_hi(w.x), x[2] = bf16_lo(w.y), x[3] = bf16_hi(w.y);
