@@ -368,13 +368,14 @@ def ua_rope_append_kv(plan, rope, q, k_new, v_new, q_out, k_cache, v_cache, bloc
     tokens, whose token rows may be strided. positions: int32 [tokens], or
     [axes, tokens] with a row for each axis of the rope (the rows' distance is
     free)."""
-    _rope_append(plan, None, rope, q, k_new, v_new, q_out, k_cache, v_cache, block_tables,
+    _rope_append(plan, None, rope, None, q, k_new, v_new, q_out, k_cache, v_cache, block_tables,
                  num_blocks, positions, k_scale, v_scale, stream)
 
 
-def _rope_append(plan, batch, rope, q, k_new, v_new, q_out, k_cache, v_cache, block_tables,
+def _rope_append(plan, batch, rope, axes, q, k_new, v_new, q_out, k_cache, v_cache, block_tables,
                  num_blocks, positions, k_scale, v_scale, stream):
-    """batch: the plan's (tokens, query heads, KV heads, head_dim), None to ask it."""
+    """batch: the plan's (tokens, query heads, KV heads, head_dim), axes: the rope's;
+    None to ask them."""
     import torch
     bf16, shape = torch.bfloat16, q.shape
     n = shape[0]
@@ -387,13 +388,14 @@ def _rope_append(plan, batch, rope, q, k_new, v_new, q_out, k_cache, v_cache, bl
         raise ValueError("q_out: a contiguous tensor of q's shape, type and device is needed")
     pp, p_stride = None, 0
     if positions is not None and positions.dim() == 2:
-        if positions.shape != (ua_rope_get_axes(rope), n) or positions.dtype != torch.int32 or (
-                positions.get_device() != dev or (n > 1 and positions.stride(1) != 1)):
+        axes = ua_rope_get_axes(rope) if axes is None else axes
+        rows, step = positions.stride()
+        if positions.shape != (axes, n) or positions.dtype != torch.int32 or (
+                positions.get_device() != dev or (n > 1 and step != 1)):
             raise ValueError("positions: an int32 tensor [axes of the rope, tokens of q] with "
                              f"contiguous rows, on q's device, is needed ({positions.dtype}, shape "
-                             f"{tuple(positions.shape)}, {ua_rope_get_axes(rope)} axes, {n} tokens)")
-        # (the distance of one row, or of rows of one token, says nothing)
-        pp, p_stride = positions.data_ptr(), positions.stride(0) if len(positions) > 1 else n
+                             f"{tuple(positions.shape)}, {axes} axes, {n} tokens)")
+        pp, p_stride = positions.data_ptr(), rows if axes > 1 else n  # (one row's distance says nothing)
         if p_stride < n:
             raise ValueError("positions: rows that overlap (expand() gives such; copy them)")
     elif positions is not None:
@@ -575,6 +577,7 @@ class Rope:
     def __init__(self, inv_freq, interleaved=False, amplitude=1.0, axes=None):
         self.handle = None
         self.handle = ua_rope_create(inv_freq, interleaved, amplitude, axes)
+        self.num_axes = ua_rope_get_axes(self.handle)
 
     @classmethod
     def scaled(cls, rotary_dim, base=10000.0, scaling=UA_ROPE_PLAIN, factor=1.0,
@@ -659,10 +662,12 @@ class Plan:
                        num_blocks, positions=None, k_scale=1.0, v_scale=1.0, stream=None):
         if len(q) < self.num_tokens:
             raise ValueError(f"q: {len(q)} tokens, the plan has {self.num_tokens}")
-        handle = _stream_handle(stream)
+        handle, axes = _stream_handle(stream), None
+        if isinstance(rope, Rope):
+            rope, axes = rope.handle, rope.num_axes
         _rope_append(self.handle, (self.num_tokens, self.num_q_heads, self.num_kv_heads, self.head_dim),
-                     rope.handle if isinstance(rope, Rope) else rope, q, k_new, v_new, q_out, k_cache,
-                     v_cache, block_tables, num_blocks, positions, k_scale, v_scale, handle)
+                     rope, axes, q, k_new, v_new, q_out, k_cache, v_cache, block_tables, num_blocks,
+                     positions, k_scale, v_scale, handle)
         if self._scales and handle not in self._scales_streams:
             self._scales_used(stream, handle)
 

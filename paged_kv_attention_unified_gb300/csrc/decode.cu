@@ -429,14 +429,18 @@ struct ScaledPage {
 
 // The two steps at base[0] and base[1] (their K and V rows at kp and vp): as
 // compute_step, with one reference for both. A step past kv_hi contributes nothing.
-template <int D, bool SHAPED>
+// release() refills the stages, by the whole warp: at the end, and above head_dim
+// 128, where an SM holds half as many warps, as soon as nothing of them is left to
+// be read (16 x 30000 keys, head_dim 192: 320 / 267 us; head_dim 256, 64 x 4096: 199 /
+// 178; but at 128, 8 x 131072 343 / 359 us).
+template <int D, bool SHAPED, class Release>
 __device__ __forceinline__ void compute_two_scaled(WarpState<D>& st, const uint8_t* const (&kp)[2],
                                                    const uint8_t* const (&vp)[2], int kv_hi,
                                                    const uint32_t (&qb)[D / 16][2],
                                                    const float (&cq)[2], const StepMask& mk,
                                                    const StepScale (&scale)[2],
                                                    const int (&base)[2], const ScaledPage<D>& page,
-                                                   int g) {
+                                                   int g, const Release& release) {
   using C = DecodeCfg<D, true>;
   StepRegs<D, true> r[2];
   const bool all = base[1] + 16 <= kv_hi;  // (the second step is the later one)
@@ -461,7 +465,7 @@ __device__ __forceinline__ void compute_two_scaled(WarpState<D>& st, const uint8
       mma16816<true>(s[n], a, qb[c][0], qb[c][1]);
     }
   }
-  if constexpr (!kLateV<D>) read_v();
+  read_v();
   float x[2][4], v_inv[2];
 #pragma unroll
   for (int n = 0; n < 2; ++n) {
@@ -493,13 +497,19 @@ __device__ __forceinline__ void compute_two_scaled(WarpState<D>& st, const uint8
       }
     }
   }
+  float top[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    top[j] = fmaxf(fmaxf(x[0][j], x[0][j + 2]), fmaxf(x[1][j], x[1][j + 2]));
+    top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], 4));
+    top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], 8));
+    top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], 16));
+  }
+  if constexpr (kLateV<D>) release();
   float p[2][4], alpha[2];
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
-    float mx = fmaxf(fmaxf(x[0][j], x[0][j + 2]), fmaxf(x[1][j], x[1][j + 2]));
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+    const float mx = top[j];
     const bool first = st.m[j] == -INFINITY;
     const float m_new = fmaxf(st.m[j], mx);
     const bool grow = first || (m_new > st.m[j] + kRescaleThreshold);
@@ -526,7 +536,6 @@ __device__ __forceinline__ void compute_two_scaled(WarpState<D>& st, const uint8
       st.acc[c][3] *= alpha[1];
     }
   }
-  if constexpr (kLateV<D>) read_v();
 #pragma unroll
   for (int n = 0; n < 2; ++n) {
     const uint32_t pb0 = movmatrix_trans(pack2<true>(p[n][0], p[n][1]));
@@ -542,6 +551,7 @@ __device__ __forceinline__ void compute_two_scaled(WarpState<D>& st, const uint8
       mma16816<true>(st.acc[c], a, pb0, pb1);
     }
   }
+  if constexpr (!kLateV<D>) release();
 }
 
 // Shared memory of one CTA: a ring of R stages per warp, each holding the K
@@ -813,15 +823,19 @@ __global__ void __launch_bounds__(kThreads, Ring<D, FP8>::kCtasPerSm)
         const uint8_t* const vp[2] = {kp[0] + 16 * RC::kRowBytes, kp[1] + 16 * RC::kRowBytes};
         const int base[2] = {step_base(done), done + 1 < my_n ? step_base(done + 1) : kv_hi};
         const StepScale scale[2] = {scale_of(done), scale_of(more)};
-        compute_two_scaled<D, SHAPED>(st_state, kp, vp, kv_hi, qb, cc, mk, scale, base, page, g);
-      }
-      __syncwarp();  // every lane has consumed the stages: they may be refilled
+        auto refill = [&]() {
+          // orders every lane's reads before the first lane's proxy fence and copies
+          __syncwarp();
 #pragma unroll
-      for (int n = 0; n < N; ++n) {
-        if (issued >= my_n) break;
-        if ((issued & 31) == 0) refill_ids(issued >> 5);
-        issue(issued);
-        ++issued;
+          for (int n = 0; n < 2; ++n) {
+            if (issued >= my_n) break;
+            if ((issued & 31) == 0) refill_ids(issued >> 5);
+            issue(issued);
+            ++issued;
+          }
+        };
+        compute_two_scaled<D, SHAPED>(st_state, kp, vp, kv_hi, qb, cc, mk, scale, base, page, g,
+                                      refill);
       }
     }
     StepRegs<D, FP8> r;

@@ -47,8 +47,8 @@ KeyGap gap_of(const Problem& p, int32_t ctx, int32_t row0, int32_t step) {
 // holding only 12 % of a tile). Equal pieces run in waves, so the step takes
 // about ceil(T * k / slots) * (L / k + overhead); the k that minimises this
 // (the fewest pieces on a tie) sets the length.
-int64_t wave_fit_chunk(int64_t tiles, int64_t len, int64_t slots) {
-  const int64_t k_max = std::min<int64_t>(UA_MAX_SPLITS, std::max<int64_t>(1, len / kMinSplitTokens));
+int64_t wave_fit_chunk(int64_t tiles, int64_t len, int64_t slots, int64_t min_split) {
+  const int64_t k_max = std::min<int64_t>(UA_MAX_SPLITS, std::max<int64_t>(1, len / min_split));
   int64_t best_size = len, best_cost = INT64_MAX;
   for (int64_t k = 1; k <= k_max; ++k) {
     const int64_t size = round_up(ceil_div(len, k), kKeyStep);
@@ -304,16 +304,17 @@ ua_status build_schedule(const Problem& p, Schedule* out) {
     shortest = std::min(shortest, b.keys());
   }
   int64_t chunk = 0;  // 0: do not split
+  const int64_t min_split = p.sinks > 0 && p.window > 0 ? kMinSplitTokensSinks : kMinSplitTokens;
   const int64_t slots = static_cast<int64_t>(num_sms) * decode_ctas_per_sm(p.head_dim, p.kv_dtype == UA_KV_BF16 ? 2 : 1);
   if (p.num_splits == 0 && n_tiles > 0 && total > 0) {
-    chunk = round_up(std::max<int64_t>(kMinSplitTokens, ceil_div(total, slots)), kKeyStep);
+    chunk = round_up(std::max<int64_t>(min_split, ceil_div(total, slots)), kKeyStep);
     chunk = std::max<int64_t>(chunk, round_up(ceil_div(longest, UA_MAX_SPLITS), kKeyStep));
     if (chunk < longest && shortest * 16 >= longest * 15) {
       // Tiles of (nearly) one length: unsplit when they alone fill HBM in
       // one wave (bf16, rows of at least 256 bytes), else whole waves.
       const bool saturating = p.kv_dtype == UA_KV_BF16 && p.head_dim >= 128 &&
                               n_tiles >= kDecodeSaturatingCtas && n_tiles <= slots;
-      chunk = saturating ? longest : wave_fit_chunk(n_tiles, longest, slots);
+      chunk = saturating ? longest : wave_fit_chunk(n_tiles, longest, slots, min_split);
     }
     if (chunk >= longest) chunk = 0;
   }
@@ -351,7 +352,7 @@ ua_status build_schedule(const Problem& p, Schedule* out) {
     else
       plan[i] = Cut{len, 1};
     if (tail_k > 0) {
-      const int64_t n = std::min<int64_t>(tail_k, len / kMinSplitTokens);
+      const int64_t n = std::min<int64_t>(tail_k, len / min_split);
       late_plan[i] = n >= 2 ? cut(len, n) : Cut{len, 1};
     }
   }

@@ -139,6 +139,10 @@ constexpr int kPieceOverheadTokens = 128;
 constexpr int kDecodeSaturatingCtas = 256;
 // Smallest automatic split piece, in key tokens.
 constexpr int kMinSplitTokens = 256;
+// And with sinks, where a decode tile's keys are as few as the window for good (one
+// token, 8 KV heads, window 1024 and 4 sinks, in 4 / 8 / 16 / 32 pieces 15.4 / 14.3
+// / 14.3 / 16.4 us).
+constexpr int kMinSplitTokensSinks = 128;
 // Default: sequences with q_len * qpk above this go to the prefill kernel
 // (when it can take the problem; otherwise every sequence is decode work).
 constexpr int kDefaultDecodeRowsMax = 32;
