@@ -752,7 +752,7 @@ __global__ void __launch_bounds__(kThreads, Ring<D, FP8>::kCtasPerSm)
   // (a step is computed at most a ring after it was issued). The copy at a refill
   // waits for loads that are a chunk old; the new ones are waited for by the first
   // step that needs them.
-  int32_t ids = -1;
+  int32_t ids = -1, slots = 0;  // (slots: of the step in its page, looked up with it)
   StepScale of_issue{1.f, 1.f}, of_before{1.f, 1.f};
   int issue_chunk = 0;
   auto refill_ids = [&](int c) {
@@ -761,6 +761,7 @@ __global__ void __launch_bounds__(kThreads, Ring<D, FP8>::kCtasPerSm)
                                     step_base(k) / p.block_size]
                    : -1;
     if constexpr (SCALED) {
+      slots = step_base(k) % p.block_size;
       of_before = of_issue;
       issue_chunk = c;
       of_issue = StepScale{1.f, 1.f};
@@ -782,8 +783,10 @@ __global__ void __launch_bounds__(kThreads, Ring<D, FP8>::kCtasPerSm)
   // Whole-warp call: every lane takes part in the shuffle, lane 0 issues.
   auto issue = [&](int k) {
     const int32_t id = __shfl_sync(0xffffffffu, ids, k & 31);
+    int32_t slot = 0;
+    if constexpr (SCALED) slot = __shfl_sync(0xffffffffu, slots, k & 31);
     if (lane == 0) {
-      const int base = step_base(k);
+      if constexpr (!SCALED) slot = step_base(k) % p.block_size;
       int32_t blk = static_cast<int32_t>(p.num_blocks);  // out of range: TMA fills zeros
       if (id >= 0 && static_cast<int64_t>(id) < p.num_blocks) blk = id;
       else record_error(p.err, UA_ERR_BOUNDS);
@@ -795,9 +798,9 @@ __global__ void __launch_bounds__(kThreads, Ring<D, FP8>::kCtasPerSm)
 #pragma unroll
       for (int pn = 0; pn < PL::kPanels; ++pn) {
         sm100::tma_load_4d(stage + pn * PL::kPanelBytes, &map_k, &wbar[st], pn * PL::kBoxDims,
-                           tile.kv_head, base % p.block_size, blk);
+                           tile.kv_head, slot, blk);
         sm100::tma_load_4d(stage + 16 * RC::kRowBytes + pn * PL::kPanelBytes, &map_v, &wbar[st],
-                           pn * PL::kBoxDims, tile.kv_head, base % p.block_size, blk);
+                           pn * PL::kBoxDims, tile.kv_head, slot, blk);
       }
     }
   };
