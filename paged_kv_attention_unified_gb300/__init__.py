@@ -369,11 +369,11 @@ def ua_rope_append_kv(plan, rope, q, k_new, v_new, q_out, k_cache, v_cache, bloc
     [axes, tokens] with a row for each axis of the rope (the rows' distance is
     free)."""
     _rope_append(plan, None, rope, None, q, k_new, v_new, q_out, k_cache, v_cache, block_tables,
-                 num_blocks, positions, k_scale, v_scale, stream)
+                 num_blocks, positions, k_scale, v_scale, _stream_handle(stream))
 
 
 def _rope_append(plan, batch, rope, axes, q, k_new, v_new, q_out, k_cache, v_cache, block_tables,
-                 num_blocks, positions, k_scale, v_scale, stream):
+                 num_blocks, positions, k_scale, v_scale, stream_handle):
     """batch: the plan's (tokens, query heads, KV heads, head_dim), axes: the rope's;
     None to ask them."""
     import torch
@@ -395,9 +395,10 @@ def _rope_append(plan, batch, rope, axes, q, k_new, v_new, q_out, k_cache, v_cac
             raise ValueError("positions: an int32 tensor [axes of the rope, tokens of q] with "
                              f"contiguous rows, on q's device, is needed ({positions.dtype}, shape "
                              f"{tuple(positions.shape)}, {axes} axes, {n} tokens)")
-        pp, p_stride = positions.data_ptr(), rows if axes > 1 else n  # (one row's distance says nothing)
-        if p_stride < n:
-            raise ValueError("positions: rows that overlap (expand() gives such; copy them)")
+        if n:
+            pp, p_stride = positions.data_ptr(), rows if axes > 1 else n  # (one row has no distance)
+            if p_stride < n:
+                raise ValueError("positions: rows that overlap (expand() gives such; copy them)")
     elif positions is not None:
         if positions.shape != (n,) or not positions.is_contiguous() or (
                 positions.dtype != torch.int32 or positions.get_device() != dev):
@@ -417,16 +418,15 @@ def _rope_append(plan, batch, rope, axes, q, k_new, v_new, q_out, k_cache, v_cac
             k_cache if isinstance(k_cache, int) else k_cache.data_ptr(),
             v_cache if isinstance(v_cache, int) else v_cache.data_ptr(),
             block_tables if isinstance(block_tables, int) else block_tables.data_ptr(),
-            int(num_blocks), pp, p_stride, float(k_scale), float(v_scale),
-            _stream_handle(stream)), "ua_rope_append_kv_axes")
+            int(num_blocks), pp, p_stride, float(k_scale), float(v_scale), stream_handle),
+            "ua_rope_append_kv_axes")
         return
     _check(lib().ua_rope_append_kv(
         plan, rope, qp, qs, kp, ks, vp, vs, q_out.data_ptr(),
         k_cache if isinstance(k_cache, int) else k_cache.data_ptr(),
         v_cache if isinstance(v_cache, int) else v_cache.data_ptr(),
         block_tables if isinstance(block_tables, int) else block_tables.data_ptr(),
-        int(num_blocks), pp, float(k_scale), float(v_scale), _stream_handle(stream)),
-        "ua_rope_append_kv")
+        int(num_blocks), pp, float(k_scale), float(v_scale), stream_handle), "ua_rope_append_kv")
 
 
 def ua_forward_oneshot(q, k_cache, v_cache, out, cu_query_lens_host, kv_lens_host,

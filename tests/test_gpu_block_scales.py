@@ -517,3 +517,82 @@ def test_scales_live_until_the_streams_are_done():
         torch.cuda.synchronize()
         assert torch.equal(got, want)
         del junk
+
+
+def test_pages_beyond_32_bits():
+    """Pages whose first element lies past 2^32: appended to and read as the first ones are."""
+    hkv, d, bs, need = 2, 128, 16, 5
+    blocks = 2 ** 32 // (bs * hkv * d) + 64
+    k_cache, v_cache = (torch.zeros(blocks, bs, hkv, d, dtype=torch.uint8, device="cuda") for _ in range(2))
+    ks, vs = (torch.zeros(blocks, hkv, device="cuda") for _ in range(2))
+    g = torch.Generator().manual_seed(43)
+    q, k, v = (torch.randn(77, h, d, generator=g).to(torch.bfloat16).cuda() for h in (4, hkv, hkv))
+    cu, kv = torch.tensor([0, 77], dtype=torch.int32, device="cuda"), torch.tensor([77], dtype=torch.int32, device="cuda")
+    outs = {}
+    for rows in (0, 10 ** 6):  # decode_rows_max: in the prefill kernel over a staged copy, in the decode kernel
+        for last in (False, True):
+            pages = torch.arange(need, dtype=torch.int32, device="cuda")
+            table = (blocks - 1 - pages if last else pages)[None].contiguous()
+            out = torch.empty_like(q)
+            with ua.Plan([0, 77], [77], 4, hkv, d, bs, need, kv_dtype=ua.UA_KV_FP8_E4M3, decode_rows_max=rows) as plan:
+                plan.set_block_scales(ks, vs)
+                plan.append_kv(k, v, k_cache, v_cache, table, blocks)
+                plan.forward(q, k_cache, v_cache, out, cu, kv, table, blocks, 77, 77, d ** -0.5)
+                assert plan.last_device_error() == 0
+            outs[rows, last] = out
+        assert torch.equal(outs[rows, False], outs[rows, True])
+    for cache, scales in ((k_cache, ks), (v_cache, vs)):
+        assert torch.equal(cache[:need], cache[-need:].flip(0)) and torch.equal(scales[:need], scales[-need:].flip(0))
+        assert int(cache[:need].count_nonzero()) > 0 and torch.all(scales[need:-need] == 0)
+
+
+def test_two_plans_on_two_streams_fill_one_cache():
+    """Sequences of the same cache, appended to and read by two plans at once."""
+    s = Step([150, 3, 90, 40], [150, 60, 200, 41], 8, 2, 128, 16, seed=44)
+    b, c = s.b, s.case
+    whole = [t.clone() for t in (b.k_cache, b.v_cache, *s.scales)]
+    with s.plan() as plan:
+        s.append(plan)
+        torch.cuda.synchronize()
+        want = [t.clone() for t in (b.k_cache, b.v_cache, *s.scales)]
+    for t, w in zip((b.k_cache, b.v_cache, *s.scales), whole):
+        t.copy_(w)
+    torch.cuda.synchronize()
+    streams, plans = [torch.cuda.Stream(), torch.cuda.Stream()], []
+    cu, kv = c.cu_query_lens.tolist(), c.kv_lens.tolist()
+    for st, (i, j) in zip(streams, ((0, 2), (2, 4))):
+        plan = ua.Plan([x - cu[i] for x in cu[i:j + 1]], kv[i:j], 8, 2, 128, 16, b.block_tables.shape[1],
+                       kv_dtype=ua.UA_KV_FP8_E4M3, stream=st)
+        plan.set_block_scales(*s.scales)
+        plans.append((plan, s.k[cu[i]:cu[j]].contiguous(), s.v[cu[i]:cu[j]].contiguous(), b.block_tables[i:j].contiguous()))
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for st, (plan, k, v, table) in zip(streams, plans):
+            plan.append_kv(k, v, b.k_cache, b.v_cache, table, b.num_blocks, stream=st)
+    torch.cuda.synchronize()
+    for t, w in zip((b.k_cache, b.v_cache, *s.scales), want):
+        assert torch.equal(t, w)
+    for plan, *_ in plans:
+        assert plan.last_device_error() == 0
+        plan.close()
+
+
+@pytest.mark.parametrize("rows", [0, 10 ** 6])
+def test_sinks_over_pages_given_back(rows):
+    """Pages that no query sees are gone, their scales hold anything."""
+    case = W.make_case("gone", [3, 70], [900, 640], 8, 2, 128, 16, kv_dtype=W.FP8, seed=45, window=100)
+    ks, vs = _scales(case, 3, True)
+    exp, spread = _expected(case, ks, vs, sinks=20, staged=rows == 0)
+    for s, (n, kv) in enumerate(zip(case.query_lens, case.kv_lens.tolist())):
+        for page in range(2, (kv - n - 100 + 1) // 16):
+            blk = int(case.block_tables[s, page])
+            case.block_tables[s, page] = -1
+            ks[blk], vs[blk] = float("nan"), 0.0
+            case.k_cache.view(torch.uint8)[blk] = case.v_cache.view(torch.uint8)[blk] = 0x7F
+    b = tu.to_device(case)
+    with tu.make_plan(b, sink_tokens=20, decode_rows_max=rows) as plan:
+        plan.set_block_scales(ks.cuda(), vs.cuda())
+        got = as_f64(tu.forward(plan, b))
+        assert plan.last_device_error() == 0
+    tail = 900 * 2.0 ** -25 * 448.0 * float(vs.nan_to_num(0.0).max())
+    assert np.all(np.abs(got - exp) <= 2.0 ** -8 * np.abs(exp) + 1.26 * 2.0 ** -8 * spread + tail)
