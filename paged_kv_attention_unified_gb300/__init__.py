@@ -369,13 +369,13 @@ def ua_rope_append_kv(plan, rope, q, k_new, v_new, q_out, k_cache, v_cache, bloc
     [axes, tokens] with a row for each axis of the rope (the rows' distance is
     free)."""
     _rope_append(plan, None, rope, None, q, k_new, v_new, q_out, k_cache, v_cache, block_tables,
-                 num_blocks, positions, k_scale, v_scale, _stream_handle(stream))
+                 num_blocks, positions, k_scale, v_scale, stream)
 
 
 def _rope_append(plan, batch, rope, axes, q, k_new, v_new, q_out, k_cache, v_cache, block_tables,
-                 num_blocks, positions, k_scale, v_scale, stream_handle):
+                 num_blocks, positions, k_scale, v_scale, stream):
     """batch: the plan's (tokens, query heads, KV heads, head_dim), axes: the rope's;
-    None to ask them."""
+    None to ask them. Returns the stream's handle."""
     import torch
     bf16, shape = torch.bfloat16, q.shape
     n = shape[0]
@@ -412,21 +412,23 @@ def _rope_append(plan, batch, rope, axes, q, k_new, v_new, q_out, k_cache, v_cac
         raise UAError(UA_ERR_INVALID_ARG, f"ua_rope_append_kv: q {tuple(shape)}, k_new "
                       f"{tuple(k_new.shape)}, v_new {tuple(v_new.shape)} on a plan of {tokens} "
                       f"tokens, {hq} query heads, {hkv} KV heads and head_dim {d}")
+    handle = _stream_handle(stream)
     if p_stride:
         _check(lib().ua_rope_append_kv_axes(
             plan, rope, qp, qs, kp, ks, vp, vs, q_out.data_ptr(),
             k_cache if isinstance(k_cache, int) else k_cache.data_ptr(),
             v_cache if isinstance(v_cache, int) else v_cache.data_ptr(),
             block_tables if isinstance(block_tables, int) else block_tables.data_ptr(),
-            int(num_blocks), pp, p_stride, float(k_scale), float(v_scale), stream_handle),
+            int(num_blocks), pp, p_stride, float(k_scale), float(v_scale), handle),
             "ua_rope_append_kv_axes")
-        return
+        return handle
     _check(lib().ua_rope_append_kv(
         plan, rope, qp, qs, kp, ks, vp, vs, q_out.data_ptr(),
         k_cache if isinstance(k_cache, int) else k_cache.data_ptr(),
         v_cache if isinstance(v_cache, int) else v_cache.data_ptr(),
         block_tables if isinstance(block_tables, int) else block_tables.data_ptr(),
-        int(num_blocks), pp, float(k_scale), float(v_scale), stream_handle), "ua_rope_append_kv")
+        int(num_blocks), pp, float(k_scale), float(v_scale), handle), "ua_rope_append_kv")
+    return handle
 
 
 def ua_forward_oneshot(q, k_cache, v_cache, out, cu_query_lens_host, kv_lens_host,
@@ -660,14 +662,15 @@ class Plan:
 
     def rope_append_kv(self, rope, q, k_new, v_new, q_out, k_cache, v_cache, block_tables,
                        num_blocks, positions=None, k_scale=1.0, v_scale=1.0, stream=None):
-        if len(q) < self.num_tokens:
-            raise ValueError(f"q: {len(q)} tokens, the plan has {self.num_tokens}")
-        handle, axes = _stream_handle(stream), None
+        if q.shape[0] < self.num_tokens:  # (len(q) takes four times as long)
+            raise ValueError(f"q: {q.shape[0]} tokens, the plan has {self.num_tokens}")
+        axes = None
         if isinstance(rope, Rope):
             rope, axes = rope.handle, rope.num_axes
-        _rope_append(self.handle, (self.num_tokens, self.num_q_heads, self.num_kv_heads, self.head_dim),
-                     rope, axes, q, k_new, v_new, q_out, k_cache, v_cache, block_tables, num_blocks,
-                     positions, k_scale, v_scale, handle)
+        handle = _rope_append(self.handle, (self.num_tokens, self.num_q_heads, self.num_kv_heads,
+                                            self.head_dim),
+                              rope, axes, q, k_new, v_new, q_out, k_cache, v_cache, block_tables,
+                              num_blocks, positions, k_scale, v_scale, stream)
         if self._scales and handle not in self._scales_streams:
             self._scales_used(stream, handle)
 

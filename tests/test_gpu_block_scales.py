@@ -596,3 +596,39 @@ def test_sinks_over_pages_given_back(rows):
         assert plan.last_device_error() == 0
     tail = 900 * 2.0 ** -25 * 448.0 * float(vs.nan_to_num(0.0).max())
     assert np.all(np.abs(got - exp) <= 2.0 ** -8 * np.abs(exp) + 1.26 * 2.0 ** -8 * spread + tail)
+
+
+@pytest.mark.parametrize("scales_first", [True, False])
+def test_scales_and_shaped_scores_in_either_order(scales_first):
+    """Prompts at a head dim whose shaped scores have a schedule of their own."""
+    case = W.make_case("order", [200, 150], [400, 750], 4, 2, 96, 16, kv_dtype=W.FP8, seed=46)
+    ks, vs = _scales(case, 4, True)
+    b = tu.to_device(case)
+    with tu.make_plan(b, decode_rows_max=0) as plan:
+        calls = [lambda: plan.set_block_scales(ks.cuda(), vs.cuda()), lambda: plan.set_scores(15.0)]
+        for call in calls if scales_first else calls[::-1]:
+            call()
+        assert plan.info.num_prefill_tiles > 0
+        got = as_f64(tu.forward(plan, b))
+        exp, spread = _expected(case, ks, vs, cap=15.0, staged=True)
+        assert np.all(np.abs(got - exp) <= 2.0 ** -8 * np.abs(exp) + 1.26 * 2.0 ** -8 * spread + 1e-30)
+        plan.set_scores()  # plain again: in the decode kernel
+        assert plan.info.num_prefill_tiles == 0
+        got = as_f64(tu.forward(plan, b))
+        exp, spread = _expected(case, ks, vs)
+        tail = 750 * 2.0 ** -25 * 448.0 * float(vs.max())
+        assert np.all(np.abs(got - exp) <= 2.0 ** -8 * np.abs(exp) + 1.26 * 2.0 ** -8 * spread + tail)
+        assert plan.last_device_error() == 0
+
+
+def test_plan_without_tokens():
+    b = tu.to_device(W.make_case("none", [0, 0], [20, 0], 4, 2, 64, 16, kv_dtype=W.FP8))
+    ks, vs = tu.new_block_scales(b)
+    with tu.make_plan(b, sink_tokens=3) as plan, ua.Rope([0.5] * 32, axes=[0, 1] * 16) as rope:
+        plan.set_block_scales(ks, vs)
+        rows = torch.zeros(0, 8, 64, dtype=torch.bfloat16, device="cuda")
+        plan.rope_append_kv(rope, rows[:, :4], rows[:, 4:6], rows[:, 6:], rows[:, :4].contiguous(), b.k_cache, b.v_cache,
+                            b.block_tables, b.num_blocks, positions=torch.zeros(2, 0, dtype=torch.int32, device="cuda"))
+        plan.append_kv(rows[:, :2], rows[:, 2:4], b.k_cache, b.v_cache, b.block_tables, b.num_blocks)
+        tu.forward(plan, b)
+        assert plan.last_device_error() == 0
