@@ -51,8 +51,8 @@
  * tcgen05 prefill kernel at head_dim 64 and 128 (tiles of one or two 128-row
  * query tiles, 128-key tiles) and one at head_dim 192 and 256 (one 128-row
  * query tile and 64-key tiles at a time, block sizes that 64 divides or that
- * divide 64), which take shaped scores at the other head dims too
- * (ua_plan_set_scores, ua_plan_create_prefix);
+ * divide 64), which take shaped scores and sinks at the other head dims too
+ * (ua_plan_set_scores, ua_plan_create_prefix, ua_plan_create_sinks);
  * block_size a multiple of 16; any GQA ratio (the prefill kernels take ratios
  * dividing 128; sequences they cannot take run in the decode kernel).
  *
@@ -608,7 +608,8 @@ ua_status ua_plan_set_scores(ua_plan* plan, float softcap, const float* alibi_sl
  *   (another one is refused there).
  * ua_forward reads scales of the blocks whose keys it reads: normal positive
  *   numbers, any from UA_MIN_BLOCK_SCALE to UA_MAX_BLOCK_SCALE (else the rows
- *   that see the block are undefined). Decode tiles apply them in binary32.
+ *   that see the block are undefined). Decode tiles apply them in binary32 (a
+ *   unified max then stands against the score plus ln of the value's scale).
  *   Prefill tiles read a staged copy code * scale rounded to bf16, exact for
  *   powers of two; they have no fp8 products.
  * ua_append_kv, ua_rope_append_kv and ua_rope_append_kv_axes set the scales of

@@ -364,7 +364,9 @@ __device__ __forceinline__ void compute_step(WarpState<D>& st, StepRegs<D, FP8>&
 // Steps a warp takes at a time over a cache with block scales. The e4m3 path
 // waits for its own chain (shared memory, conversions, products, row maximum,
 // exponentials, products) more than for memory; two steps in one chain share the
-// maximum and the rescale and leave twice as many independent instructions.
+// maximum and the rescale and leave twice as many independent instructions (8 x
+// 131072 keys, 64 and 8 heads of 128: one step 399 us, two 394, and 367 with the
+// page layout below; 64 x 512 to 8192 keys 130, 126 and 108.5).
 template <bool SCALED>
 constexpr int kStepsAtOnce = SCALED ? 2 : 1;
 
@@ -374,8 +376,8 @@ constexpr int kStepsAtOnce = SCALED ? 2 : 1;
 // lane groups g and all four t. Those read K rows that differ in bit 2, at chunks
 // t and 4 + t, and V rows 0, 2, 4, 6 (or 5, 7, 1, 3) at two neighbouring chunks:
 // eight different ones either way, so that no read has bank conflicts (with plain
-// rows and keys 4t .. 4t + 3 to a lane a step's reads take three times as many
-// wavefronts).
+// rows and keys 4t .. 4t + 3 to a lane a step's reads take 96 wavefronts at head_dim
+// 128, so 32).
 __device__ __forceinline__ int scaled_key_of_row(int m) { return m ^ ((m & 1) << 2); }
 
 template <int D>
