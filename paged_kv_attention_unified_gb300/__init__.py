@@ -664,12 +664,12 @@ class Plan:
                        num_blocks, positions=None, k_scale=1.0, v_scale=1.0, stream=None):
         if q.shape[0] < self.num_tokens:  # (len(q) takes four times as long)
             raise ValueError(f"q: {q.shape[0]} tokens, the plan has {self.num_tokens}")
-        axes = None
+        turn, axes = rope, None  # (rope keeps a caller's temporary alive through the call)
         if isinstance(rope, Rope):
-            rope, axes = rope.handle, rope.num_axes
+            turn, axes = rope.handle, rope.num_axes
         handle = _rope_append(self.handle, (self.num_tokens, self.num_q_heads, self.num_kv_heads,
                                             self.head_dim),
-                              rope, axes, q, k_new, v_new, q_out, k_cache, v_cache, block_tables,
+                              turn, axes, q, k_new, v_new, q_out, k_cache, v_cache, block_tables,
                               num_blocks, positions, k_scale, v_scale, stream)
         if self._scales and handle not in self._scales_streams:
             self._scales_used(stream, handle)
