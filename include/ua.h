@@ -608,10 +608,13 @@ ua_status ua_plan_set_scores(ua_plan* plan, float softcap, const float* alibi_sl
  *   (another one is refused there).
  * ua_forward reads scales of the blocks whose keys it reads: normal positive
  *   numbers, any from UA_MIN_BLOCK_SCALE to UA_MAX_BLOCK_SCALE (else the rows
- *   that see the block are undefined). Decode tiles apply them in binary32 (a
- *   unified max then stands against the score plus ln of the value's scale).
+ *   that see the block are undefined). Decode tiles apply them in binary32: a
+ *   row's weights are rounded to f16 (2^-11 of a weight, or 2^-25 of the row's
+ *   largest) as they are without scales, whatever scales its blocks have.
  *   Prefill tiles read a staged copy code * scale rounded to bf16, exact for
- *   powers of two; they have no fp8 products.
+ *   powers of two, and sum weights of at most 2^8 times its values in binary32
+ *   (values near 448 UA_MAX_BLOCK_SCALE overflow there when thousands of keys
+ *   share a row's weight); they have no fp8 products.
  * ua_append_kv, ua_rope_append_kv and ua_rope_append_kv_axes set the scales of
  *   the blocks they write to. With A the largest finite magnitude among the
  *   step's new elements of a block and head (keys after their rotation, in

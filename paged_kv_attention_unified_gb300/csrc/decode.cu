@@ -32,11 +32,11 @@
 // counters given, the last piece of a group to finish merges the group in the
 // same launch (otherwise the combine kernel does).
 // Over an e4m3 cache with block scales every step lies in one page, so the key
-// scale multiplies the step's scores, and the value scale vs goes into the
-// exponent: with x' = x + log2 vs the weights 2^(x' - m) of the stored codes are
-// what O accumulates, and l accumulates 2^(x' - m) / vs in binary32. One
-// exponential a score as before, and the f16 weights keep the range that they have
-// without scales, whatever the scales of a row's pages.
+// scale multiplies the step's scores, and the value scale vs the weights of its
+// codes: l sums the weights as they are, O is held in a unit of the warp's
+// (ValueUnit) and takes weights times vs / unit where f16 has room for those, and
+// the product of a step times vs / unit in binary32 where it has not. Weights have
+// the range that they have without scales, whatever the scales of a row's pages.
 #include <type_traits>
 
 #include "score_shape.cuh"
@@ -232,11 +232,34 @@ struct StepScale {
   float k, v;
 };
 
-__device__ __forceinline__ float lg2(float x) {
-  float y;
-  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
+// The unit of a warp's O accumulators over a cache with block scales, a power of
+// two: a step's values count v / unit of a code's. While that lies in [1, 2^7] it
+// goes into the weights before they are rounded to f16 (which are at most 2^8, so
+// nothing overflows, and no weight is smaller than without scales). The unit
+// follows the pages in steps of exact products. It stays within [2^-60, 2^22] and
+// at 2^-64 of the largest scale so far or above: then O, at most 2^8 a key times 448
+// of those, stays below 2^128 for 2^31 keys, and what the quietest page (2^-100)
+// adds beside the loudest (2^100) is a number of binary32.
+struct ValueUnit {
+  float inv = 0.f, top = 0.f;  // 1 / unit (0: nothing taken yet); the largest scale so far
+  __device__ __forceinline__ static float power(float x) {  // 2^floor(log2 x)
+    return __uint_as_float(__float_as_uint(x) & 0x7f800000u);
+  }
+  __device__ __forceinline__ static float inverse(float x) {  // of a power of two
+    return __uint_as_float((254u << 23) - __float_as_uint(x));
+  }
+  __device__ __forceinline__ bool near(float least, float most) const {
+    return least * inv >= 1.f && most * inv <= 128.f;
+  }
+  // A unit for pages with scales from least to most; returns old / new.
+  __device__ __forceinline__ float follow(float least, float most) {
+    top = fmaxf(top, most);
+    const float unit = fminf(fmaxf(fmaxf(power(least) * 0.125f, power(top) * 0x1p-64f), 0x1p-60f), 0x1p22f);
+    const float factor = inv > 0.f ? unit * inv : 1.f;  // new / old
+    inv = inverse(unit);
+    return inverse(factor);
+  }
+};
 
 template <int D, bool FP8, bool SHAPED>
 __device__ __forceinline__ void compute_step(WarpState<D>& st, StepRegs<D, FP8>& r,
@@ -440,7 +463,7 @@ __device__ __forceinline__ void compute_two_scaled(WarpState<D>& st, const uint8
                                                    const uint8_t* const (&vp)[2], int kv_hi,
                                                    const uint32_t (&qb)[D / 16][2],
                                                    const float (&cq)[2], const StepMask& mk,
-                                                   const StepScale (&scale)[2],
+                                                   const StepScale (&scale)[2], ValueUnit& unit,
                                                    const int (&base)[2], const ScaledPage<D>& page,
                                                    int g, const Release& release) {
   using C = DecodeCfg<D, true>;
@@ -468,23 +491,18 @@ __device__ __forceinline__ void compute_two_scaled(WarpState<D>& st, const uint8
     }
   }
   read_v();
-  float x[2][4], v_inv[2];
+  float x[2][4];
 #pragma unroll
   for (int n = 0; n < 2; ++n) {
     const float cc[2] = {cq[0] * scale[n].k, cq[1] * scale[n].k};
-    const float v_log2 = lg2(scale[n].v);
-    v_inv[n] = rcp_approx(scale[n].v);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int key = base[n] + page.k_key + 8 * (e >> 1);
+      x[n][e] = s[n][e] * cc[e & 1];
       if constexpr (SHAPED) {
-        x[n][e] = s[n][e] * cc[e & 1];
         if (mk.cap_log2 > 0.f) x[n][e] = cap_score(x[n][e] * mk.cap_arg, mk.cap_log2);
         const RowBias& b = mk.bias[e & 1];
         x[n][e] = fmaf(-b.slope2, static_cast<float>(abs(mk.pos[e & 1] - key) - b.shift), x[n][e]);
-        x[n][e] += v_log2;
-      } else {
-        x[n][e] = fmaf(s[n][e], cc[e & 1], v_log2);
       }
     }
     if (base[n] < mk.lo_full || base[n] + 16 > mk.hi_full) {
@@ -525,9 +543,18 @@ __device__ __forceinline__ void compute_two_scaled(WarpState<D>& st, const uint8
     for (int n = 0; n < 2; ++n) {
       p[n][j] = ex2(x[n][j] - sub);
       p[n][j + 2] = ex2(x[n][j + 2] - sub);
-      st.l[j] = fmaf(p[n][j] + p[n][j + 2], v_inv[n], st.l[j]);
+      st.l[j] += p[n][j] + p[n][j + 2];
     }
     st.m[j] = m_use;
+  }
+  // (the scales are the same for the whole warp)
+  const float least = fminf(scale[0].v, scale[1].v), most = fmaxf(scale[0].v, scale[1].v);
+  bool near = unit.near(least, most);
+  if (!near) {
+    const float shrink = unit.follow(least, most);
+    alpha[0] *= shrink;
+    alpha[1] *= shrink;
+    near = unit.near(least, most);
   }
   if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
 #pragma unroll
@@ -538,19 +565,42 @@ __device__ __forceinline__ void compute_two_scaled(WarpState<D>& st, const uint8
       st.acc[c][3] *= alpha[1];
     }
   }
+  // A step's V codes of chunk c as an f16 operand.
+  auto v_operand = [&](int n, int c, uint32_t (&a)[4]) {
+    const uint32_t sel = (c & 1) ? 0x7362u : 0x5140u;
+    const uint32_t lo = __byte_perm(r[n].v[0][c >> 1], r[n].v[1][c >> 1], sel);
+    const uint32_t hi = __byte_perm(r[n].v[2][c >> 1], r[n].v[3][c >> 1], sel);
+    e4m3x4_to_f16x2x2(lo, a[0], a[1]);
+    e4m3x4_to_f16x2x2(hi, a[2], a[3]);
+  };
+  if (near) {
 #pragma unroll
-  for (int n = 0; n < 2; ++n) {
-    const uint32_t pb0 = movmatrix_trans(pack2<true>(p[n][0], p[n][1]));
-    const uint32_t pb1 = movmatrix_trans(pack2<true>(p[n][2], p[n][3]));
+    for (int n = 0; n < 2; ++n) {
+      const float f = scale[n].v * unit.inv;
+      const uint32_t pb0 = movmatrix_trans(pack2<true>(p[n][0] * f, p[n][1] * f));
+      const uint32_t pb1 = movmatrix_trans(pack2<true>(p[n][2] * f, p[n][3] * f));
 #pragma unroll
-    for (int c = 0; c < C::NC; ++c) {
-      uint32_t a[4];
-      const uint32_t sel = (c & 1) ? 0x7362u : 0x5140u;
-      const uint32_t lo = __byte_perm(r[n].v[0][c >> 1], r[n].v[1][c >> 1], sel);
-      const uint32_t hi = __byte_perm(r[n].v[2][c >> 1], r[n].v[3][c >> 1], sel);
-      e4m3x4_to_f16x2x2(lo, a[0], a[1]);
-      e4m3x4_to_f16x2x2(hi, a[2], a[3]);
-      mma16816<true>(st.acc[c], a, pb0, pb1);
+      for (int c = 0; c < C::NC; ++c) {
+        uint32_t a[4];
+        v_operand(n, c, a);
+        mma16816<true>(st.acc[c], a, pb0, pb1);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      const float f = scale[n].v * unit.inv;
+      const uint32_t pb0 = movmatrix_trans(pack2<true>(p[n][0], p[n][1]));
+      const uint32_t pb1 = movmatrix_trans(pack2<true>(p[n][2], p[n][3]));
+#pragma unroll
+      for (int c = 0; c < C::NC; ++c) {
+        uint32_t a[4];
+        v_operand(n, c, a);
+        float o[4] = {0.f, 0.f, 0.f, 0.f};
+        mma16816<true>(o, a, pb0, pb1);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) st.acc[c][e] = fmaf(o[e], f, st.acc[c][e]);
+      }
     }
   }
   if constexpr (!kLateV<D>) release();
@@ -574,7 +624,7 @@ struct Ring {
   static constexpr int kAlloc = kBytes + 1024;  // slack for 1024-byte alignment (swizzle atoms)
   static constexpr int kCtasPerSm = decode_ctas_per_sm(D, kElt);
   static_assert(kAlloc == decode_smem_bytes(D, kElt), "decode shared memory");
-  static_assert(kWarps * UA_DECODE_ROWS * (D + 2) * 4 <= kRing, "merge buffers alias the ring");
+  static_assert(kWarps * (UA_DECODE_ROWS * (D + 2) + 1) * 4 <= kRing, "merge buffers alias the ring");
 };
 
 template <int D, bool FP8, bool SCALED>
@@ -597,6 +647,7 @@ __global__ void __launch_bounds__(kThreads, Ring<D, FP8>::kCtasPerSm)
   float (*red_m)[UA_DECODE_ROWS] =
       reinterpret_cast<float (*)[UA_DECODE_ROWS]>(dsm + kWarps * UA_DECODE_ROWS * D * 4);
   float (*red_l)[UA_DECODE_ROWS] = red_m + kWarps;
+  [[maybe_unused]] float* const red_unit = red_l[kWarps];  // (SCALED: 1 / the warp's unit of O)
 
   const ua_tile tile = p.tiles[blockIdx.x];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -806,6 +857,7 @@ __global__ void __launch_bounds__(kThreads, Ring<D, FP8>::kCtasPerSm)
       }
     }
   };
+  [[maybe_unused]] ValueUnit unit;
   int issued = 0, done = 0;
   if (my_n > 0) {
     refill_ids(0);
@@ -839,8 +891,8 @@ __global__ void __launch_bounds__(kThreads, Ring<D, FP8>::kCtasPerSm)
             ++issued;
           }
         };
-        compute_two_scaled<D, SHAPED>(st_state, kp, vp, kv_hi, qb, cc, mk, scale, base, page, g,
-                                      refill);
+        compute_two_scaled<D, SHAPED>(st_state, kp, vp, kv_hi, qb, cc, mk, scale, unit, base, page,
+                                      g, refill);
       }
     }
     StepRegs<D, FP8> r;
@@ -886,6 +938,9 @@ __global__ void __launch_bounds__(kThreads, Ring<D, FP8>::kCtasPerSm)
       red_l[warp][2 * t + j] = st_state.l[j];
     }
   }
+  if constexpr (SCALED) {
+    if (lane == 0) red_unit[warp] = unit.inv;
+  }
 #pragma unroll
   for (int c = 0; c < C::NC; ++c) {
     const int d0 = v_dim<D, FP8>(2 * c, g);
@@ -901,17 +956,26 @@ __global__ void __launch_bounds__(kThreads, Ring<D, FP8>::kCtasPerSm)
   const int d0 = (threadIdx.x % 16) * kSeg;
   const bool row_ok = n < nrows;
   float M = -INFINITY, L = 0.f;
+  [[maybe_unused]] float inv_unit = INFINITY;  // SCALED: of the merged O, the largest of the warps'
   float o[kSeg];
 #pragma unroll
   for (int e = 0; e < kSeg; ++e) o[e] = 0.f;
   if (row_ok) {
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) M = fmaxf(M, red_m[w][n]);
+    if constexpr (SCALED) {
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w)
+        if (red_unit[w] > 0.f) inv_unit = fminf(inv_unit, red_unit[w]);
+    }
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       const float mw = red_m[w][n];
-      const float f = (mw == -INFINITY) ? 0.f : ex2(mw - M);
+      float f = (mw == -INFINITY) ? 0.f : ex2(mw - M);
       L += f * red_l[w][n];
+      if constexpr (SCALED) {
+        if (red_unit[w] > 0.f) f *= inv_unit * ValueUnit::inverse(red_unit[w]);
+      }
 #pragma unroll
       for (int e = 0; e < kSeg; ++e) o[e] += f * red_acc[w][n][d0 + e];
     }
@@ -941,7 +1005,9 @@ __global__ void __launch_bounds__(kThreads, Ring<D, FP8>::kCtasPerSm)
       for (int i = 0; i < kSeg / 2; ++i) *reinterpret_cast<uint32_t*>(dst + 4 * i) = packed[i];
     }
   };
-  const float inv = L > 0.f ? p.v_scale / L : 0.f;
+  const float inv = !(L > 0.f) ? 0.f
+                    : SCALED   ? ValueUnit::inverse(inv_unit) / L
+                               : p.v_scale / L;
   if (tile.slot < 0) {
     if (row_ok) store_out(o, inv);
     stamp_end();
