@@ -820,7 +820,7 @@ __global__ void __launch_bounds__(kThreads, Ring<D, FP8>::kCtasPerSm)
       of_issue = StepScale{1.f, 1.f};
       if (ids >= 0 && static_cast<int64_t>(ids) < p.num_blocks) {
         const int64_t at = static_cast<int64_t>(ids) * p.num_kv_heads + tile.kv_head;
-        of_issue = StepScale{__ldg(p.k_scales + at), __ldg(p.v_scales + at)};
+        of_issue = StepScale{usable_scale(__ldg(p.k_scales + at)), usable_scale(__ldg(p.v_scales + at))};
       }
     }
   };

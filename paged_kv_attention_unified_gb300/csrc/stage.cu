@@ -112,8 +112,8 @@ __global__ void __launch_bounds__(kStageWarps * 32) stage_kernel(const StagePara
         float k_scale = 1.f, v_scale = 1.f;
         if constexpr (SCALED) {
           const int64_t at = static_cast<int64_t>(blk) * p.num_kv_heads + c / p.head_chunks;
-          k_scale = __ldg(p.k_scales + at);
-          v_scale = __ldg(p.v_scales + at);
+          k_scale = usable_scale(__ldg(p.k_scales + at));
+          v_scale = usable_scale(__ldg(p.v_scales + at));
         }
         uint4 lo, hi;
         widen16<SCALED>(kc[u], k_scale, lo, hi);

@@ -87,6 +87,13 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// A block scale as the attention kernels take it: one outside the limits, NaN too,
+// as the nearest limit. What lies in such a block is then a number: beside weights
+// of 0, in the rows of a tile that do not see it, a NaN or infinity would spoil them.
+__device__ __forceinline__ float usable_scale(float s) {
+  return fminf(fmaxf(s, UA_MIN_BLOCK_SCALE), UA_MAX_BLOCK_SCALE);  // (fmaxf passes over NaN)
+}
+
 // Streaming 16-byte / 8-byte loads of cache data: read-only, not kept in L1.
 __device__ __forceinline__ uint4 ld_stream_v4(const void* p) {
   uint4 r;

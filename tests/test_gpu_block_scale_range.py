@@ -55,7 +55,12 @@ def _forward(case, ks, vs, phi=None, **plan_args):
 
 def _check(case, ks, vs, skip=(), phi=None, sinks=0, **plan_args):
     got, staged = _forward(case, ks, vs, phi, sink_tokens=sinks, **plan_args)
-    exp, _, rows = _rows(case, ks, vs, staged, sinks=sinks)
+    _compare(case, got, staged, ks, vs, skip, sinks=sinks)
+
+
+def _compare(case, got, staged, ks, vs, skip=(), **shape):
+    """skip: tokens whose rows hold anything."""
+    exp, _, rows = _rows(case, ks, vs, staged, **shape)
     eps, low = (2.0 ** -8 + 2.0 ** -11, 0.0) if staged else (2.0 ** -10, 2.0 ** -25)
     for (tok, h), (t, p, v) in rows.items():
         if tok in skip:
@@ -146,3 +151,22 @@ def test_scales_that_rise_and_fall_from_page_to_page(ratio):
         for i, page in enumerate(case.block_tables[s].tolist()):
             vs[page] = 2.0 ** -6 * ratio ** (i % 3)
     _check(case, ks, vs)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf"), 0.0, -1.0, 1e-40])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_a_block_without_a_usable_scale_spoils_only_the_rows_that_see_it(d, bad):
+    """It lies in the tiles of rows that do not: behind their positions, or before their window."""
+    for ql, kv, window, page, skip, rows in (
+            (3, 33, 0, 2, (2,), 10 ** 6), (2, 49, 17, 1, (0,), 10 ** 6), (16, 700, 0, 43, range(4, 16), 10 ** 6),
+            (200, 257, 0, 16, (199,), 0), (150, 256, 91, 0, (), 0), (150, 256, 92, 0, (0,), 0),
+            (150, 256, 92, 0, (0,), 10 ** 6)):
+        case = _case("bad", [ql], [kv], d, seed=d + kv, window=window)
+        ks, vs = _scales(case)
+        block = int(case.block_tables[0, page])
+        for which in ((0,), (1,), (0, 1)):
+            x = [ks.clone(), vs.clone()]
+            for i in which:
+                x[i][block] = bad
+            got, staged = _forward(case, *x, decode_rows_max=rows)
+            _compare(case, got, staged, ks, vs, skip)
