@@ -1334,7 +1334,8 @@ ua_status ua_rope_append_kv_axes(const ua_plan* plan, const ua_rope* rope, const
                         static_cast<const void*>(k_cache), static_cast<const void*>(v_cache)})
     if (!aligned16(x)) return UA_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(positions) & 3u) != 0) return UA_ERR_INVALID_ARG;
-  if (positions != nullptr && positions_stride < plan->total_q) return UA_ERR_INVALID_ARG;
+  if (positions != nullptr && rope->axes > 1 && positions_stride < plan->total_q)
+    return UA_ERR_INVALID_ARG;
   const int64_t q_row = static_cast<int64_t>(pr.num_q_heads) * pr.head_dim;
   const int64_t kv_row = static_cast<int64_t>(pr.num_kv_heads) * pr.head_dim;
   if (q_stride < q_row || k_stride < kv_row || v_stride < kv_row || q_stride % 8 != 0 ||

@@ -164,3 +164,25 @@ def test_refusals():
         assert lib.ua_rope_append_kv_axes(*args(0, None)) == ua.UA_OK
         torch.cuda.synchronize()
         assert plan.last_device_error() == 0
+
+
+@pytest.mark.parametrize("axes", [None, [0] * 32])
+def test_one_axis_has_no_row_distance(axes):
+    """The distance of the rows of positions plays no part where there is one row."""
+    s = Step([3, 20], [20, 20], 4, 2, 64, 16, seed=8)
+    w = R.frequencies(64, 10000.0)[0]
+    pos = torch.from_numpy(_places(23, 1, 9)).to(torch.int32).cuda()
+    with tu.make_plan(s.b) as plan, ua.Rope(w, axes=axes) as rope:
+        want = s.run(plan, rope, pos[0])
+        cache = s.b.k_cache.clone()
+        lib, b, p = ua.lib(), s.b, lambda t: t.data_ptr()  # noqa: E731
+        for stride in (0, -1, 22, 2 ** 62, -2 ** 63):
+            s.b.k_cache.zero_()
+            out = torch.zeros_like(want)
+            assert lib.ua_rope_append_kv_axes(
+                plan.handle, rope.handle, p(s.q), s.q.stride(0), p(s.k), s.k.stride(0), p(s.v), s.v.stride(0), p(out),
+                p(b.k_cache), p(b.v_cache), p(b.block_tables), b.num_blocks, p(pos), stride, 1.0, 1.0,
+                torch.cuda.current_stream().cuda_stream) == ua.UA_OK
+            rows = s.case.block_tables.numpy()[s.seq, s.slot_pos // 16], s.slot_pos % 16
+            assert torch.equal(out, want) and torch.equal(b.k_cache[rows], cache[rows])
+        assert plan.last_device_error() == 0
