@@ -676,9 +676,10 @@ const char* ua_status_string(int32_t status);
  * tile of the plan, in order, copies the raw K and V rows of its key range
  * [kv_lo, kv_hi) (clamped by kv_lens[seq]) for its KV head into k_out/v_out,
  * packed tile after tile, rows of head_dim elements of the cache's element
- * size. The row offset of tile n is the sum of the clamped range lengths of
- * tiles 0..n-1. Page ids are resolved exactly as in ua_forward. The outputs
- * must hold `rows_cap` rows.
+ * size. With sinks, the steps of 16 keys that the tile passes over (behind the
+ * sinks, and in nobody's window from its first row on) are left out here too.
+ * The row offset of tile n is the number of rows of tiles 0..n-1. Page ids are
+ * resolved exactly as in ua_forward. The outputs must hold `rows_cap` rows.
  */
 ua_status ua_gather_kv_debug(const ua_plan* plan, const void* k_cache, const void* v_cache,
                              const int32_t* kv_lens, const int32_t* block_tables,

@@ -11,6 +11,7 @@
 // One CTA per combine group (one decode tile cut into pieces): warp n owns
 // packed row n, every lane a contiguous run of head_dim/32 dimensions, so the
 // partial rows are read with coalesced 16-, 8- or 4-byte loads.
+#include "planner.h"
 #include "ua_device.cuh"
 #include "ua_kernels.h"
 
@@ -95,20 +96,24 @@ __global__ void __launch_bounds__(32 * UA_DECODE_ROWS) combine_kernel(const Comb
   }
 }
 
-// One CTA per decode tile: copy the raw K and V rows of its key range.
+// One CTA per decode tile: copy the raw K and V rows of its key range, but for
+// those of its gap (empty, or inside the range).
 __global__ void gather_debug_kernel(const KernelParams p, const int64_t* row_offsets,
-                                    int row_bytes, uint8_t* k_out, uint8_t* v_out) {
+                                    const KeyGap* gaps, int row_bytes, uint8_t* k_out,
+                                    uint8_t* v_out) {
   const ua_tile tile = p.tiles[blockIdx.x];
   const int kv_len = p.kv_lens[tile.seq];
   const int hi = min(min(tile.kv_hi, kv_len), p.max_blocks_per_seq * p.block_size);
-  const int n = max(hi - tile.kv_lo, 0);
+  const KeyGap gap = gaps[blockIdx.x];
+  const int n = max(hi - tile.kv_lo - (gap.hi - gap.lo), 0);
   const int chunks = row_bytes / 16;
   const int head_dim_elems = row_bytes;  // offsets below are in bytes
   for (int idx = threadIdx.x; idx < n * chunks; idx += blockDim.x) {
-    const int key = tile.kv_lo + idx / chunks;
-    const int ch = idx % chunks;
+    const int row = idx / chunks, ch = idx % chunks;
+    const int at = tile.kv_lo + row;
+    const int key = at < gap.lo ? at : at + (gap.hi - gap.lo);
     const int64_t page = page_of(p, tile.seq, key);
-    const int64_t dst = (row_offsets[blockIdx.x] + (key - tile.kv_lo)) * row_bytes + ch * 16;
+    const int64_t dst = (row_offsets[blockIdx.x] + row) * row_bytes + ch * 16;
     uint4 kx = make_uint4(0u, 0u, 0u, 0u), vx = kx;
     if (page >= 0) {
       const int64_t src =
@@ -140,10 +145,11 @@ cudaError_t launch_combine(const CombineParams& c, int head_dim, cudaStream_t st
   return cudaGetLastError();
 }
 
-cudaError_t launch_gather_debug(const KernelParams& p, const int64_t* row_offsets, int head_dim,
-                                int elt_bytes, void* k_out, void* v_out, cudaStream_t stream) {
+cudaError_t launch_gather_debug(const KernelParams& p, const int64_t* row_offsets,
+                                const KeyGap* gaps, int head_dim, int elt_bytes, void* k_out,
+                                void* v_out, cudaStream_t stream) {
   if (p.num_tiles <= 0) return cudaSuccess;
-  gather_debug_kernel<<<p.num_tiles, 256, 0, stream>>>(p, row_offsets, head_dim * elt_bytes,
+  gather_debug_kernel<<<p.num_tiles, 256, 0, stream>>>(p, row_offsets, gaps, head_dim * elt_bytes,
                                                        static_cast<uint8_t*>(k_out),
                                                        static_cast<uint8_t*>(v_out));
   return cudaGetLastError();

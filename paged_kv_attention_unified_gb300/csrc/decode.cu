@@ -786,8 +786,9 @@ __global__ void __launch_bounds__(kThreads, Ring<D, FP8>::kCtasPerSm)
   int nsteps = kv_hi > kv_lo ? (kv_hi - kv_lo + 15) / 16 : 0;
   int gap_lo = INT_MAX, gap = 0;  // a range that spans the keys behind the sinks passes over them
   if constexpr (SHAPED) {
-    const KeyGap no_row = key_gap(p.shape.sinks, p.window, ctx + tile.row0 / p.qpk, kKeyStep);
-    if (no_row.hi > no_row.lo && kv_lo < no_row.lo && kv_hi > no_row.hi) {
+    const KeyGap no_row = gap_within(
+        key_gap(p.shape.sinks, p.window, ctx + tile.row0 / p.qpk, kKeyStep), kv_lo, kv_hi);
+    if (no_row.hi > no_row.lo) {
       gap_lo = no_row.lo;
       gap = no_row.hi - no_row.lo;
       nsteps -= gap / 16;

@@ -85,6 +85,11 @@ constexpr KeyGap key_gap(int32_t sinks, int32_t window, int32_t min_pos, int32_t
   const int32_t lo = (sinks + step - 1) / step * step, hi = (min_pos - window + 1) / step * step;
   return hi > lo ? KeyGap{lo, hi} : KeyGap{0, 0};
 }
+// The gap if it lies within a decode tile's range [lo, hi); a split piece without it
+// has an empty one.
+constexpr KeyGap gap_within(KeyGap gap, int32_t lo, int32_t hi) {
+  return gap.hi > gap.lo && lo < gap.lo && hi > gap.hi ? gap : KeyGap{0, 0};
+}
 
 // Granularity of key ranges: one decode step reads 16 tokens, so split pieces
 // and decode ranges start on multiples of 16.

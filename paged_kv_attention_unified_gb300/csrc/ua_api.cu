@@ -1562,27 +1562,40 @@ ua_status ua_gather_kv_debug(const ua_plan* plan, const void* k_cache, const voi
     return UA_ERR_INVALID_ARG;
   plan = serving(plan);
   const ua::Schedule& s = plan->sched;
-  // Row offsets from the host ranges; the kernel clamps by the device kv_lens,
-  // which the caller guarantees equal the plan's.
+  // Row offsets from the host ranges, without the keys between the sinks and the
+  // window that the decode kernel passes over; the kernel clamps by the device
+  // kv_lens, which the caller guarantees equal the plan's.
+  const ua::Problem& pr = plan->prob;
+  std::vector<int32_t> ctx(static_cast<size_t>(pr.num_seqs), 0);  // of sequences with new tokens
+  for (auto t = s.append.rbegin(); t != s.append.rend(); ++t) ctx[t->seq] = t->kv_lo;
   std::vector<int64_t> offs(s.decode.size() + 1, 0);
-  for (size_t i = 0; i < s.decode.size(); ++i)
-    offs[i + 1] = offs[i] + (s.decode[i].kv_hi - s.decode[i].kv_lo);
+  std::vector<ua::KeyGap> gaps(s.decode.size());
+  for (size_t i = 0; i < s.decode.size(); ++i) {
+    const ua_tile& t = s.decode[i];
+    const int32_t min_pos = ctx[t.seq] + t.row0 / (pr.num_q_heads / pr.num_kv_heads);
+    gaps[i] = ua::gap_within(ua::key_gap(pr.sinks, pr.window, min_pos, ua::kKeyStep), t.kv_lo, t.kv_hi);
+    offs[i + 1] = offs[i] + (t.kv_hi - t.kv_lo) - (gaps[i].hi - gaps[i].lo);
+  }
   if (offs.back() > rows_cap) return UA_ERR_INVALID_ARG;
   if (s.decode.empty()) return UA_OK;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   const ua_status uploaded = after_upload(plan, cs);
   if (uploaded != UA_OK) return uploaded;
   int64_t* d_offs = nullptr;
-  if (cudaMalloc(&d_offs, offs.size() * sizeof(int64_t)) != cudaSuccess) return UA_ERR_CUDA;
-  ua_status st = from_cuda(cudaMemcpyAsync(d_offs, offs.data(), offs.size() * sizeof(int64_t),
-                                           cudaMemcpyHostToDevice, cs));
+  const size_t off_bytes = offs.size() * sizeof(int64_t), gap_bytes = gaps.size() * sizeof(ua::KeyGap);
+  if (cudaMalloc(&d_offs, off_bytes + gap_bytes) != cudaSuccess) return UA_ERR_CUDA;
+  ua::KeyGap* const d_gaps = reinterpret_cast<ua::KeyGap*>(d_offs + offs.size());
+  ua_status st = from_cuda(cudaMemcpyAsync(d_offs, offs.data(), off_bytes, cudaMemcpyHostToDevice, cs));
+  if (st == UA_OK)
+    st = from_cuda(cudaMemcpyAsync(d_gaps, gaps.data(), gap_bytes, cudaMemcpyHostToDevice, cs));
   if (st == UA_OK) {
     ua::KernelParams kp = base_params(plan, nullptr, k_cache, v_cache, nullptr, nullptr, kv_lens,
                                       block_tables, num_blocks, 1.f, 1.f, 1.f);
     kp.tiles = plan->d_decode;
     kp.num_tiles = static_cast<int32_t>(s.decode.size());
     const int elt = plan->prob.kv_dtype == UA_KV_FP8_E4M3 ? 1 : 2;
-    st = from_cuda(ua::launch_gather_debug(kp, d_offs, plan->prob.head_dim, elt, k_out, v_out, cs));
+    st = from_cuda(
+        ua::launch_gather_debug(kp, d_offs, d_gaps, plan->prob.head_dim, elt, k_out, v_out, cs));
   }
   if (cudaStreamSynchronize(cs) != cudaSuccess && st == UA_OK) st = UA_ERR_CUDA;
   cudaFree(d_offs);

@@ -240,7 +240,9 @@ struct StageParams {
 cudaError_t launch_stage(const StageParams& p, int sms, cudaStream_t stream);
 
 // Test aid: copy the raw K/V rows each tile reads into dense buffers.
-cudaError_t launch_gather_debug(const KernelParams& p, const int64_t* row_offsets, int head_dim,
-                                int elt_bytes, void* k_out, void* v_out, cudaStream_t stream);
+struct KeyGap;
+cudaError_t launch_gather_debug(const KernelParams& p, const int64_t* row_offsets,
+                                const KeyGap* gaps, int head_dim, int elt_bytes, void* k_out,
+                                void* v_out, cudaStream_t stream);
 
 }  // namespace ua

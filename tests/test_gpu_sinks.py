@@ -234,3 +234,40 @@ def test_refusals():
     b.causal = 0
     with pytest.raises(ValueError):
         tu.make_plan(b, sink_tokens=4, prefix_lens=[3])
+
+
+@pytest.mark.parametrize("dtype", [W.BF16, W.FP8])
+@pytest.mark.parametrize("splits", [1, 3, 7])
+def test_gather_takes_the_keys_that_the_decode_kernel_reads(splits, dtype):
+    """Over pages given back: no row of theirs, no error, every other row bit for bit."""
+    window, sinks, elt = 100, 20, 1 if dtype == W.FP8 else 2
+    case = W.make_case("gather", [1, 3, 9, 1], [900, 640, 433, 60], 8, 2, 128, 16, kv_dtype=dtype, seed=33, window=window)
+    _give_back(case, sinks)
+    b = tu.to_device(case)
+    with _plan(b, sinks, num_splits=splits, decode_rows_max=10 ** 6) as plan:
+        _, _, dec, _ = ua.ua_schedule(b.cu_host, b.kv_host, 8, 2, 128, 16, int(b.block_tables.shape[1]),
+                                      kv_dtype=b.kv_dtype, window=window, num_splits=splits,
+                                      num_sms=plan.info.num_sms, decode_rows_max=10 ** 6, sink_tokens=sinks)
+        want = []
+        for t in dec:
+            n, kv = case.query_lens[t["seq"]], int(case.kv_lens[t["seq"]])
+            first = kv - n + t["row0"] // 4  # position of the tile's first row
+            unseen = lambda key: sinks <= key <= first - window  # noqa: E731
+            for key in range(t["kv_lo"], t["kv_hi"]):
+                step = key // 16 * 16
+                if not (unseen(step) and unseen(step + 15)):
+                    want.append((int(case.block_tables[t["seq"], key // 16]), key % 16, t["kv_head"]))
+        ranges = sum(t["kv_hi"] - t["kv_lo"] for t in dec)
+        assert splits == 7 or len(want) < ranges  # (seven pieces end and start at the gap)
+        assert min(page for page, _, _ in want) >= 0
+        ko, vo = (torch.zeros((len(want) + 1, 128 * elt), dtype=torch.uint8, device="cuda") for _ in range(2))
+        ua.ua_gather_kv_debug(plan.handle, b.k_cache, b.v_cache, b.kv_lens, b.block_tables, b.num_blocks, ko, vo,
+                              len(want))
+        assert plan.last_device_error() == 0
+        with pytest.raises(ua.UAError):
+            ua.ua_gather_kv_debug(plan.handle, b.k_cache, b.v_cache, b.kv_lens, b.block_tables, b.num_blocks, ko, vo,
+                                  len(want) - 1)
+    page, slot, head = (torch.tensor(x) for x in zip(*want))
+    for got, cache in ((ko, case.k_cache), (vo, case.v_cache)):
+        raw = cache.contiguous().view(torch.uint8).reshape(case.num_blocks, 16, 2, 128 * elt)
+        assert torch.equal(got.cpu()[:-1], raw[page, slot, head]) and not got[-1].any()
