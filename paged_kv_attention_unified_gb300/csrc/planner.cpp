@@ -37,6 +37,7 @@ void key_range(const Problem& p, int32_t seq, int32_t ctx, int32_t kv_len, int32
 
 // The gap of the packed rows from row0 on of a sequence with ctx earlier keys.
 KeyGap gap_of(const Problem& p, int32_t ctx, int32_t row0, int32_t step) {
+  if (p.sinks <= 0 || p.window <= 0) return {0, 0};  // (before the division)
   return key_gap(p.sinks, p.window, ctx + row0 / (p.num_q_heads / p.num_kv_heads), step);
 }
 
@@ -270,8 +271,13 @@ ua_status build_schedule(const Problem& p, Schedule* out) {
     }
   }
 
-  // Fill tiles: each sequence's new tokens by the page they go to.
-  if (p.kv_dtype == UA_KV_FP8_E4M3) {
+  // Fill tiles: each sequence's new tokens by the page they go to. One token a
+  // sequence: the append tiles.
+  if (p.fill && s.max_q > 1) {
+    size_t n_fill = 0;
+    for (int32_t q = 0; q < p.num_seqs; ++q)
+      n_fill += static_cast<size_t>((p.cu_query_lens[q + 1] - p.cu_query_lens[q]) / p.block_size + 2);
+    s.fill.reserve(n_fill);
     for (int32_t q = 0; q < p.num_seqs; ++q) {
       const int32_t q0 = p.cu_query_lens[q];
       const int32_t ql = p.cu_query_lens[q + 1] - q0;

@@ -29,6 +29,7 @@ struct Problem {
   int32_t causal = 1;
   int32_t window = 0;
   int32_t sinks = 0;            // first keys that stay visible under the window
+  bool fill = false;            // make the tiles of an append with block scales
   int32_t num_splits = 0;       // 0: automatic
   int32_t num_sms = 152;
   int32_t decode_rows_max = -1; // < 0: default
@@ -62,8 +63,9 @@ struct Schedule {
   // sequence: seq, row0 = first token (row of k_new), nrows = tokens,
   // kv_lo = logical cache position of the first token, kv_hi = kv_lo + nrows.
   std::vector<ua_tile> append;
-  // fp8 caches, append with block scales: the new tokens of one page, fields as
-  // the append tiles'; the most tokens of one.
+  // fp8 caches, append with block scales (Problem::fill): the new tokens of one page,
+  // fields as the append tiles'; the most tokens of one. Empty where no sequence has
+  // more than one new token: the append tiles are the same.
   std::vector<ua_tile> fill;
   int32_t fill_rows = 0;
   std::vector<ua_combine_group> groups;

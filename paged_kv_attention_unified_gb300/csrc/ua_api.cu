@@ -467,6 +467,8 @@ ua_status create_plan(ua_plan** out, const int32_t* cu_query_lens_host,
                             num_kv_heads, head_dim, block_size, max_blocks_per_seq, kv_dtype,
                             causal, window, num_splits, sms, decode_rows_max, shaped,
                             prefix_lens_host, sinks);
+  // (the entry points that upload a batch's arrays with its plan use it for one forward)
+  plan->prob.fill = kv_dtype == UA_KV_FP8_E4M3 && extra == nullptr;
   ua_status st;
   try {
     st = ua::build_schedule(plan->prob, &plan->sched);
@@ -854,12 +856,13 @@ ua::FillParams fill_params(const ua_plan* plan, const void* k_new, const void* v
   fp.v_cache = v_cache;
   fp.k_scales = plan->k_scales;
   fp.v_scales = plan->v_scales;
-  fp.tiles = plan->d_fill;
+  const ua::Schedule& s = plan->sched;
+  fp.tiles = s.fill.empty() ? plan->d_append : plan->d_fill;
   fp.block_tables = block_tables;
   fp.err = plan->d_err;
   fp.num_blocks = num_blocks;
-  fp.num_tiles = static_cast<int32_t>(plan->sched.fill.size());
-  fp.max_rows = plan->sched.fill_rows;
+  fp.num_tiles = static_cast<int32_t>(s.fill.empty() ? s.append.size() : s.fill.size());
+  fp.max_rows = s.fill.empty() ? 1 : s.fill_rows;
   fp.num_kv_heads = plan->prob.num_kv_heads;
   fp.head_dim = plan->prob.head_dim;
   fp.max_blocks_per_seq = plan->prob.max_blocks_per_seq;

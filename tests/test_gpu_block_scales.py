@@ -632,3 +632,19 @@ def test_plan_without_tokens():
         plan.append_kv(rows[:, :2], rows[:, 2:4], b.k_cache, b.v_cache, b.block_tables, b.num_blocks)
         tu.forward(plan, b)
         assert plan.last_device_error() == 0
+
+
+@pytest.mark.parametrize("rope", [False, True])
+@pytest.mark.parametrize("d,hkv,bs", [(128, 8, 16), (64, 1, 64), (96, 2, 32), (256, 2, 16)])
+def test_a_token_a_sequence(d, hkv, bs, rope):
+    """Steps whose tiles are those of the plain append."""
+    kv = [1, 16, 17, 40, 0, 65, 129, 700]
+    s = Step([1, 1, 1, 1, 0, 1, 1, 1], kv, 2 * hkv, hkv, d, bs, seed=d + 11)
+    with s.plan() as plan, ua.Rope(R.frequencies(d, 10000.0)[0]) as r:
+        s.rope_append(plan, r) if rope else s.append(plan)
+        assert plan.last_device_error() == 0
+    if not rope:
+        return s.check(as_f64(s.k), as_f64(s.v))
+    pos = np.array([x - 1 for x in kv if x])
+    s.check(R.rotate(as_f64(s.k), pos, R.frequencies(d, 10000.0)[0], False), as_f64(s.v),
+            2.5e-6 * R.pair_size(as_f64(s.k), d, False))
