@@ -146,8 +146,9 @@ struct Geometry {
   int nmax;                  // key tiles loaded
   int nsink, skip;           // key tiles before the keys that no row sees, and how many those are
   // First key of key tile j.
+  template <bool SHAPED>
   __device__ __forceinline__ int key_of(int j) const {
-    return kv_lo + j * kKeys + (j >= nsink ? skip : 0);
+    return kv_lo + j * kKeys + (SHAPED && j >= nsink ? skip : 0);
   }
 };
 
@@ -161,6 +162,7 @@ static_assert(sizeof(Item) <= kItemBytes, "work-tile descriptor too large");
 
 // Per-sequence values from the device arrays; ranges are clamped so that
 // disagreeing host/device lengths cannot send a read out of bounds.
+template <bool SHAPED>
 __device__ __forceinline__ Geometry geometry_of(const PrefillParams& p, const ua_tile& tile) {
   Geometry g;
   g.q_start = p.cu_query_lens[tile.seq];
@@ -171,7 +173,8 @@ __device__ __forceinline__ Geometry geometry_of(const PrefillParams& p, const ua
   g.kv_hi = min(min(tile.kv_hi, kv_len), p.max_blocks_per_seq * p.block_size);
   g.kv_lo = tile.kv_lo;
   g.prefix = p.shape.prefix_lens ? p.shape.prefix_lens[tile.seq] : 0;
-  const KeyGap gap = key_gap(p.shape.sinks, p.window, g.ctx + tile.row0 / p.qpk, kKeys);
+  KeyGap gap{0, 0};
+  if constexpr (SHAPED) gap = key_gap(p.shape.sinks, p.window, g.ctx + tile.row0 / p.qpk, kKeys);
   g.nsink = gap.lo / kKeys;
   g.skip = gap.hi - gap.lo;
   g.nmax = 0;
@@ -205,7 +208,7 @@ __device__ __forceinline__ void give_up(const PrefillParams& p, volatile int32_t
 // empty it publishes an end marker. The last CTA to finish (p.counters[1])
 // resets both counters for the next launch; a CTA that gives up still counts
 // itself, so the reset happens on the error path too.
-template <int D, bool F8>
+template <int D, bool F8, bool SHAPED>
 __device__ __forceinline__ void scheduler_role(const PrefillParams& p, const Bars<D, F8>& bar,
                                                uint8_t* ring, volatile int32_t* abort) {
   for (int k = 0;; ++k) {
@@ -223,7 +226,7 @@ __device__ __forceinline__ void scheduler_role(const PrefillParams& p, const Bar
       it.seq = tile.seq;
       it.kv_head = tile.kv_head;
       it.row0 = tile.row0;
-      it.g = geometry_of(p, tile);
+      it.g = geometry_of<SHAPED>(p, tile);
     }
     *reinterpret_cast<Item*>(ring + s * kItemBytes) = it;
     mbar_arrive(bar.item_full(s));  // release: the descriptor is visible to its readers
@@ -254,7 +257,7 @@ __device__ __forceinline__ bool take_item(const PrefillParams& p, const Bars<D, 
 // previous work tile has read it). Warp 2 (kIsV): the V ring. The first lane
 // loads Q; every lane looks up and copies its part of a key tile (tile_pages.cuh).
 // Ring positions run on across the CTA's work tiles.
-template <int D, bool F8, bool kIsV>
+template <int D, bool F8, bool SHAPED, bool kIsV>
 __device__ __forceinline__ void producer_role(const CUtensorMap* map_q, const CUtensorMap* map_kv,
                                               const PrefillParams& p, const uint8_t* ring,
                                               uint8_t* sQ, uint8_t* sRing, uint32_t full,
@@ -306,7 +309,7 @@ __device__ __forceinline__ void producer_role(const CUtensorMap* map_q, const CU
       if (tile.end) break;
       const Geometry& g = tile.g;
       if (g.nmax <= 0) continue;
-      TilePages<kKeys, kPanels> pages;
+      TilePages<kKeys, kPanels, SHAPED> pages;
       if (!kIsV) ok = all(lane != 0 || load_q(tile, g, 0));
       for (int j = 0; ok && j < g.nmax; ++j, ++step) {
         const int s = step % kStages;
@@ -318,7 +321,7 @@ __device__ __forceinline__ void producer_role(const CUtensorMap* map_q, const CU
         }
         if (lane == 0) mbar_arrive_expect_tx(full + 8u * s, L::kTile);
         __syncwarp();
-        pages.fetch(p, lane, tile.seq, g.ctx, g.key_of(j), g.kv_hi);
+        pages.fetch(p, lane, tile.seq, g.ctx, g.template key_of<SHAPED>(j), g.kv_hi);
         pages.copy(map_kv, p, lane, tile.kv_head, sRing + s * L::kTile, L::kPanel, L::kPanelDims,
                    full + 8u * s);
         last_phase[s] = step / kStages;
@@ -782,6 +785,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                    const __grid_constant__ CUtensorMap map_k,
                    const __grid_constant__ CUtensorMap map_v, const PrefillParams p) {
   using L = Smem<D, F8>;
+  constexpr bool kShaped = SHAPE != kShapePlain;
   constexpr int KS = L::kKStages, VS = L::kVStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>(
@@ -840,15 +844,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(
         SHAPE == kShapePlain ? kCtrlRegs : kShapedCtrlRegs));
     if (warp == 0) {
-      producer_role<D, F8, false>(&map_q, &map_k, p, ring, sQ, sK, bar.kfull(0), bar.kempty(0), bar,
-                                  lane, abort, never);
+      producer_role<D, F8, kShaped, false>(&map_q, &map_k, p, ring, sQ, sK, bar.kfull(0),
+                                           bar.kempty(0), bar, lane, abort, never);
     } else if (warp == 2) {
-      producer_role<D, F8, true>(&map_q, &map_v, p, ring, sQ, sV, bar.vfull(0), bar.vempty(0), bar,
-                                 lane, abort, never);
+      producer_role<D, F8, kShaped, true>(&map_q, &map_v, p, ring, sQ, sV, bar.vfull(0),
+                                          bar.vempty(0), bar, lane, abort, never);
     } else if (warp == 1 && lane == 0) {
       mma_role<D, F8>(p, ring, sQ, sK, sV, tmem, bar, abort, never);
     } else if (warp == 3 && lane == 0) {
-      scheduler_role<D, F8>(p, bar, ring, abort);
+      scheduler_role<D, F8, kShaped>(p, bar, ring, abort);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(

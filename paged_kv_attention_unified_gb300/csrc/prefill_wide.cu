@@ -104,12 +104,13 @@ struct Item {
   int seq, kv_head, row0, rows;  // packed rows [row0, row0 + rows) of the KV head
   int q_start, ctx, kv_lo, kv_hi;
   int ntiles;                    // key tiles of 64 from kv_lo
-  int nsink, skip;               // key tiles before the keys that no row sees, and how many those are
   int end;                       // 1: no more items for this CTA
   int prefix;                    // keys below it are visible to every row (0: none)
+  int nsink, skip;               // key tiles before the keys that no row sees, and how many those are
   // First key of key tile j.
+  template <bool SHAPED>
   __device__ __forceinline__ int key_of(int j) const {
-    return kv_lo + j * kKeys + (j >= nsink ? skip : 0);
+    return kv_lo + j * kKeys + (SHAPED && j >= nsink ? skip : 0);
   }
 };
 static_assert(sizeof(Item) <= kItemBytes, "item descriptor too large");
@@ -132,6 +133,7 @@ __device__ __forceinline__ bool take_item(const PrefillParams& p, const Bars& ba
 // One thread of warp 3: claims the next work tile of the plan (one query tile)
 // from the shared queue and publishes it once every role has taken the
 // previous one. The key range ends at the last visible key of its last row.
+template <bool SHAPED>
 __device__ __forceinline__ void scheduler_role(const PrefillParams& p, const Bars& bar,
                                                uint8_t* slot, volatile int32_t* abort) {
   int k = 0;
@@ -170,9 +172,11 @@ __device__ __forceinline__ void scheduler_role(const PrefillParams& p, const Bar
     const int last = it.row0 + it.rows - 1;
     it.prefix = p.shape.prefix_lens ? p.shape.prefix_lens[tile.seq] : 0;
     const int hi = p.causal ? min(kv_hi, max(it.ctx + last / p.qpk + 1, it.prefix)) : kv_hi;
-    const KeyGap gap = key_gap(p.shape.sinks, p.window, it.ctx + it.row0 / p.qpk, kKeys);
-    it.nsink = gap.lo / kKeys;
-    it.skip = gap.hi - gap.lo;
+    if constexpr (SHAPED) {
+      const KeyGap gap = key_gap(p.shape.sinks, p.window, it.ctx + it.row0 / p.qpk, kKeys);
+      it.nsink = gap.lo / kKeys;
+      it.skip = gap.hi - gap.lo;
+    }
     it.ntiles = hi > it.kv_lo + it.skip ? (hi - it.kv_lo - it.skip + kKeys - 1) / kKeys : 0;
     if (it.ntiles > 0) ok = publish(it);
   }
@@ -188,7 +192,7 @@ __device__ __forceinline__ void scheduler_role(const PrefillParams& p, const Bar
 // Warp 0 (Q and the K ring) or warp 2 (kIsV: the V ring): the first lane loads Q,
 // every lane looks up and copies its part of a key tile (tile_pages.cuh).
 // Ring positions run on across items.
-template <int D, bool kIsV>
+template <int D, bool SHAPED, bool kIsV>
 __device__ __forceinline__ void producer_role(const CUtensorMap* map_q, const CUtensorMap* map_kv,
                                               const PrefillParams& p, const uint8_t* slot,
                                               uint8_t* sQ, uint8_t* sRing, const Bars& bar, int lane,
@@ -221,7 +225,7 @@ __device__ __forceinline__ void producer_role(const CUtensorMap* map_q, const CU
       __syncwarp();
       if (lane == 0) mbar_arrive(bar.item_empty());
       if (it.end) break;
-      TilePages<kKeys, kPanels> pages;
+      TilePages<kKeys, kPanels, SHAPED> pages;
       if (!kIsV) {
         // Q of this item, once the last S MMA of the previous item has read Q
         bool free = true;
@@ -253,7 +257,7 @@ __device__ __forceinline__ void producer_role(const CUtensorMap* map_q, const CU
         }
         if (lane == 0) mbar_arrive_expect_tx(full, kStage);
         __syncwarp();
-        pages.fetch(p, lane, it.seq, it.ctx, it.key_of(j), it.kv_hi);
+        pages.fetch(p, lane, it.seq, it.ctx, it.template key_of<SHAPED>(j), it.kv_hi);
         pages.copy(map_kv, p, lane, it.kv_head, sRing + s * kStage, kPanelKV, 64, full);
         last_phase[s] = step / kStages;
       }
@@ -395,7 +399,7 @@ __device__ __forceinline__ bool softmax_item(const PrefillParams& p, const Item&
     if (!__all_sync(0xffffffffu, mbar_wait(bar.s_full(g % 2), (g / 2) & 1, abort, p.timeout_ns)))
       return false;
     tc_fence_after();
-    const int base = it.kv_lo + j * kKeys + (kShaped && j >= it.nsink ? it.skip : 0);
+    const int base = it.template key_of<kShaped>(j);
     const int hi_col = min(it.kv_hi, p.causal ? last_key + 1 : it.kv_hi) - base;
     const int lo_col = p.window > 0 ? pos - p.window + 1 - base : INT_MIN;
     uint32_t pk[kKeys / 2];
@@ -566,6 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const __grid_constant__ CUtensorMap map_k,
                         const __grid_constant__ CUtensorMap map_v, const PrefillParams p) {
   using G = Geo<D>;
+  constexpr bool kShaped = SHAPE != kShapePlain;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -616,13 +621,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
 
   if (warp == 0) {
-    producer_role<D, false>(&map_q, &map_k, p, slot, sQ, sK, bar, lane, abort, never);
+    producer_role<D, kShaped, false>(&map_q, &map_k, p, slot, sQ, sK, bar, lane, abort, never);
   } else if (warp == 1) {
     if (lane == 0) mma_role<D>(p, slot, sQ, sK, sV, tmem, bar, abort, never);
   } else if (warp == 2) {
-    producer_role<D, true>(&map_q, &map_v, p, slot, sQ, sV, bar, lane, abort, never);
+    producer_role<D, kShaped, true>(&map_q, &map_v, p, slot, sQ, sV, bar, lane, abort, never);
   } else if (warp == 3) {
-    if (lane == 0) scheduler_role(p, bar, slot, abort);
+    if (lane == 0) scheduler_role<kShaped>(p, bar, slot, abort);
   } else {
     softmax_role<D, SHAPE>(p, slot, sV, tmem, bar, abort, warp, lane);
   }

@@ -17,7 +17,10 @@ namespace ua {
 // 128 with a window of 1024 405 / 281. A tile ahead of the copies the same lookups
 // cost where they save nothing: 32 KV heads in 128-slot pages 515 / 497 us, ahead
 // 589 (the CTAs of a head drift apart and find less of its keys in L2).
-template <int KEYS, int PANELS>
+// SHAPED: there may be sinks. (The instances without them do no arithmetic of the gap,
+// here and in the kernels: it cost head_dim 192 2 %, 911 / 927 us for 4 x 4096 tokens
+// and 32 KV heads in 128-slot pages, and 256 1.4 %, 1029 / 1041.)
+template <int KEYS, int PANELS, bool SHAPED>
 struct TilePages {
   static_assert(KEYS / 16 * PANELS <= 32, "a copy to a lane");
   int32_t id;   // the page, as the block table has it
@@ -29,11 +32,13 @@ struct TilePages {
   __device__ __forceinline__ void fetch(const PrefillParams& p, int lane, int seq, int ctx,
                                         int base, int kv_hi) {
     const int key = base + box(lane) * p.rows_per_box;
-    // Boxes whose keys lie between the sinks and the first query's window are not
-    // looked up: a session may have given such pages back.
-    const KeyGap unseen = key_gap(p.shape.sinks, p.window, ctx, 1);
-    wanted = box(lane) * p.rows_per_box < KEYS && key < kv_hi &&
-             !(key >= unseen.lo && key + p.rows_per_box <= unseen.hi);
+    wanted = box(lane) * p.rows_per_box < KEYS && key < kv_hi;
+    if constexpr (SHAPED) {
+      // Boxes whose keys lie between the sinks and the first query's window are not
+      // looked up: a session may have given such pages back.
+      const KeyGap unseen = key_gap(p.shape.sinks, p.window, ctx, 1);
+      wanted = wanted && !(key >= unseen.lo && key + p.rows_per_box <= unseen.hi);
+    }
     id = -1;
     slot = 0;
     if (wanted) {
