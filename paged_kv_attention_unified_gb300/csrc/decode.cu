@@ -806,7 +806,11 @@ __global__ void __launch_bounds__(kThreads, Ring<D, FP8>::kCtasPerSm)
   // (a step is computed at most a ring after it was issued). The copy at a refill
   // waits for loads that are a chunk old; the new ones are waited for by the first
   // step that needs them.
-  int32_t ids = -1, slots = 0;  // (slots: of the step in its page, looked up with it)
+  // A step's slot in its page is looked up with the page where a step's place costs the
+  // arithmetic of a gap too (8 x 131072 keys, e4m3, 64 and 8 heads, capped: 375 us, 391
+  // with both at the copies, 386 without a gap), or scales come with the page anyway.
+  constexpr bool kSlotWithPage = SCALED || SHAPED;
+  int32_t ids = -1, slots = 0;
   StepScale of_issue{1.f, 1.f}, of_before{1.f, 1.f};
   int issue_chunk = 0;
   auto refill_ids = [&](int c) {
@@ -814,8 +818,8 @@ __global__ void __launch_bounds__(kThreads, Ring<D, FP8>::kCtasPerSm)
     ids = k < my_n ? p.block_tables[static_cast<int64_t>(tile.seq) * p.max_blocks_per_seq +
                                     step_base(k) / p.block_size]
                    : -1;
+    if constexpr (kSlotWithPage) slots = step_base(k) % p.block_size;
     if constexpr (SCALED) {
-      slots = step_base(k) % p.block_size;
       of_before = of_issue;
       issue_chunk = c;
       of_issue = StepScale{1.f, 1.f};
@@ -837,10 +841,10 @@ __global__ void __launch_bounds__(kThreads, Ring<D, FP8>::kCtasPerSm)
   // Whole-warp call: every lane takes part in the shuffle, lane 0 issues.
   auto issue = [&](int k) {
     const int32_t id = __shfl_sync(0xffffffffu, ids, k & 31);
-    int32_t slot = 0;
-    if constexpr (SCALED) slot = __shfl_sync(0xffffffffu, slots, k & 31);
+    [[maybe_unused]] int32_t slot = 0;
+    if constexpr (kSlotWithPage) slot = __shfl_sync(0xffffffffu, slots, k & 31);
     if (lane == 0) {
-      if constexpr (!SCALED) slot = step_base(k) % p.block_size;
+      const int base = step_base(k);
       int32_t blk = static_cast<int32_t>(p.num_blocks);  // out of range: TMA fills zeros
       if (id >= 0 && static_cast<int64_t>(id) < p.num_blocks) blk = id;
       else record_error(p.err, UA_ERR_BOUNDS);
@@ -852,9 +856,9 @@ __global__ void __launch_bounds__(kThreads, Ring<D, FP8>::kCtasPerSm)
 #pragma unroll
       for (int pn = 0; pn < PL::kPanels; ++pn) {
         sm100::tma_load_4d(stage + pn * PL::kPanelBytes, &map_k, &wbar[st], pn * PL::kBoxDims,
-                           tile.kv_head, slot, blk);
+                           tile.kv_head, kSlotWithPage ? slot : base % p.block_size, blk);
         sm100::tma_load_4d(stage + 16 * RC::kRowBytes + pn * PL::kPanelBytes, &map_v, &wbar[st],
-                           pn * PL::kBoxDims, tile.kv_head, slot, blk);
+                           pn * PL::kBoxDims, tile.kv_head, kSlotWithPage ? slot : base % p.block_size, blk);
       }
     }
   };
