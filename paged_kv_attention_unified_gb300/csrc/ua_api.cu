@@ -1064,6 +1064,7 @@ ua_status ua_forward(const ua_plan* plan, const void* q, const void* k_cache,
       sp.block_size = plan->prob.block_size;
       sp.num_blocks = num_blocks;
       sp.row_elems = plan->prob.num_kv_heads * plan->prob.head_dim;
+      sp.gaps = plan->prob.sinks > 0 ? 1 : 0;
       sp.err = plan->d_err;
       sp.k_scales = kp.k_scales;
       sp.v_scales = kp.v_scales;

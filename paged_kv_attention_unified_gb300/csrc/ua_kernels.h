@@ -229,6 +229,7 @@ struct StageParams {
   int32_t block_size;
   int64_t num_blocks;
   int32_t row_elems;             // Hkv * d, a multiple of 8
+  int32_t gaps;                  // whether tiles may hold keys that no query sees
   int32_t* err;                  // error word (UA_ERR_BOUNDS)
   // Block scales [num_blocks][Hkv], or null; 16-code chunks of a head.
   const float* k_scales;
