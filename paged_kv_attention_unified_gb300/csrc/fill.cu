@@ -78,7 +78,7 @@ constexpr Layout layout_of(Turn t) {
 }
 
 // The block-th CTA of the cache's part.
-template <Turn TURN>
+template <Turn TURN, bool AXES>
 __device__ __forceinline__ void fill_block(const RopeTable& rope, const FillParams& p, int block) {
   extern __shared__ float2 turn[];  // [tokens of a round][pairs]
   __shared__ uint32_t copy[TURN == kTurnHalfOdd ? kWarps * 32 * kUnitWords : 1];
@@ -164,7 +164,7 @@ __device__ __forceinline__ void fill_block(const RopeTable& rope, const FillPara
         const int i = threadIdx.x & ((1 << wide) - 1);
         const int at = turn_at(i, pairs);
         if (i < pairs) {
-          const PairFrequency f(rope, p.positions, p.positions_stride, p.axes, i);
+          const PairFrequency<AXES> f(rope, p.positions, p.positions_stride, i);
           for (int t = threadIdx.x >> wide; t < tokens; t += kThreads >> wide) {
             const int tok = r * round_tokens + t;
             turn[t * turn_row(pairs) + at] = f.at(tile.row0 + tok, tile.kv_lo + tok);
@@ -333,20 +333,20 @@ __device__ __forceinline__ void fill_block(const RopeTable& rope, const FillPara
   }
 }
 
-template <Turn TURN>
+template <Turn TURN, bool AXES>
 __global__ void __launch_bounds__(kThreads, 4)
     fill_kernel(const __grid_constant__ RopeTable rope, const FillParams p, const RopeAppendParams q,
                 int fill_blocks) {
   const int block = blockIdx.x;
   if (block < fill_blocks) {
-    fill_block<TURN>(rope, p, block);
+    fill_block<TURN, AXES>(rope, p, block);
   } else if constexpr (TURN != kTurnNone) {
     const RopeScale one{1.f, 1.f, 1.f};  // (no cache rows here)
-    rope_append_block<false, layout_of(TURN)>(rope, q, one, one, block - fill_blocks);
+    rope_append_block<false, layout_of(TURN), AXES>(rope, q, one, one, block - fill_blocks);
   }
 }
 
-template <Turn TURN>
+template <Turn TURN, bool AXES = false>
 cudaError_t launch(const RopeTable& rope, const FillParams& p, const RopeAppendParams& q, int smem,
                    cudaStream_t stream) {
   const int groups = (p.num_kv_heads + p.heads_per_cta - 1) / p.heads_per_cta;
@@ -354,9 +354,9 @@ cudaError_t launch(const RopeTable& rope, const FillParams& p, const RopeAppendP
   const int64_t blocks = fill_blocks + (TURN == kTurnNone ? 0 : int64_t{kParts} * q.num_tiles);
   if (blocks > INT32_MAX) return cudaErrorInvalidValue;
   static std::atomic<uint64_t> smem_set{0};
-  const cudaError_t e = set_smem_once(fill_kernel<TURN>, kMostSmem, smem_set);
+  const cudaError_t e = set_smem_once(fill_kernel<TURN, AXES>, kMostSmem, smem_set);
   if (e != cudaSuccess) return e;
-  fill_kernel<TURN><<<static_cast<unsigned>(blocks), kThreads, smem, stream>>>(
+  fill_kernel<TURN, AXES><<<static_cast<unsigned>(blocks), kThreads, smem, stream>>>(
       rope, p, q, static_cast<int>(fill_blocks));
   return cudaGetLastError();
 }
@@ -381,9 +381,15 @@ cudaError_t launch_fill(const RopeTable* rope, FillParams p, RopeAppendParams q,
   const int smem = tokens * turn_row(p.rotary_dim / 2) * static_cast<int>(sizeof(float2));
   if (smem > kMostSmem) return cudaErrorInvalidValue;
   q.num_kv_heads = 0;
-  if (p.interleaved) return launch<kTurnInterleaved>(*rope, p, q, smem, stream);
-  return p.rotary_dim % 16 == 0 ? launch<kTurnHalf>(*rope, p, q, smem, stream)
-                                : launch<kTurnHalfOdd>(*rope, p, q, smem, stream);
+  const bool axes = p.positions != nullptr && p.axes > 1;
+  if (p.interleaved)
+    return axes ? launch<kTurnInterleaved, true>(*rope, p, q, smem, stream)
+                : launch<kTurnInterleaved>(*rope, p, q, smem, stream);
+  if (p.rotary_dim % 16 == 0)
+    return axes ? launch<kTurnHalf, true>(*rope, p, q, smem, stream)
+                : launch<kTurnHalf>(*rope, p, q, smem, stream);
+  return axes ? launch<kTurnHalfOdd, true>(*rope, p, q, smem, stream)
+              : launch<kTurnHalfOdd>(*rope, p, q, smem, stream);
 }
 
 }  // namespace ua

@@ -52,11 +52,11 @@ namespace {
 
 using namespace rope_device;
 
-template <bool FP8, Layout LAYOUT>
+template <bool FP8, Layout LAYOUT, bool AXES>
 __global__ void __launch_bounds__(kThreads)
     rope_append_kernel(const __grid_constant__ RopeTable rope, const RopeAppendParams p,
                        const RopeScale k_scale, const RopeScale v_scale) {
-  rope_append_block<FP8, LAYOUT>(rope, p, k_scale, v_scale, blockIdx.x);
+  rope_append_block<FP8, LAYOUT, AXES>(rope, p, k_scale, v_scale, blockIdx.x);
 }
 
 RopeScale split_scale(float scale) {
@@ -65,16 +65,16 @@ RopeScale split_scale(float scale) {
   return {std::ldexp(1.f, 1 - e), mant, 1.f / mant};
 }
 
-template <bool FP8>
+template <bool FP8, bool AXES>
 cudaError_t launch(const RopeTable& rope, const RopeAppendParams& p, cudaStream_t stream) {
   const RopeScale ks = split_scale(p.k_scale), vs = split_scale(p.v_scale);
   const int grid = p.num_tiles * kParts;
   if (p.interleaved)
-    rope_append_kernel<FP8, kInterleaved><<<grid, kThreads, 0, stream>>>(rope, p, ks, vs);
+    rope_append_kernel<FP8, kInterleaved, AXES><<<grid, kThreads, 0, stream>>>(rope, p, ks, vs);
   else if (p.rotary_dim % 16 == 0)
-    rope_append_kernel<FP8, kHalf><<<grid, kThreads, 0, stream>>>(rope, p, ks, vs);
+    rope_append_kernel<FP8, kHalf, AXES><<<grid, kThreads, 0, stream>>>(rope, p, ks, vs);
   else
-    rope_append_kernel<FP8, kHalfOdd><<<grid, kThreads, 0, stream>>>(rope, p, ks, vs);
+    rope_append_kernel<FP8, kHalfOdd, AXES><<<grid, kThreads, 0, stream>>>(rope, p, ks, vs);
   return cudaGetLastError();
 }
 
@@ -86,7 +86,9 @@ cudaError_t launch_rope_append(const RopeTable& rope, const RopeAppendParams& p,
   if (p.tiles == nullptr || p.rotary_dim > 2 * kMaxPairs || p.rotary_dim > p.head_dim ||
       p.head_dim % 32 != 0)
     return cudaErrorInvalidValue;
-  return p.fp8 ? launch<true>(rope, p, stream) : launch<false>(rope, p, stream);
+  if (p.positions != nullptr && p.axes > 1)
+    return p.fp8 ? launch<true, true>(rope, p, stream) : launch<false, true>(rope, p, stream);
+  return p.fp8 ? launch<true, false>(rope, p, stream) : launch<false, false>(rope, p, stream);
 }
 
 }  // namespace ua
