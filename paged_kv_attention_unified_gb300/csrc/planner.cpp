@@ -310,8 +310,10 @@ ua_status build_schedule(const Problem& p, Schedule* out) {
     shortest = std::min(shortest, b.keys());
   }
   int64_t chunk = 0;  // 0: do not split
-  const int64_t min_split = p.sinks > 0 && p.window > 0 ? kMinSplitTokensSinks : kMinSplitTokens;
   const int64_t slots = static_cast<int64_t>(num_sms) * decode_ctas_per_sm(p.head_dim, p.kv_dtype == UA_KV_BF16 ? 2 : 1);
+  const bool few_keys = p.sinks > 0 && p.window > 0 && longest >= kMinSplitSinksFrom &&
+                        longest <= kMinSplitSinksTo && total <= kMinSplitTokensSinks * slots;
+  const int64_t min_split = few_keys ? kMinSplitTokensSinks : kMinSplitTokens;
   if (p.num_splits == 0 && n_tiles > 0 && total > 0) {
     chunk = round_up(std::max<int64_t>(min_split, ceil_div(total, slots)), kKeyStep);
     chunk = std::max<int64_t>(chunk, round_up(ceil_div(longest, UA_MAX_SPLITS), kKeyStep));
@@ -329,7 +331,7 @@ ua_status build_schedule(const Problem& p, Schedule* out) {
   // half a wave leave a second wave of `late` whole tiles behind the first:
   // the step takes two tile times for little more than one tile time of work.
   // The `late` tiles that start last in the longest-first order below are cut
-  // into k = slots / late pieces (each of at least kMinSplitTokens keys), so
+  // into k = slots / late pieces (each of at least min_split keys), so
   // they fill the slots the first wave frees and end a fraction of a tile
   // after it.
   int64_t tail_k = 0;

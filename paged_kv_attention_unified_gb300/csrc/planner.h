@@ -146,10 +146,15 @@ constexpr int kPieceOverheadTokens = 128;
 constexpr int kDecodeSaturatingCtas = 256;
 // Smallest automatic split piece, in key tokens.
 constexpr int kMinSplitTokens = 256;
-// And with sinks, where a decode tile's keys are as few as the window for good (one
-// token, 8 KV heads, window 1024 and 4 sinks, in 4 / 8 / 16 / 32 pieces 15.4 / 14.3
-// / 14.3 / 16.4 us).
+// And with sinks, where a decode tile's keys stay as few as the window: half of it for
+// tiles that become at least three such pieces and at most 24, and all of them one
+// wave. 32 query and 8 KV heads of 128, one sequence, window (and 4 sinks) 256 / 496 /
+// 1024 / 2000 / 3000 / 4096 in a graph: pieces from 128 keys 8.1 / 7.4 / 9.0 / 11.4 /
+// 12.1 / 13.7 us, from 256 7.5 / 9.5 / 10.1 / 11.8 / 12.4 / 11.6; window 1024, 2 / 6 / 8
+// sequences 9.2 / 11.1 / 12.9 and 10.5 / 11.6 / 12.0; 64 KV heads 13.2 and 12.0. (More
+// pieces a tile cost its last one their merge, more CTAs than one wave another start.)
 constexpr int kMinSplitTokensSinks = 128;
+constexpr int kMinSplitSinksFrom = 384, kMinSplitSinksTo = 3072;
 // Default: sequences with q_len * qpk above this go to the prefill kernel
 // (when it can take the problem; otherwise every sequence is decode work).
 constexpr int kDefaultDecodeRowsMax = 32;

@@ -125,3 +125,13 @@ def test_refusals():
         ua.ua_schedule(*args, window=5, sink_tokens=4, causal=0, prefix_lens=[3])
     with pytest.raises(ValueError):
         ua.ua_schedule(*args, window=5, sink_tokens=4, prefix_lens=[3, 3])
+
+
+@pytest.mark.parametrize("n,window,hkv,pieces", [
+    (1, 256, 8, 1), (1, 496, 8, 4), (1, 1024, 8, 8), (1, 4096, 8, 16), (6, 1024, 8, 8), (8, 1024, 8, 4),
+    (1, 1024, 64, 4), (100, 1024, 8, 1)])
+def test_small_pieces_only_where_they_are_few(n, window, hkv, pieces):
+    """The pieces of a tile: from 128 keys where they are few and fill one wave, else from 256."""
+    _, _, dec, _ = ua.ua_schedule(list(range(n + 1)), [30000] * n, 64, hkv, 128, 16, 1875, window=window, sink_tokens=4)
+    one = [t for t in dec if t["seq"] == 0 and t["kv_head"] == 0]
+    assert len(one) == pieces
