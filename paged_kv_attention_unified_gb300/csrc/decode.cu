@@ -239,7 +239,9 @@ struct StepScale {
 // follows the pages in steps of exact products. It stays within [2^-60, 2^22] and
 // at 2^-64 of the largest scale so far or above: then O, at most 2^8 a key times 448
 // of those, stays below 2^128 for 2^31 keys, and what the quietest page (2^-100)
-// adds beside the loudest (2^100) is a number of binary32.
+// adds beside the loudest (2^100) is a number of binary32. Pages of one step pair 2^12
+// apart all along, the slowest case (64 x 4096 keys, us): head_dim 64 74.0 -> 75.9, 128
+// 94.8 -> 94.9, 256 172.2 -> 173.5.
 struct ValueUnit {
   float inv = 0.f, top = 0.f;  // 1 / unit (0: nothing taken yet); the largest scale so far
   __device__ __forceinline__ static float power(float x) {  // 2^floor(log2 x)

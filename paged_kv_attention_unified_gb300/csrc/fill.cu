@@ -25,7 +25,9 @@
 // Bytes: 2 B read and 1 B written per new element of K and V, 4 B per element of q.
 // 4 x 4096 tokens, 32 heads and 8 of 128, 16-slot pages: 75 us, the queries' part
 // alone 42 (at the rate of HBM), the cache's 33 (15 at that rate: the angles' sines
-// and the chain of loads, maximum and stores of a CTA); without rotation 23. The two
+// and the chain of loads, maximum and stores of a CTA); without rotation 23. Rotary dims
+// that 16 does not divide: 100 of 128 rotated 112 us, 72 of 96 107 (71 with all 96; the
+// pairs' partners come through shared memory and 200 bytes a thread are spilled). The two
 // parts run one after the other: mixed CTA by CTA the same work takes 86 us, its two
 // bodies do not fit the instruction cache together.
 #include <cstdint>
