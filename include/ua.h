@@ -244,10 +244,11 @@ ua_status ua_schedule_prefix(const int32_t* cu_query_lens_host, const int32_t* k
  * sink_tokens).
  * sink_tokens: >= 0; without effect under window <= 0, where every key stays.
  * prefix_lens_host: as ua_plan_create_prefix, or NULL (no prefix; causal 0 or 1).
- * Keys that no query of a sequence sees -- from sink_tokens up to the first
- * query's window -- are not read, and a page that holds only such keys is not
- * looked up: its block-table entry may be anything (the page may have been given
- * back). Positions stay those in the cache: block tables keep an entry per
+ * A page that holds only keys that no query of a sequence sees -- from sink_tokens
+ * up to the first query's window -- is neither looked up nor read: its block-table
+ * entry may be anything (the page may have been given back). In other pages such
+ * keys may be read beside their neighbours, and count for nothing if they are
+ * finite, as every masked key below kv_len. Positions stay those in the cache: block tables keep an entry per
  * logical block. With sinks, sequences that are too long for the decode kernel
  * run in a prefill kernel at every head dim (see ua_plan_set_scores). In the
  * tile lists a range [kv_lo, kv_hi) holds the keys that its rows pass over.
