@@ -311,8 +311,10 @@ ua_status build_schedule(const Problem& p, Schedule* out) {
   }
   int64_t chunk = 0;  // 0: do not split
   const int64_t slots = static_cast<int64_t>(num_sms) * decode_ctas_per_sm(p.head_dim, p.kv_dtype == UA_KV_BF16 ? 2 : 1);
-  const bool few_keys = p.sinks > 0 && p.window > 0 && longest >= kMinSplitSinksFrom &&
-                        longest <= kMinSplitSinksTo && total <= kMinSplitTokensSinks * slots;
+  const bool few_keys = p.sinks > 0 && p.window > 0 &&
+                        longest >= kFewestSinkPieces * kMinSplitTokensSinks &&
+                        longest <= kMostSinkPieces * kMinSplitTokensSinks &&
+                        total <= kMinSplitTokensSinks * slots;
   const int64_t min_split = few_keys ? kMinSplitTokensSinks : kMinSplitTokens;
   if (p.num_splits == 0 && n_tiles > 0 && total > 0) {
     chunk = round_up(std::max<int64_t>(min_split, ceil_div(total, slots)), kKeyStep);

@@ -154,7 +154,7 @@ constexpr int kMinSplitTokens = 256;
 // sequences 9.2 / 11.1 / 12.9 and 10.5 / 11.6 / 12.0; 64 KV heads 13.2 and 12.0. (More
 // pieces a tile cost its last one their merge, more CTAs than one wave another start.)
 constexpr int kMinSplitTokensSinks = 128;
-constexpr int kMinSplitSinksFrom = 384, kMinSplitSinksTo = 3072;
+constexpr int kFewestSinkPieces = 3, kMostSinkPieces = 24;
 // Default: sequences with q_len * qpk above this go to the prefill kernel
 // (when it can take the problem; otherwise every sequence is decode work).
 constexpr int kDefaultDecodeRowsMax = 32;
