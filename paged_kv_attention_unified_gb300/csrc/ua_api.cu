@@ -1558,7 +1558,7 @@ ua_status ua_last_device_error(ua_plan* plan, int32_t* code) {
 ua_status ua_gather_kv_debug(const ua_plan* plan, const void* k_cache, const void* v_cache,
                              const int32_t* kv_lens, const int32_t* block_tables,
                              int64_t num_blocks, void* k_out, void* v_out, int64_t rows_cap,
-                             ua_stream_t stream) {
+                             ua_stream_t stream) try {
   if (plan == nullptr || !k_cache || !v_cache || !kv_lens || !block_tables || !k_out || !v_out)
     return UA_ERR_INVALID_ARG;
   if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_out) || !aligned16(v_out) ||
@@ -1604,6 +1604,8 @@ ua_status ua_gather_kv_debug(const ua_plan* plan, const void* k_cache, const voi
   if (cudaStreamSynchronize(cs) != cudaSuccess && st == UA_OK) st = UA_ERR_CUDA;
   cudaFree(d_offs);
   return st;
+} catch (const std::bad_alloc&) {
+  return UA_ERR_INVALID_ARG;
 }
 
 ua_status ua_plan_set_profiling(ua_plan* plan, int32_t enable) {
